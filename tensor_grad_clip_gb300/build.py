@@ -2,8 +2,8 @@
 
     python -m tensor_grad_clip_gb300.build [--force]
 
-The translation units (kernels.cu, soma_opt.cpp, noalloc.cu) compile in parallel and link
-into tensor_grad_clip_gb300/_build/libsoma_opt.so with the CUDA runtime linked
+The translation units (SOURCES) compile in parallel and link into
+tensor_grad_clip_gb300/_build/libsoma_opt.so with the CUDA runtime linked
 statically, so the library needs nothing but the driver at load time.
 """
 from __future__ import annotations
@@ -20,8 +20,9 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libsoma_opt.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-SOURCES = ["kernels.cu", "soma_opt.cpp", "noalloc.cu"]
-HEADERS = ["soma_kernels.h"]
+SOURCES = ["kernels.cu", "soma_opt.cpp", "noalloc.cu", "ops.cpp", "layer_norm.cu", "linear.cu", "distill.cu"]
+HEADERS = ["soma_kernels.h", "ops_kernels.h", "ops_device.cuh"]
+PUBLIC_HEADERS = ["soma_opt.h", "soma_ops.h"]
 
 
 def nvcc() -> str:
@@ -34,7 +35,7 @@ def nvcc() -> str:
 
 def _inputs():
     files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS]
-    files.append(os.path.join(INCLUDE, "soma_opt.h"))
+    files += [os.path.join(INCLUDE, h) for h in PUBLIC_HEADERS]
     return files
 
 
