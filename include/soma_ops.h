@@ -109,6 +109,12 @@ soma_status_t soma_linear_backward(int32_t device, const void *dy, int64_t dy_st
                                    int64_t m, int64_t n, int64_t k, int32_t dtype, int32_t activation,
                                    void *stream);
 
+/* Every wait inside the matrix products is bounded (about a second; a step of
+ * their pipeline takes microseconds).  Waits for `device` and returns
+ * SOMA_ERR_STATE if one ran out since the last check, which leaves that
+ * call's outputs invalid: a fault of the library, not of its arguments. */
+soma_status_t soma_linear_check(int32_t device);
+
 /* ---- distillation from a teacher's top logits -------------------------------
  * A teacher answers each row with `top` of its logits and their places in
  * the vocabulary.  With temperature T > 0,

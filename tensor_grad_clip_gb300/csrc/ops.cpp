@@ -100,6 +100,28 @@ soma_status_t check_workspace(const void* workspace, int64_t have, int64_t need)
     return SOMA_OK;
 }
 
+// A 16-bit operand of a matrix product: where it is, or the part of the
+// workspace that a copy with aligned rows takes.
+struct Operand {
+    const void* p;
+    int64_t stride, rows, cols;
+    bool copy;
+    Operand(const void* q, int64_t s, int64_t r, int64_t c)
+        : p(q), stride(s), rows(r), cols(c), copy(soma::gemm_operand_needs_copy(q, s, r)) {}
+    int64_t bytes() const { return copy ? align256(rows * ((cols + 7) / 8 * 8) * 2) : 0; }
+    // Enqueues the copy, if any, and advances the workspace past it.
+    int place(char*& workspace, void* stream) {
+        if (!copy) return cudaSuccess;
+        const int64_t to = (cols + 7) / 8 * 8;
+        const int e = soma::launch_repack(p, stride, workspace, to, rows, cols, stream);
+        p = workspace;
+        stride = to;
+        workspace += align256(rows * to * 2);
+        copy = false;
+        return e;
+    }
+};
+
 #define SOMA_TRY(x)                              \
     do {                                         \
         const soma_status_t st_ = (x);           \
@@ -130,6 +152,15 @@ soma_status_t check_linear(int64_t m, int64_t n, int64_t k, int32_t dtype, int32
         return fail(SOMA_ERR_DTYPE, "dtype = %d: the linear layer takes bf16 or fp16", (int)dtype);
     if (act < SOMA_ACT_NONE || act > SOMA_ACT_SILU) return fail(SOMA_ERR_INVALID_ARG, "activation = %d", (int)act);
     return SOMA_OK;
+}
+
+// Workspace of the backward pass: the bias gradient's partial sums, dz (with
+// an activation, or where dy's rows are not aligned), and copies of x and
+// weight where theirs are not.
+int64_t backward_bytes(const Operand& dy, const Operand& x, const Operand& weight, int32_t act, int sms) {
+    const bool dz = act != SOMA_ACT_NONE || dy.copy;
+    return align256(soma::act_bwd_workspace(dy.rows, dy.cols, sms)) +
+           (dz ? align256(dy.rows * ((dy.cols + 7) / 8 * 8) * 2) : 0) + x.bytes() + weight.bytes();
 }
 
 soma_status_t check_distill(const soma::DistillArgs& a, int64_t vocab, int64_t top, double temperature) {
@@ -239,10 +270,10 @@ soma_status_t soma_layer_norm_backward(int32_t device, const void* dy, int64_t d
 soma_status_t soma_linear_forward_workspace(int32_t device, const void* x, int64_t x_stride, const void* weight,
                                             int64_t weight_stride, int64_t m, int64_t n, int64_t k, int32_t dtype,
                                             int64_t* bytes) {
-    (void)device; (void)x; (void)x_stride; (void)weight; (void)weight_stride;
+    (void)device;
     if (!bytes) return fail(SOMA_ERR_INVALID_ARG, "bytes is NULL");
     SOMA_TRY(check_linear(m, n, k, dtype, SOMA_ACT_NONE));
-    *bytes = 0;
+    *bytes = m == 0 || n == 0 ? 0 : Operand(x, x_stride, m, k).bytes() + Operand(weight, weight_stride, n, k).bytes();
     return SOMA_OK;
 }
 
@@ -251,7 +282,6 @@ soma_status_t soma_linear_forward(int32_t device, const void* x, int64_t x_strid
                                   int64_t residual_stride, void* y, int64_t y_stride, void* z_out, int64_t z_stride,
                                   void* workspace, int64_t workspace_bytes, int64_t m, int64_t n, int64_t k,
                                   int32_t dtype, int32_t activation, void* stream) {
-    (void)workspace; (void)workspace_bytes;
     SOMA_TRY(check_linear(m, n, k, dtype, activation));
     SOMA_TRY(check_matrix("x", x, x_stride, m, k, 2));
     SOMA_TRY(check_matrix("weight", weight, weight_stride, n, k, 2));
@@ -260,22 +290,29 @@ soma_status_t soma_linear_forward(int32_t device, const void* x, int64_t x_strid
     SOMA_TRY(check_matrix("y", y, y_stride, m, n, 2));
     SOMA_TRY(check_matrix("z_out", z_out, z_stride, m, n, 2, true));
     if (m == 0 || n == 0) return SOMA_OK;
+    Operand a(x, x_stride, m, k), b(weight, weight_stride, n, k);
+    SOMA_TRY(check_workspace(workspace, workspace_bytes, a.bytes() + b.bytes()));
     SOMA_ON_DEVICE(device);
-    soma::GemmArgs g{x, x_stride, true, weight, weight_stride, true, bias, residual, residual_stride, y, y_stride,
-                     z_out, z_stride, (int32_t)m, (int32_t)n, (int32_t)k, dtype, activation};
-    return cuda_status(soma::launch_gemm(g, sms, stream), "linear");
+    char* ws = static_cast<char*>(workspace);
+    int e = a.place(ws, stream);
+    if (e == cudaSuccess) e = b.place(ws, stream);
+    if (e == cudaSuccess)
+        e = soma::launch_gemm({a.p, a.stride, true, b.p, b.stride, true, bias, residual, residual_stride, y, y_stride,
+                               z_out, z_stride, (int32_t)m, (int32_t)n, (int32_t)k, dtype, activation},
+                              sms, stream);
+    return cuda_status(e, "linear");
 }
 
 soma_status_t soma_linear_backward_workspace(int32_t device, const void* dy, int64_t dy_stride, const void* x,
                                              int64_t x_stride, const void* weight, int64_t weight_stride, int64_t m,
                                              int64_t n, int64_t k, int32_t dtype, int32_t activation,
                                              int64_t* bytes) {
-    (void)dy; (void)dy_stride; (void)x; (void)x_stride; (void)weight; (void)weight_stride;
     if (!bytes) return fail(SOMA_ERR_INVALID_ARG, "bytes is NULL");
     SOMA_TRY(check_linear(m, n, k, dtype, activation));
     const int sms = sm_count(device);
     if (sms <= 0) return fail(SOMA_ERR_CUDA, "no SM count for device %d", (int)device);
-    *bytes = align256(soma::act_bwd_workspace(m, n, sms)) + (activation != SOMA_ACT_NONE ? m * n * 2 : 0);
+    *bytes = m == 0 || n == 0 ? 0 : backward_bytes(Operand(dy, dy_stride, m, n), Operand(x, x_stride, m, k),
+                                                   Operand(weight, weight_stride, n, k), activation, sms);
     return SOMA_OK;
 }
 
@@ -306,32 +343,42 @@ soma_status_t soma_linear_backward(int32_t device, const void* dy, int64_t dy_st
         if (dbias && e == cudaSuccess) e = cudaMemsetAsync(dbias, 0, (size_t)n * 2, st);
         return cuda_status(e, "linear backward");
     }
-    const int64_t partial_bytes = align256(soma::act_bwd_workspace(m, n, sms));
-    const bool act = activation != SOMA_ACT_NONE;
-    SOMA_TRY(check_workspace(workspace, workspace_bytes, partial_bytes + (act ? m * n * 2 : 0)));
-    const void* dz = dy;
-    int64_t dz_stride = dy_stride;
-    if (act || dbias) {
-        char* ws = static_cast<char*>(workspace);
-        soma::ActBwdArgs b{dy, dy_stride, z, z_stride, act ? ws + partial_bytes : nullptr, n, dbias,
-                           reinterpret_cast<float*>(ws), m, (int32_t)n, dtype, activation};
-        e = soma::launch_act_bwd(b, sms, stream);
-        if (act) {
-            dz = b.dz;
-            dz_stride = n;
+    Operand g(dy, dy_stride, m, n), a(x, x_stride, m, k), b(weight, weight_stride, n, k);
+    SOMA_TRY(check_workspace(workspace, workspace_bytes, backward_bytes(g, a, b, activation, sms)));
+    char* ws = static_cast<char*>(workspace);
+    const bool products = dx || dweight;
+    const bool store = products && (activation != SOMA_ACT_NONE || g.copy);
+    if (store || dbias) {
+        const int64_t dz_stride = (n + 7) / 8 * 8;
+        char* dz = ws + align256(soma::act_bwd_workspace(m, n, sms));
+        e = soma::launch_act_bwd({dy, dy_stride, z, z_stride, store ? dz : nullptr, dz_stride, dbias,
+                                  reinterpret_cast<float*>(ws), m, (int32_t)n, dtype, activation},
+                                 sms, stream);
+        if (store) {
+            g = Operand(dz, dz_stride, m, n);
+            ws = dz + align256(m * dz_stride * 2);
         }
     }
-    if (dx && e == cudaSuccess) {
-        soma::GemmArgs g{dz, dz_stride, true, weight, weight_stride, false, nullptr, nullptr, 0, dx, dx_stride,
-                         nullptr, 0, (int32_t)m, (int32_t)k, (int32_t)n, dtype, SOMA_ACT_NONE};
-        e = soma::launch_gemm(g, sms, stream);
-    }
-    if (dweight && e == cudaSuccess) {
-        soma::GemmArgs g{dz, dz_stride, false, x, x_stride, false, nullptr, nullptr, 0, dweight, dweight_stride,
-                         nullptr, 0, (int32_t)n, (int32_t)k, (int32_t)m, dtype, SOMA_ACT_NONE};
-        e = soma::launch_gemm(g, sms, stream);
-    }
+    if (dx && e == cudaSuccess) e = b.place(ws, stream);
+    if (dx && e == cudaSuccess)
+        e = soma::launch_gemm({g.p, g.stride, true, b.p, b.stride, false, nullptr, nullptr, 0, dx, dx_stride, nullptr, 0,
+                               (int32_t)m, (int32_t)k, (int32_t)n, dtype, SOMA_ACT_NONE},
+                              sms, stream);
+    if (dweight && e == cudaSuccess) e = a.place(ws, stream);
+    if (dweight && e == cudaSuccess)
+        e = soma::launch_gemm({g.p, g.stride, false, a.p, a.stride, false, nullptr, nullptr, 0, dweight, dweight_stride,
+                               nullptr, 0, (int32_t)n, (int32_t)k, (int32_t)m, dtype, SOMA_ACT_NONE},
+                              sms, stream);
     return cuda_status(e, "linear backward");
+}
+
+soma_status_t soma_linear_check(int32_t device) {
+    SOMA_ON_DEVICE(device);
+    (void)sms;
+    int gave_up = 0;
+    SOMA_TRY(cuda_status(soma::take_gave_up(&gave_up), "linear check"));
+    if (gave_up) return fail(SOMA_ERR_STATE, "a matrix product gave up waiting for its own pipeline: its results are not valid");
+    return SOMA_OK;
 }
 
 // ---- distillation loss ----------------------------------------------------

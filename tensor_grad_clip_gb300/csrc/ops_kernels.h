@@ -68,6 +68,16 @@ struct GemmArgs {
 
 int launch_gemm(const GemmArgs& a, int sm_count, void* stream);
 
+// launch_gemm reads operands by TMA: rows that do not start on 16-byte
+// boundaries (needs_copy) are first copied into rows that do.
+bool gemm_operand_needs_copy(const void* p, int64_t stride, int64_t rows);
+int launch_repack(const void* src, int64_t src_stride, void* dst, int64_t dst_stride, int64_t rows, int64_t cols,
+                  void* stream);
+
+// Whether a bounded wait of a matrix product on the current device ran out
+// since the last call (waits for the device).
+int take_gave_up(int* value);
+
 // dz = dy * act'(z) (dz == nullptr: not stored), and dbias = column sums of
 // the unrounded dz (dbias == nullptr: not wanted).
 struct ActBwdArgs {
