@@ -43,6 +43,13 @@ extern "C" {
  * none).  Valid until the thread's next call. */
 const char *soma_ops_last_error(void);
 
+/* Kernels that wait for their own asynchronous copies bound that wait (about
+ * a second; a step of their pipelines takes microseconds).  This call waits
+ * for `device` and returns SOMA_ERR_STATE if such a wait ran out since the
+ * last check, which leaves that call's outputs invalid: a fault of the
+ * library, not of its arguments. */
+soma_status_t soma_ops_check(int32_t device);
+
 /* ---- layer norm -------------------------------------------------------------
  * Over each row of x[rows][cols]:
  *   mean = sum_c x_c / cols,  rstd = 1 / sqrt(sum_c (x_c - mean)^2 / cols + eps)
@@ -108,12 +115,6 @@ soma_status_t soma_linear_backward(int32_t device, const void *dy, int64_t dy_st
                                    int64_t dweight_stride, void *dbias, void *workspace, int64_t workspace_bytes,
                                    int64_t m, int64_t n, int64_t k, int32_t dtype, int32_t activation,
                                    void *stream);
-
-/* Every wait inside the matrix products is bounded (about a second; a step of
- * their pipeline takes microseconds).  Waits for `device` and returns
- * SOMA_ERR_STATE if one ran out since the last check, which leaves that
- * call's outputs invalid: a fault of the library, not of its arguments. */
-soma_status_t soma_linear_check(int32_t device);
 
 /* ---- distillation from a teacher's top logits -------------------------------
  * A teacher answers each row with `top` of its logits and their places in

@@ -35,7 +35,7 @@ SIGNATURES = {
                                             _I64P]),
     "soma_linear_backward": (_S, [_I32, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I64,
                                   _I64, _I64, _I64, _I32, _I32, _P]),
-    "soma_linear_check": (_S, [_I32]),
+    "soma_ops_check": (_S, [_I32]),
     "soma_distill_forward": (_S, [_I32, _P, _I64, _P, _I64, _P, _I64, _P, _D, _P, _P, _I64, _I64, _I64, _I32, _I32,
                                   _I32, _P]),
     "soma_distill_backward": (_S, [_I32, _P, _P, _I64, _P, _P, _I64, _P, _I64, _P, _D, _P, _I64, _I64, _I64, _I64,

@@ -21,7 +21,7 @@ LIB = os.path.join(OUT_DIR, "libsoma_opt.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["kernels.cu", "soma_opt.cpp", "noalloc.cu", "ops.cpp", "layer_norm.cu", "linear.cu", "distill.cu"]
-HEADERS = ["soma_kernels.h", "ops_kernels.h", "ops_device.cuh", "tcgen05.cuh"]
+HEADERS = ["soma_kernels.h", "ops_kernels.h", "ops_device.cuh", "mbarrier.cuh", "tcgen05.cuh"]
 PUBLIC_HEADERS = ["soma_opt.h", "soma_ops.h"]
 
 

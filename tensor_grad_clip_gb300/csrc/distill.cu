@@ -1,5 +1,21 @@
 // Distillation loss from a teacher's top logits (formulas in soma_ops.h).
+//
+// A row's logits are streamed in 16-byte vectors: the forward pass reads them
+// once (maximum and sum of exponentials together, in fp32), the backward pass
+// reads them once and writes the gradient, and the one-call form reads a row
+// twice, the second time from L2, where the rows in progress all fit.  One
+// exponential and about six other instructions per element keep the bound
+// with HBM.  The teacher's entries (at most 1024) live in shared memory; one
+// warp works on them while the others stream.
+//
+// A cluster of CTAs shares a row when there are fewer rows than CTAs that the
+// device holds, or when the rows in progress would not fit L2; the CTAs'
+// maxima and sums are joined through distributed shared memory, in rank
+// order.  Which thread takes which elements does not depend on where rows
+// start in memory, so neither do the results.
 #include <math.h>
+
+#include <algorithm>
 
 #include "ops_device.cuh"
 #include "ops_kernels.h"
@@ -8,126 +24,425 @@
 namespace soma {
 namespace {
 
-constexpr int kBlock = 256;
+constexpr int kMaxCluster = 8;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-__device__ __forceinline__ float block_sum(float x, float* scratch) {
-    __syncthreads();
-    scratch[threadIdx.x] = x;
-    __syncthreads();
-    float r = 0.f;
-    for (int i = 0; i < kBlock; ++i) r += scratch[i];
-    return r;
-}
-__device__ __forceinline__ float block_max(float x, float* scratch) {
-    __syncthreads();
-    scratch[threadIdx.x] = x;
-    __syncthreads();
-    float r = -INFINITY;
-    for (int i = 0; i < kBlock; ++i) r = fmaxf(r, scratch[i]);
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 
-template <typename T, typename U, int PASS>
-__global__ void __launch_bounds__(kBlock) distill_kernel(const __grid_constant__ DistillArgs a) {
-    __shared__ float scratch[kBlock];
-    __shared__ float p[SOMA_DISTILL_MAX_TOP], zt[SOMA_DISTILL_MAX_TOP];
-    __shared__ int at[SOMA_DISTILL_MAX_TOP];
-    const int t = threadIdx.x;
-    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        const T* z = static_cast<const T*>(a.logits) + r * a.logits_stride;
-        T* dz = static_cast<T*>(a.dlogits) + r * a.dlogits_stride;
-        const float w = a.row_weight ? a.row_weight[r] : 1.f;
-        const float scale = PASS == kDistillBackward ? a.grad_loss[r] * w : w;
-        if (scale == 0.f) {
-            if (t == 0 && PASS != kDistillBackward) a.loss[r] = 0.f;
-            if (t == 0 && PASS != kDistillBackward && a.lse) a.lse[r] = 0.f;
-            if (PASS != kDistillForward)
-                for (int v = t; v < a.vocab; v += kBlock) dz[v] = from_f32<T>(0.f);
-            continue;
-        }
-        __syncthreads();
-        float top = -INFINITY;
-        for (int j = t; j < a.top; j += kBlock) {
-            const int64_t i = a.index_type == SOMA_INDEX_I64
-                                  ? static_cast<const int64_t*>(a.index)[r * a.index_stride + j]
-                                  : static_cast<const int32_t*>(a.index)[r * a.index_stride + j];
-            const bool ok = i >= 0 && i < a.vocab;
-            at[j] = ok ? (int)i : -1;
-            p[j] = ok ? to_f32(static_cast<const U*>(a.teacher)[r * a.teacher_stride + j]) : -INFINITY;
-            zt[j] = ok ? to_f32(z[i]) : 0.f;
-            top = isnan(p[j]) ? p[j] : fmaxf(top, p[j]);
-        }
-        top = block_max(top, scratch);
-        float total = 0.f;
-        for (int j = t; j < a.top; j += kBlock)
-            if (p[j] != -INFINITY) total += expf((p[j] - top) * a.inv_temperature);
-        total = block_sum(total, scratch);
-        const bool any = !(top == -INFINITY && total == 0.f);
-        float lse, m = 0.f;
-        if (PASS == kDistillBackward) {
-            lse = a.lse_in[r];
-        } else {
-            m = -INFINITY;
-            for (int v = t; v < a.vocab; v += kBlock) m = fmaxf(m, to_f32(z[v]));
-            m = block_max(m, scratch);
-            float s = 0.f;
-            for (int v = t; v < a.vocab; v += kBlock) {
-                const float x = to_f32(z[v]);
-                if (x != -INFINITY) s += expf((x - m) * a.inv_temperature);
-            }
-            s = block_sum(s, scratch);
-            lse = m * a.inv_temperature + logf(s);
-        }
-        float loss = 0.f;
-        for (int j = t; j < a.top; j += kBlock) {
-            const float logp = (p[j] - top) * a.inv_temperature - logf(total);
-            const float pj = any && at[j] >= 0 ? expf(logp) : 0.f;
-            if (pj != 0.f) loss += pj * (logp - zt[j] * a.inv_temperature + lse);
-            p[j] = pj;
-        }
-        if (PASS != kDistillBackward) {
-            loss = block_sum(loss, scratch);
-            if (t == 0) {
-                a.loss[r] = w * a.temperature * a.temperature * loss;
-                if (a.lse) a.lse[r] = lse;
-            }
-        }
-        if (PASS != kDistillForward) {
-            __syncthreads();
-            const float g = scale * a.temperature;
-            for (int v = t; v < a.vocab; v += kBlock)
-                dz[v] = from_f32<T>(any ? g * expf(fmaf(to_f32(z[v]), a.inv_temperature, -lse)) : 0.f);
-            __syncthreads();
-            for (int j = t; j < a.top; j += kBlock) {
-                if (at[j] < 0) continue;
-                float sum = 0.f;
-                bool first = true;
-                for (int i = 0; i < a.top; ++i) {
-                    if (at[i] != at[j]) continue;
-                    if (i < j) first = false;
-                    sum += p[i];
-                }
-                if (first && any)
-                    dz[at[j]] = from_f32<T>(g * (expf(fmaf(zt[j], a.inv_temperature, -lse)) - sum));
+// A maximum m and the sum of exp2((x - m) c) over what has been seen.  m
+// starts at the lowest finite value, so that masked logits (-inf) add 0.
+struct MaxSum {
+    float m, s;
+};
+constexpr float kLowest = -3.402823466e38f;
+
+__device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b, float c) {
+    const float m = fmaxf(a.m, b.m);
+    return {m, a.s * exp2f((a.m - m) * c) + b.s * exp2f((b.m - m) * c)};
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float2 cluster_read(const float2* p, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+// Maximum; NaN if any x is.
+__device__ __forceinline__ float larger(float a, float b) { return a > b || a != a ? a : b; }
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x = larger(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+
+// A row of logits as vectors of kVec elements, vector i from element kVec i
+// on, wherever the row starts: where that is inside a 16-byte word, a vector
+// is shifted out of two words.
+template <typename T, bool kKeep>
+struct RowReader {
+    static constexpr int kVec = 16 / sizeof(T);
+    const T* row;
+    const uint4* words;  // the word that holds the row's first element
+    int phase, cols;
+    // Vectors [inner_begin, inner_end) are whole and lie in words inside the
+    // matrix, whose first and last rows may end inside a word.
+    int inner_begin, inner_end;
+
+    __device__ __forceinline__ RowReader(const T* base, int64_t stride, int64_t rows, int64_t r, int n)
+        : row(base + r * stride), phase((int)((uintptr_t)row & 15)), cols(n) {
+        words = reinterpret_cast<const uint4*>((uintptr_t)row & ~(uintptr_t)15);
+        inner_begin = (uintptr_t)words < (uintptr_t)base ? 1 : 0;
+        const uintptr_t end = (uintptr_t)(base + (rows - 1) * stride + cols) & ~(uintptr_t)15;
+        // vector i takes bytes up to 16 (i + 1), or 16 (i + 2) when shifted
+        const int64_t fit = ((int64_t)(end - (uintptr_t)words) >> 4) - (phase ? 1 : 0);
+        inner_end = (int)min(fit < 0 ? (int64_t)0 : fit, (int64_t)(cols / kVec));
+    }
+    // One vector anywhere in the row; elements past the row's end are -inf.
+    __device__ __forceinline__ void gather(int i, float (&x)[kVec]) const {
+#pragma unroll
+        for (int q = 0; q < kVec; ++q) x[q] = kVec * i + q < cols ? to_f32(row[kVec * i + q]) : -INFINITY;
+    }
+    // Vectors [i, i + n step) of whole words, step apart.
+    template <bool kShift, int kN>
+    __device__ __forceinline__ void load(int i, int step, uint4 (&u)[kN], uint4 (&v)[kShift ? kN : 1]) const {
+#pragma unroll
+        for (int q = 0; q < kN; ++q) {
+            const uint4* w = words + i + q * step;
+            if (kShift) {  // the neighbouring vector's word comes out of L1
+                u[q] = w[0];
+                v[kShift ? q : 0] = w[1];
+            } else if (kKeep) {  // read again from L2
+                asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(u[q].x), "=r"(u[q].y), "=r"(u[q].z), "=r"(u[q].w)
+                             : "l"(w)
+                             : "memory");
+            } else {
+                u[q] = __ldcs(w);
             }
         }
     }
+    template <bool kShift>
+    __device__ __forceinline__ void widen(const uint4& u, const uint4& v, float (&x)[kVec]) const {
+        widen16(kShift ? shifted<T>(u, v, phase) : u, x, T{});
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ void take(MaxSum& a, const float (&x)[16 / sizeof(T)], float c) {
+    constexpr int kVec = 16 / sizeof(T);
+    float m = x[0];
+#pragma unroll
+    for (int i = 1; i < kVec; ++i) m = fmaxf(m, x[i]);
+    if (m > a.m) {
+        a.s *= exp2_fast((a.m - m) * c);
+        a.m = m;
+    }
+    const float2 back = both(-a.m), cc = both(c);
+#pragma unroll
+    for (int i = 0; i < kVec; i += 2) {
+        const float2 d = mul2(add2(make_float2(x[i], x[i + 1]), back), cc);
+        a.s += exp2_fast(d.x) + exp2_fast(d.y);
+    }
+}
+
+// Maximum and sum of vectors [begin, end): vector i is thread i - begin mod
+// kBlock's, in ascending order.
+template <typename T, bool kKeep, int kBlock, bool kShift>
+__device__ __forceinline__ MaxSum stream_max_sum(const RowReader<T, kKeep>& row, int begin, int end, float c) {
+    constexpr int kVec = 16 / sizeof(T), kAhead = kShift ? 2 : 4;
+    MaxSum a{kLowest, 0.f};
+    int i = begin + threadIdx.x;
+    float x[kVec];
+    if (i < row.inner_begin && i < end) {
+        row.gather(i, x);
+        take<T>(a, x, c);
+        i += kBlock;
+    }
+    const int inner = min(end, row.inner_end);
+    uint4 u[kAhead], v[kShift ? kAhead : 1];
+    for (; i + (kAhead - 1) * kBlock < inner; i += kAhead * kBlock) {
+        row.template load<kShift, kAhead>(i, kBlock, u, v);
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) {
+            row.template widen<kShift>(u[q], v[kShift ? q : 0], x);
+            take<T>(a, x, c);
+        }
+    }
+    for (; i < inner; i += kBlock) {
+        uint4 u1[1], v1[1];
+        row.template load<kShift, 1>(i, kBlock, u1, v1);
+        row.template widen<kShift>(u1[0], v1[0], x);
+        take<T>(a, x, c);
+    }
+    for (; i < end; i += kBlock) {
+        row.gather(i, x);
+        take<T>(a, x, c);
+    }
+    return a;
+}
+
+// g q for one vector, q = exp(z / T - lse).
+template <typename T>
+__device__ __forceinline__ void scaled_softmax(float (&x)[16 / sizeof(T)], float inv_t, float lse, float g) {
+    const float2 inv2 = both(inv_t), lse2 = both(-lse), log2 = both(kLog2e), g2 = both(g);
+#pragma unroll
+    for (int q = 0; q < 16 / (int)sizeof(T); q += 2) {
+        const float2 d = mul2(fma2(make_float2(x[q], x[q + 1]), inv2, lse2), log2);
+        const float2 e = mul2(make_float2(exp2_fast(d.x), exp2_fast(d.y)), g2);
+        x[q] = e.x;
+        x[q + 1] = e.y;
+    }
+}
+
+// out = g q of vectors [begin, end).  Rows of logits and gradient that start
+// on 16-byte boundaries go vector by vector; else whole warps take
+// consecutive vectors together, as store_vector needs.
+template <typename T, int kBlock>
+__device__ __forceinline__ void stream_gradient(const RowReader<T, false>& row, T* out, int begin, int end, float inv_t,
+                                                float lse, float g) {
+    constexpr int kVec = 16 / sizeof(T);
+    float x[kVec];
+    const int out_phase = (int)((uintptr_t)out & 15);
+    const int inner = min(end, row.inner_end);
+    if (out_phase == 0 && row.phase == 0) {
+        constexpr int kAhead = 4;
+        uint4 u[kAhead], none[1];
+        int i = begin + threadIdx.x;
+        for (; i + (kAhead - 1) * kBlock < inner; i += kAhead * kBlock) {
+            row.template load<false, kAhead>(i, kBlock, u, none);
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) {
+                row.template widen<false>(u[q], none[0], x);
+                scaled_softmax<T>(x, inv_t, lse, g);
+                __stcs(reinterpret_cast<uint4*>(out) + i + q * kBlock, narrow16(x, T{}));
+            }
+        }
+        for (; i < end; i += kBlock) {
+            row.gather(i, x);
+            scaled_softmax<T>(x, inv_t, lse, g);
+            store_vector<T, true>(out, (int64_t)kVec * i, row.cols, 0, x);
+        }
+        return;
+    }
+    const int lane = threadIdx.x & 31;
+    const int cols = min(row.cols, end * kVec);  // (a CTA of a cluster stores nothing past its part)
+    for (int base = begin + (threadIdx.x & ~31); base < end; base += kBlock) {
+        const int i = base + lane;
+        if (base >= row.inner_begin && base + 32 <= inner) {
+            uint4 u[1], v[1];
+            if (row.phase) {
+                row.template load<true, 1>(i, 0, u, v);
+                row.template widen<true>(u[0], v[0], x);
+            } else {
+                row.template load<false, 1>(i, 0, u, v);
+                row.template widen<false>(u[0], v[0], x);
+            }
+        } else {
+            row.gather(i, x);
+        }
+        scaled_softmax<T>(x, inv_t, lse, g);
+        store_vector<T, false>(out, (int64_t)kVec * i, cols, out_phase, x);
+    }
+}
+
+template <typename T, int kBlock>
+__device__ __forceinline__ void stream_zeros(T* out, int begin, int end, int cols) {
+    constexpr int kVec = 16 / sizeof(T);
+    const float zero[kVec] = {};
+    const int out_phase = (int)((uintptr_t)out & 15);
+    for (int base = begin + (threadIdx.x & ~31); base < end; base += kBlock)
+        store_vector<T, false>(out, (int64_t)kVec * (base + (threadIdx.x & 31)), min(cols, end * kVec), out_phase, zero);
+}
+
+// Teacher logit j of row r.
+template <typename U>
+__device__ __forceinline__ float teacher_at(const DistillArgs& a, int64_t r, int j) {
+    return to_f32(static_cast<const U*>(a.teacher)[r * a.teacher_stride + j]);
+}
+
+// kBlock threads per CTA: few for short rows, of which an SM then holds many.
+template <typename T, int PASS, int kBlock>
+__global__ void __launch_bounds__(kBlock, 1536 / kBlock) distill_kernel(const __grid_constant__ DistillArgs a, int cluster) {
+    constexpr int kVec = 16 / sizeof(T), kWarps = kBlock / 32;
+    __shared__ float2 warp_part[kWarps];
+    __shared__ float2 cta_part;
+    __shared__ float p[SOMA_DISTILL_MAX_TOP], zt[SOMA_DISTILL_MAX_TOP];
+    __shared__ int at[SOMA_DISTILL_MAX_TOP];
+    __shared__ int any_entry;
+    const int t = threadIdx.x, lane = t & 31;
+    const int64_t r = blockIdx.x / cluster;
+    const int rank = (int)(blockIdx.x % cluster);
+    T* dz = static_cast<T*>(a.dlogits) + r * a.dlogits_stride;
+    const float w = a.row_weight ? a.row_weight[r] : 1.f;
+    const float scale = PASS == kDistillBackward ? a.grad_loss[r] * w : w;
+
+    // this CTA's vectors of the row
+    const int vectors = (a.vocab + kVec - 1) / kVec;
+    const int begin = (int)((int64_t)vectors * rank / cluster), end = (int)((int64_t)vectors * (rank + 1) / cluster);
+
+    if (scale == 0.f) {  // (the same for all CTAs of the row)
+        if (PASS != kDistillBackward && t == 0 && rank == 0) {
+            a.loss[r] = 0.f;
+            if (a.lse) a.lse[r] = 0.f;
+        }
+        if (PASS != kDistillForward) stream_zeros<T, kBlock>(dz, begin, end, a.vocab);
+        return;
+    }
+    const T* z0 = static_cast<const T*>(a.logits);
+    const T* z = z0 + r * a.logits_stride;
+
+    // The teacher's entries and the student's logits at their places.
+    if (t == 0) any_entry = 0;
+    __syncthreads();
+    for (int j = t; j < a.top; j += kBlock) {
+        const int64_t i = a.index_type == SOMA_INDEX_I64 ? static_cast<const int64_t*>(a.index)[r * a.index_stride + j]
+                                                         : static_cast<const int32_t*>(a.index)[r * a.index_stride + j];
+        const bool ok = i >= 0 && i < a.vocab;
+        float x = -INFINITY;
+        if (ok) {
+            x = a.teacher_dtype == kF32    ? teacher_at<float>(a, r, j)
+                : a.teacher_dtype == kBF16 ? teacher_at<__nv_bfloat16>(a, r, j)
+                                           : teacher_at<__half>(a, r, j);
+        }
+        at[j] = ok ? (int)i : -1;
+        p[j] = x;
+        zt[j] = ok ? to_f32(z[i]) : 0.f;
+        if (x != -INFINITY) any_entry = 1;
+    }
+    // The student's normalizer.
+    float lse = 0.f;
+    if (PASS == kDistillBackward) {
+        lse = a.lse_in[r];
+        if (cluster > 1) cluster_sync_all();  // every CTA has read zt: dz may take the logits' place
+        else __syncthreads();
+    } else {
+        const float c = a.inv_temperature * kLog2e;
+        const RowReader<T, PASS == kDistillLossGrad> row(z0, a.logits_stride, a.rows, r, a.vocab);
+        MaxSum mine = row.phase ? stream_max_sum<T, PASS == kDistillLossGrad, kBlock, true>(row, begin, end, c)
+                                : stream_max_sum<T, PASS == kDistillLossGrad, kBlock, false>(row, begin, end, c);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            mine = join(mine, {__shfl_xor_sync(0xffffffffu, mine.m, o), __shfl_xor_sync(0xffffffffu, mine.s, o)}, c);
+        if (lane == 0) warp_part[t >> 5] = make_float2(mine.m, mine.s);
+        __syncthreads();
+        // every warp joins the warps' parts, a lane each
+        const float2 part = warp_part[lane % kWarps];
+        mine = {part.x, part.y};
+#pragma unroll
+        for (int o = kWarps / 2; o > 0; o >>= 1)
+            mine = join(mine, {__shfl_xor_sync(0xffffffffu, mine.m, o), __shfl_xor_sync(0xffffffffu, mine.s, o)}, c);
+        if (cluster > 1) {
+            if (t == 0) cta_part = make_float2(mine.m, mine.s);
+            cluster_sync_all();
+            const float2 other = cluster_read(&cta_part, lane % cluster);
+            mine = {other.x, other.y};
+            for (int o = cluster / 2; o > 0; o >>= 1)
+                mine = join(mine, {__shfl_xor_sync(0xffffffffu, mine.m, o), __shfl_xor_sync(0xffffffffu, mine.s, o)}, c);
+        }
+        lse = fmaf(mine.m, a.inv_temperature, logf(mine.s));
+    }
+    const bool any = any_entry != 0;
+    if (t < 32) {  // the teacher's distribution, and the loss
+        float top = -INFINITY, total = 0.f, loss = 0.f;
+        for (int j = lane; j < a.top; j += 32) top = larger(top, p[j]);
+        top = warp_max(top);
+        for (int j = lane; j < a.top; j += 32)
+            if (p[j] != -INFINITY) total += expf((p[j] - top) * a.inv_temperature);
+        total = warp_sum(total);
+        const float log_total = logf(total);
+        for (int j = lane; j < a.top; j += 32) {
+            const float logp = (p[j] - top) * a.inv_temperature - log_total;
+            const float pj = any && at[j] >= 0 ? expf(logp) : 0.f;
+            if (pj != 0.f) loss += pj * (logp - fmaf(zt[j], a.inv_temperature, -lse));
+            p[j] = pj;
+        }
+        if (PASS != kDistillBackward) {
+            loss = warp_sum(loss);
+            if (t == 0 && rank == 0) {
+                a.loss[r] = any ? w * a.temperature * a.temperature * loss : 0.f;
+                if (a.lse) a.lse[r] = lse;
+            }
+        }
+        __syncwarp();
+    }
+    if (PASS != kDistillForward) {
+        const float g = scale * a.temperature;
+        const RowReader<T, false> row(z0, a.logits_stride, a.rows, r, a.vocab);
+        if (any) stream_gradient<T, kBlock>(row, dz, begin, end, a.inv_temperature, lse, g);
+        else stream_zeros<T, kBlock>(dz, begin, end, a.vocab);
+        __syncthreads();
+        for (int j = t; any && j < a.top; j += kBlock) {
+            const int v = at[j];
+            if (v < begin * kVec || v >= end * kVec) continue;
+            float sum = 0.f;
+            bool first = true;
+            for (int i = 0; i < a.top; ++i) {
+                if (at[i] != v) continue;
+                if (i < j) first = false;
+                sum += p[i];
+            }
+            if (first) dz[v] = from_f32<T>(g * (exp2_fast(fmaf(zt[j], a.inv_temperature, -lse) * kLog2e) - sum));
+        }
+    }
+    if (cluster > 1 && PASS != kDistillBackward) cluster_sync_all();  // no CTA leaves while another may read its part
+}
+
+// CTAs that share a row: enough to fill the device with few rows (each at
+// least 16 KB of logits), and in the one-call form so many that the rows in
+// progress stay within 32 MB, well inside L2 beside the gradient's writes.
+int cluster_of(const DistillArgs& a, DistillPass pass, int64_t row_bytes, int64_t ctas) {
+    int cluster = 1;
+    while (cluster < kMaxCluster && row_bytes >= cluster * 2 * 16384 &&
+           (a.rows * cluster * 2 <= ctas ||
+            (pass == kDistillLossGrad && std::min(a.rows, ctas / cluster) * row_bytes > (32 << 20))))
+        cluster *= 2;
+    return cluster;
+}
+
+template <typename T, int kBlock>
+int launch_rows(const DistillArgs& a, DistillPass pass, int sm_count, cudaStream_t stream) {
+    auto kernel = pass == kDistillForward    ? distill_kernel<T, kDistillForward, kBlock>
+                  : pass == kDistillBackward ? distill_kernel<T, kDistillBackward, kBlock>
+                                             : distill_kernel<T, kDistillLossGrad, kBlock>;
+    int cluster = cluster_of(a, pass, (int64_t)a.vocab * (int)sizeof(T), (int64_t)sm_count * (1536 / kBlock));
+    cudaLaunchConfig_t cfg{};
+    cfg.blockDim = dim3(kBlock);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    // a grid holds 2^31 - 1 CTAs: longer lists of rows go in parts
+    const int64_t most = 0x7fffffff / kMaxCluster;
+    int e = cudaSuccess;
+    for (int64_t r0 = 0; r0 < a.rows && e == cudaSuccess; r0 += most) {
+        DistillArgs part = a;
+        part.rows = std::min(a.rows - r0, most);
+        if (r0 > 0) {
+            part.logits = static_cast<const T*>(a.logits) + r0 * a.logits_stride;
+            part.teacher = static_cast<const char*>(a.teacher) + r0 * a.teacher_stride * (a.teacher_dtype == kF32 ? 4 : 2);
+            part.index = static_cast<const char*>(a.index) + r0 * a.index_stride * (a.index_type == SOMA_INDEX_I64 ? 8 : 4);
+            if (a.row_weight) part.row_weight = a.row_weight + r0;
+            if (a.grad_loss) part.grad_loss = a.grad_loss + r0;
+            if (a.lse_in) part.lse_in = a.lse_in + r0;
+            if (a.loss) part.loss = a.loss + r0;
+            if (a.lse) part.lse = a.lse + r0;
+            if (a.dlogits) part.dlogits = static_cast<T*>(a.dlogits) + r0 * a.dlogits_stride;
+        }
+        cfg.gridDim = dim3((unsigned)(part.rows * cluster));
+        e = (int)cudaLaunchKernelEx(&cfg, kernel, part, cluster);
+    }
+    return e;
 }
 
 }  // namespace
 
 int launch_distill(const DistillArgs& a, DistillPass pass, int sm_count, void* stream) {
     return with_type(a.dtype, [&](auto t) {
-        return with_type(a.teacher_dtype, [&](auto u) {
-            using T = decltype(t);
-            using U = decltype(u);
-            const int grid = (int)(a.rows < 8 * sm_count ? a.rows : 8 * sm_count);
-            cudaStream_t st = (cudaStream_t)stream;
-            if (pass == kDistillForward) distill_kernel<T, U, kDistillForward><<<grid, kBlock, 0, st>>>(a);
-            else if (pass == kDistillBackward) distill_kernel<T, U, kDistillBackward><<<grid, kBlock, 0, st>>>(a);
-            else distill_kernel<T, U, kDistillLossGrad><<<grid, kBlock, 0, st>>>(a);
-            return (int)cudaGetLastError();
-        });
+        using T = decltype(t);
+        if ((int64_t)a.vocab * (int)sizeof(T) <= 32768) return launch_rows<T, 128>(a, pass, sm_count, (cudaStream_t)stream);
+        return launch_rows<T, 512>(a, pass, sm_count, (cudaStream_t)stream);
     });
 }
 

@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
     __syncwarp();
     if (gave_up) {  // what is still in flight lands before the CTA's memory is given back
         if (threadIdx.x == 0) g_gave_up = 1;
-        for (int i = 0; i < 100; ++i) __nanosleep(20000);
+        outlast_copies();
     }
     tcgen05_before_sync();
     if (CG == 2) cluster_sync_all();
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
     __syncwarp();
     if (gave_up) {
         if (threadIdx.x == 0) g_gave_up = 1;
-        for (int i = 0; i < 100; ++i) __nanosleep(20000);
+        outlast_copies();
     }
     if (splits > 1) cluster_sync_all();  // every partial sum has arrived; no CTA's memory is written after this
     else __syncthreads();
@@ -667,7 +667,7 @@ int launch_gemm(const GemmArgs& a, int sm_count, void* stream) {
     });
 }
 
-int take_gave_up(int* value) {
+int take_linear_gave_up(int* value) {
     int e = cudaMemcpyFromSymbol(value, g_gave_up, sizeof(int));
     if (e == cudaSuccess && *value) {
         const int zero = 0;

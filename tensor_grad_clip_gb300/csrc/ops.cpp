@@ -210,6 +210,18 @@ extern "C" {
 
 const char* soma_ops_last_error(void) { return g_error.c_str(); }
 
+soma_status_t soma_ops_check(int32_t device) {
+    SOMA_ON_DEVICE(device);
+    (void)sms;
+    int norm = 0, linear = 0;
+    SOMA_TRY(cuda_status(soma::take_norm_gave_up(&norm), "check"));
+    SOMA_TRY(cuda_status(soma::take_linear_gave_up(&linear), "check"));
+    if (norm || linear)
+        return fail(SOMA_ERR_STATE, "a %s kernel gave up waiting for its own copies: its results are not valid",
+                    norm ? "layer norm" : "linear");
+    return SOMA_OK;
+}
+
 // ---- layer norm -----------------------------------------------------------
 
 soma_status_t soma_layer_norm_forward(int32_t device, const void* x, int64_t x_stride, const void* weight,
@@ -370,15 +382,6 @@ soma_status_t soma_linear_backward(int32_t device, const void* dy, int64_t dy_st
                                nullptr, 0, (int32_t)n, (int32_t)k, (int32_t)m, dtype, SOMA_ACT_NONE},
                               sms, stream);
     return cuda_status(e, "linear backward");
-}
-
-soma_status_t soma_linear_check(int32_t device) {
-    SOMA_ON_DEVICE(device);
-    (void)sms;
-    int gave_up = 0;
-    SOMA_TRY(cuda_status(soma::take_gave_up(&gave_up), "linear check"));
-    if (gave_up) return fail(SOMA_ERR_STATE, "a matrix product gave up waiting for its own pipeline: its results are not valid");
-    return SOMA_OK;
 }
 
 // ---- distillation loss ----------------------------------------------------

@@ -74,10 +74,6 @@ bool gemm_operand_needs_copy(const void* p, int64_t stride, int64_t rows);
 int launch_repack(const void* src, int64_t src_stride, void* dst, int64_t dst_stride, int64_t rows, int64_t cols,
                   void* stream);
 
-// Whether a bounded wait of a matrix product on the current device ran out
-// since the last call (waits for the device).
-int take_gave_up(int* value);
-
 // dz = dy * act'(z) (dz == nullptr: not stored), and dbias = column sums of
 // the unrounded dz (dbias == nullptr: not wanted).
 struct ActBwdArgs {
@@ -121,5 +117,10 @@ struct DistillArgs {
 enum DistillPass : int32_t { kDistillForward, kDistillBackward, kDistillLossGrad };
 
 int launch_distill(const DistillArgs& a, DistillPass pass, int sm_count, void* stream);
+
+// Whether a bounded wait inside a kernel of the current device ran out since
+// the last call (waits for the device).
+int take_norm_gave_up(int* value);
+int take_linear_gave_up(int* value);
 
 }  // namespace soma
