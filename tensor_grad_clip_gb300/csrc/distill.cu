@@ -9,9 +9,8 @@
 // warp works on them while the others stream.
 //
 // A cluster of CTAs shares a row when there are fewer rows than CTAs that the
-// device holds, or when the rows in progress would not fit L2; the CTAs'
-// maxima and sums are joined through distributed shared memory, in rank
-// order.  Which thread takes which elements does not depend on where rows
+// device holds; the CTAs' maxima and sums are joined through distributed
+// shared memory, in rank order.  Which thread takes which elements does not depend on where rows
 // start in memory, so neither do the results.
 #include <math.h>
 
@@ -73,58 +72,6 @@ __device__ __forceinline__ float warp_max(float x) {
     for (int o = 16; o > 0; o >>= 1) x = larger(x, __shfl_xor_sync(0xffffffffu, x, o));
     return x;
 }
-
-// A row of logits as vectors of kVec elements, vector i from element kVec i
-// on, wherever the row starts: where that is inside a 16-byte word, a vector
-// is shifted out of two words.
-template <typename T, bool kKeep>
-struct RowReader {
-    static constexpr int kVec = 16 / sizeof(T);
-    const T* row;
-    const uint4* words;  // the word that holds the row's first element
-    int phase, cols;
-    // Vectors [inner_begin, inner_end) are whole and lie in words inside the
-    // matrix, whose first and last rows may end inside a word.
-    int inner_begin, inner_end;
-
-    __device__ __forceinline__ RowReader(const T* base, int64_t stride, int64_t rows, int64_t r, int n)
-        : row(base + r * stride), phase((int)((uintptr_t)row & 15)), cols(n) {
-        words = reinterpret_cast<const uint4*>((uintptr_t)row & ~(uintptr_t)15);
-        inner_begin = (uintptr_t)words < (uintptr_t)base ? 1 : 0;
-        const uintptr_t end = (uintptr_t)(base + (rows - 1) * stride + cols) & ~(uintptr_t)15;
-        // vector i takes bytes up to 16 (i + 1), or 16 (i + 2) when shifted
-        const int64_t fit = ((int64_t)(end - (uintptr_t)words) >> 4) - (phase ? 1 : 0);
-        inner_end = (int)min(fit < 0 ? (int64_t)0 : fit, (int64_t)(cols / kVec));
-    }
-    // One vector anywhere in the row; elements past the row's end are -inf.
-    __device__ __forceinline__ void gather(int i, float (&x)[kVec]) const {
-#pragma unroll
-        for (int q = 0; q < kVec; ++q) x[q] = kVec * i + q < cols ? to_f32(row[kVec * i + q]) : -INFINITY;
-    }
-    // Vectors [i, i + n step) of whole words, step apart.
-    template <bool kShift, int kN>
-    __device__ __forceinline__ void load(int i, int step, uint4 (&u)[kN], uint4 (&v)[kShift ? kN : 1]) const {
-#pragma unroll
-        for (int q = 0; q < kN; ++q) {
-            const uint4* w = words + i + q * step;
-            if (kShift) {  // the neighbouring vector's word comes out of L1
-                u[q] = w[0];
-                v[kShift ? q : 0] = w[1];
-            } else if (kKeep) {  // read again from L2
-                asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(u[q].x), "=r"(u[q].y), "=r"(u[q].z), "=r"(u[q].w)
-                             : "l"(w)
-                             : "memory");
-            } else {
-                u[q] = __ldcs(w);
-            }
-        }
-    }
-    template <bool kShift>
-    __device__ __forceinline__ void widen(const uint4& u, const uint4& v, float (&x)[kVec]) const {
-        widen16(kShift ? shifted<T>(u, v, phase) : u, x, T{});
-    }
-};
 
 template <typename T>
 __device__ __forceinline__ void take(MaxSum& a, const float (&x)[16 / sizeof(T)], float c) {
@@ -196,9 +143,12 @@ __device__ __forceinline__ void scaled_softmax(float (&x)[16 / sizeof(T)], float
 // out = g q of vectors [begin, end).  Rows of logits and gradient that start
 // on 16-byte boundaries go vector by vector; else whole warps take
 // consecutive vectors together, as store_vector needs.
-template <typename T, int kBlock>
+// ready() waits for what the first vector needs (lse, and for the others to
+// be done with logits that the gradient replaces); the first loads are in
+// flight meanwhile.
+template <typename T, int kBlock, typename Ready>
 __device__ __forceinline__ void stream_gradient(const RowReader<T, false>& row, T* out, int begin, int end, float inv_t,
-                                                float lse, float g) {
+                                                float g, Ready&& ready) {
     constexpr int kVec = 16 / sizeof(T);
     float x[kVec];
     const int out_phase = (int)((uintptr_t)out & 15);
@@ -207,8 +157,11 @@ __device__ __forceinline__ void stream_gradient(const RowReader<T, false>& row, 
         constexpr int kAhead = 4;
         uint4 u[kAhead], none[1];
         int i = begin + threadIdx.x;
-        for (; i + (kAhead - 1) * kBlock < inner; i += kAhead * kBlock) {
-            row.template load<false, kAhead>(i, kBlock, u, none);
+        const bool full = i + (kAhead - 1) * kBlock < inner;
+        if (full) row.template load<false, kAhead>(i, kBlock, u, none);
+        const float lse = ready();
+        for (bool loaded = true; i + (kAhead - 1) * kBlock < inner; i += kAhead * kBlock, loaded = false) {
+            if (!loaded) row.template load<false, kAhead>(i, kBlock, u, none);
 #pragma unroll
             for (int q = 0; q < kAhead; ++q) {
                 row.template widen<false>(u[q], none[0], x);
@@ -223,6 +176,7 @@ __device__ __forceinline__ void stream_gradient(const RowReader<T, false>& row, 
         }
         return;
     }
+    const float lse = ready();
     const int lane = threadIdx.x & 31;
     const int cols = min(row.cols, end * kVec);  // (a CTA of a cluster stores nothing past its part)
     for (int base = begin + (threadIdx.x & ~31); base < end; base += kBlock) {
@@ -265,8 +219,8 @@ __global__ void __launch_bounds__(kBlock, 1536 / kBlock) distill_kernel(const __
     constexpr int kVec = 16 / sizeof(T), kWarps = kBlock / 32;
     __shared__ float2 warp_part[kWarps];
     __shared__ float2 cta_part;
-    __shared__ float p[SOMA_DISTILL_MAX_TOP], zt[SOMA_DISTILL_MAX_TOP];
-    __shared__ int at[SOMA_DISTILL_MAX_TOP];
+    __shared__ __align__(16) float p[SOMA_DISTILL_MAX_TOP], zt[SOMA_DISTILL_MAX_TOP];
+    __shared__ __align__(16) int at[SOMA_DISTILL_MAX_TOP];
     __shared__ int any_entry;
     const int t = threadIdx.x, lane = t & 31;
     const int64_t r = blockIdx.x / cluster;
@@ -290,39 +244,57 @@ __global__ void __launch_bounds__(kBlock, 1536 / kBlock) distill_kernel(const __
     const T* z0 = static_cast<const T*>(a.logits);
     const T* z = z0 + r * a.logits_stride;
 
-    // The teacher's entries and the student's logits at their places.
+    // The teacher's entries: each thread's first one is loaded here and put
+    // away by put_entries, with the student's logits at their places.
     if (t == 0) any_entry = 0;
-    __syncthreads();
-    for (int j = t; j < a.top; j += kBlock) {
-        const int64_t i = a.index_type == SOMA_INDEX_I64 ? static_cast<const int64_t*>(a.index)[r * a.index_stride + j]
-                                                         : static_cast<const int32_t*>(a.index)[r * a.index_stride + j];
-        const bool ok = i >= 0 && i < a.vocab;
-        float x = -INFINITY;
-        if (ok) {
-            x = a.teacher_dtype == kF32    ? teacher_at<float>(a, r, j)
-                : a.teacher_dtype == kBF16 ? teacher_at<__nv_bfloat16>(a, r, j)
-                                           : teacher_at<__half>(a, r, j);
+    auto index_at = [&](int j) {
+        return a.index_type == SOMA_INDEX_I64 ? static_cast<const int64_t*>(a.index)[r * a.index_stride + j]
+                                              : (int64_t) static_cast<const int32_t*>(a.index)[r * a.index_stride + j];
+    };
+    auto logit_at = [&](int j) {
+        return a.teacher_dtype == kF32    ? teacher_at<float>(a, r, j)
+               : a.teacher_dtype == kBF16 ? teacher_at<__nv_bfloat16>(a, r, j)
+                                          : teacher_at<__half>(a, r, j);
+    };
+    const int64_t first_index = t < a.top ? index_at(t) : -1;
+    const float first_logit = t < a.top ? logit_at(t) : -INFINITY;
+    auto put_entries = [&] {
+        for (int j = t; j < (a.top + 3) / 4 * 4; j += kBlock) {
+            const int64_t i = j >= a.top ? -1 : j == t ? first_index : index_at(j);
+            const bool ok = i >= 0 && i < a.vocab;
+            const float x = !ok ? -INFINITY : j == t ? first_logit : logit_at(j);
+            at[j] = ok ? (int)i : -1;
+            p[j] = x;
+            zt[j] = ok ? to_f32(z[i]) : 0.f;
+            if (x != -INFINITY) any_entry = 1;
         }
-        at[j] = ok ? (int)i : -1;
-        p[j] = x;
-        zt[j] = ok ? to_f32(z[i]) : 0.f;
-        if (x != -INFINITY) any_entry = 1;
-    }
+    };
     // The student's normalizer.
     float lse = 0.f;
+    MaxSum mine{kLowest, 0.f};
+    const float c = a.inv_temperature * kLog2e;
+    __syncthreads();
     if (PASS == kDistillBackward) {
         lse = a.lse_in[r];
-        if (cluster > 1) cluster_sync_all();  // every CTA has read zt: dz may take the logits' place
-        else __syncthreads();
+        put_entries();
     } else {
-        const float c = a.inv_temperature * kLog2e;
         const RowReader<T, PASS == kDistillLossGrad> row(z0, a.logits_stride, a.rows, r, a.vocab);
-        MaxSum mine = row.phase ? stream_max_sum<T, PASS == kDistillLossGrad, kBlock, true>(row, begin, end, c)
-                                : stream_max_sum<T, PASS == kDistillLossGrad, kBlock, false>(row, begin, end, c);
+        mine = row.phase ? stream_max_sum<T, PASS == kDistillLossGrad, kBlock, true>(row, begin, end, c)
+                         : stream_max_sum<T, PASS == kDistillLossGrad, kBlock, false>(row, begin, end, c);
+        put_entries();
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             mine = join(mine, {__shfl_xor_sync(0xffffffffu, mine.m, o), __shfl_xor_sync(0xffffffffu, mine.s, o)}, c);
         if (lane == 0) warp_part[t >> 5] = make_float2(mine.m, mine.s);
+    }
+    // What the CTAs of the row have to know of one another: lse, and that all
+    // have read zt (dz may take the logits' place).
+    auto ready = [&] {
+        if (PASS == kDistillBackward) {
+            if (cluster > 1) cluster_sync_all();
+            else __syncthreads();
+            return lse;
+        }
         __syncthreads();
         // every warp joins the warps' parts, a lane each
         const float2 part = warp_part[lane % kWarps];
@@ -338,10 +310,11 @@ __global__ void __launch_bounds__(kBlock, 1536 / kBlock) distill_kernel(const __
             for (int o = cluster / 2; o > 0; o >>= 1)
                 mine = join(mine, {__shfl_xor_sync(0xffffffffu, mine.m, o), __shfl_xor_sync(0xffffffffu, mine.s, o)}, c);
         }
-        lse = fmaf(mine.m, a.inv_temperature, logf(mine.s));
-    }
-    const bool any = any_entry != 0;
-    if (t < 32) {  // the teacher's distribution, and the loss
+        return fmaf(mine.m, a.inv_temperature, logf(mine.s));
+    };
+    // The teacher's distribution, and the loss, by the first warp.
+    auto teach = [&] {
+        const bool any = any_entry != 0;
         float top = -INFINITY, total = 0.f, loss = 0.f;
         for (int j = lane; j < a.top; j += 32) top = larger(top, p[j]);
         top = warp_max(top);
@@ -362,39 +335,44 @@ __global__ void __launch_bounds__(kBlock, 1536 / kBlock) distill_kernel(const __
                 if (a.lse) a.lse[r] = lse;
             }
         }
-        __syncwarp();
-    }
-    if (PASS != kDistillForward) {
+    };
+    if (PASS == kDistillForward) {
+        lse = ready();
+        if (t < 32) teach();
+    } else {
         const float g = scale * a.temperature;
         const RowReader<T, false> row(z0, a.logits_stride, a.rows, r, a.vocab);
-        if (any) stream_gradient<T, kBlock>(row, dz, begin, end, a.inv_temperature, lse, g);
-        else stream_zeros<T, kBlock>(dz, begin, end, a.vocab);
+        stream_gradient<T, kBlock>(row, dz, begin, end, a.inv_temperature, g, [&] { return lse = ready(); });
+        if (t < 32) teach();
         __syncthreads();
-        for (int j = t; any && j < a.top; j += kBlock) {
-            const int v = at[j];
-            if (v < begin * kVec || v >= end * kVec) continue;
-            float sum = 0.f;
-            bool first = true;
-            for (int i = 0; i < a.top; ++i) {
-                if (at[i] != v) continue;
-                if (i < j) first = false;
-                sum += p[i];
+        if (any_entry == 0) {  // no teacher: what was just written goes back to 0
+            stream_zeros<T, kBlock>(dz, begin, end, a.vocab);
+        } else {
+            for (int j = t; j < a.top; j += kBlock) {
+                const int v = at[j];
+                if (v < begin * kVec || v >= end * kVec) continue;
+                float sum = 0.f;
+                bool first = true;
+                for (int i = 0; i < a.top; i += 4) {  // (p of the entries past top is -inf: never at v)
+                    const int4 i4 = *reinterpret_cast<const int4*>(at + i);
+                    const float4 p4 = *reinterpret_cast<const float4*>(p + i);
+                    if (i4.x == v) { first &= i >= j; sum += p4.x; }
+                    if (i4.y == v) { first &= i + 1 >= j; sum += p4.y; }
+                    if (i4.z == v) { first &= i + 2 >= j; sum += p4.z; }
+                    if (i4.w == v) { first &= i + 3 >= j; sum += p4.w; }
+                }
+                if (first) dz[v] = from_f32<T>(g * (exp2_fast(fmaf(zt[j], a.inv_temperature, -lse) * kLog2e) - sum));
             }
-            if (first) dz[v] = from_f32<T>(g * (exp2_fast(fmaf(zt[j], a.inv_temperature, -lse) * kLog2e) - sum));
         }
     }
     if (cluster > 1 && PASS != kDistillBackward) cluster_sync_all();  // no CTA leaves while another may read its part
 }
 
-// CTAs that share a row: enough to fill the device with few rows (each at
-// least 16 KB of logits), and in the one-call form so many that the rows in
-// progress stay within 32 MB, well inside L2 beside the gradient's writes.
-int cluster_of(const DistillArgs& a, DistillPass pass, int64_t row_bytes, int64_t ctas) {
+// CTAs that share a row: enough to fill the device with few rows, each with
+// at least 16 KB of logits.
+int cluster_of(const DistillArgs& a, int64_t row_bytes, int64_t ctas) {
     int cluster = 1;
-    while (cluster < kMaxCluster && row_bytes >= cluster * 2 * 16384 &&
-           (a.rows * cluster * 2 <= ctas ||
-            (pass == kDistillLossGrad && std::min(a.rows, ctas / cluster) * row_bytes > (32 << 20))))
-        cluster *= 2;
+    while (cluster < kMaxCluster && row_bytes >= cluster * 2 * 16384 && a.rows * cluster * 2 <= ctas) cluster *= 2;
     return cluster;
 }
 
@@ -403,7 +381,7 @@ int launch_rows(const DistillArgs& a, DistillPass pass, int sm_count, cudaStream
     auto kernel = pass == kDistillForward    ? distill_kernel<T, kDistillForward, kBlock>
                   : pass == kDistillBackward ? distill_kernel<T, kDistillBackward, kBlock>
                                              : distill_kernel<T, kDistillLossGrad, kBlock>;
-    int cluster = cluster_of(a, pass, (int64_t)a.vocab * (int)sizeof(T), (int64_t)sm_count * (1536 / kBlock));
+    int cluster = cluster_of(a, (int64_t)a.vocab * (int)sizeof(T), (int64_t)sm_count * (1536 / kBlock));
     cudaLaunchConfig_t cfg{};
     cfg.blockDim = dim3(kBlock);
     cfg.stream = stream;

@@ -18,35 +18,79 @@ constexpr float kSqrtHalf = 0.70710678118654752f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kSqrt2OverPi = 0.79788456080286536f;
 constexpr float kCubic = 0.044715f;
+constexpr float kLog2e = 1.4426950408889634f;
 
-// 1 / (1 + exp(-x)); exp overflows to inf far left, where the result is 0.
-__device__ __forceinline__ float logistic(float x) { return 1.f / (1.f + expf(-x)); }
-
-__device__ __forceinline__ float activate(float z, int act) {
-    switch (act) {
-        case SOMA_ACT_RELU: return z < 0.f ? 0.f : z;  // NaN stays NaN
-        case SOMA_ACT_GELU: return 0.5f * z * (1.f + erff(z * kSqrtHalf));
-        // (1 + tanh u) / 2 is the logistic function of 2u
-        case SOMA_ACT_GELU_TANH: return z * logistic(2.f * kSqrt2OverPi * z * fmaf(kCubic * z, z, 1.f));
-        case SOMA_ACT_SILU: return z * logistic(z);
-        default: return z;
-    }
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float reciprocal_fast(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
-__device__ __forceinline__ float act_slope(float z, int act) {
+// 1 / (1 + exp(-x)); the exponential overflows to inf far left, where the result is 0.
+__device__ __forceinline__ float logistic(float x) { return reciprocal_fast(1.f + exp2_fast(-kLog2e * x)); }
+
+// The normal distribution's cdf and exp(-z^2 / 2), by Abramowitz and Stegun's
+// formula 7.1.26 for erf (absolute error below 1.5e-7): one exponential, one
+// reciprocal and a polynomial of degree 5, where the outputs have 8 or 11 bits.
+__device__ __forceinline__ float normal_cdf(float z, float& bell) {
+    const float x = fabsf(z) * kSqrtHalf;
+    const float t = reciprocal_fast(fmaf(0.3275911f, x, 1.f));
+    bell = exp2_fast(-kLog2e * x * x);
+    float q = fmaf(1.061405429f, t, -1.453152027f);
+    q = fmaf(q, t, 1.421413741f);
+    q = fmaf(q, t, -0.284496736f);
+    q = fmaf(q, t, 0.254829592f);
+    const float tail = 0.5f * q * t * bell;
+    return z > 0.f ? 1.f - tail : tail;
+}
+
+template <int kAct>
+__device__ __forceinline__ float activate(float z) {
+    if (kAct == SOMA_ACT_RELU) return z < 0.f ? 0.f : z;  // NaN stays NaN
+    if (kAct == SOMA_ACT_GELU) {
+        float bell;
+        return z * normal_cdf(z, bell);
+    }
+    // (1 + tanh u) / 2 is the logistic function of 2u
+    if (kAct == SOMA_ACT_GELU_TANH) return z * logistic(2.f * kSqrt2OverPi * z * fmaf(kCubic * z, z, 1.f));
+    if (kAct == SOMA_ACT_SILU) return z * logistic(z);
+    return z;
+}
+
+template <int kAct>
+__device__ __forceinline__ float act_slope(float z) {
+    if (kAct == SOMA_ACT_RELU) return z > 0.f ? 1.f : 0.f;
+    if (kAct == SOMA_ACT_GELU) {
+        float bell;
+        const float cdf = normal_cdf(z, bell);
+        return fmaf(z * kInvSqrt2Pi, bell, cdf);
+    }
+    if (kAct == SOMA_ACT_GELU_TANH) {
+        const float s = logistic(2.f * kSqrt2OverPi * z * fmaf(kCubic * z, z, 1.f));
+        const float du = 2.f * kSqrt2OverPi * fmaf(3.f * kCubic * z, z, 1.f);
+        return fmaf(z * s * (1.f - s), du, s);
+    }
+    if (kAct == SOMA_ACT_SILU) {
+        const float s = logistic(z);
+        return s * fmaf(z, 1.f - s, 1.f);
+    }
+    return 1.f;
+}
+
+// Calls f with the activation as a compile-time constant.
+template <typename F>
+__host__ __device__ __forceinline__ void with_act(int act, F&& f) {
     switch (act) {
-        case SOMA_ACT_RELU: return z > 0.f ? 1.f : 0.f;
-        case SOMA_ACT_GELU: return fmaf(z * kInvSqrt2Pi, expf(-0.5f * z * z), 0.5f * (1.f + erff(z * kSqrtHalf)));
-        case SOMA_ACT_GELU_TANH: {
-            const float s = logistic(2.f * kSqrt2OverPi * z * fmaf(kCubic * z, z, 1.f));
-            const float du = 2.f * kSqrt2OverPi * fmaf(3.f * kCubic * z, z, 1.f);
-            return fmaf(z * s * (1.f - s), du, s);
-        }
-        case SOMA_ACT_SILU: {
-            const float s = logistic(z);
-            return s * fmaf(z, 1.f - s, 1.f);
-        }
-        default: return 1.f;
+        case SOMA_ACT_RELU: f(std::integral_constant<int, SOMA_ACT_RELU>{}); break;
+        case SOMA_ACT_GELU: f(std::integral_constant<int, SOMA_ACT_GELU>{}); break;
+        case SOMA_ACT_GELU_TANH: f(std::integral_constant<int, SOMA_ACT_GELU_TANH>{}); break;
+        case SOMA_ACT_SILU: f(std::integral_constant<int, SOMA_ACT_SILU>{}); break;
+        default: f(std::integral_constant<int, SOMA_ACT_NONE>{}); break;
     }
 }
 
@@ -91,7 +135,7 @@ __device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
 
 // x += eight packed values.
 template <typename T>
-__device__ __forceinline__ void add8(float (&x)[8], const uint4& w) {
+__device__ __forceinline__ void add8(float* x, const uint4& w) {
     float2 t;
     t = unpack2<T>(w.x); x[0] += t.x; x[1] += t.y;
     t = unpack2<T>(w.y); x[2] += t.x; x[3] += t.y;
@@ -153,86 +197,96 @@ struct TileShape {
     static constexpr uint32_t kTmemCols = 2 * BN;
 };
 
-// One warp's 32 x 64 block: rows row0.., columns col0... `acc` is the block's
-// TMEM address; block is 4 KB of staging (128-byte rows, 16-byte pieces
-// swizzled by the row like the output's tensor map), bias 64 values.
+// Staging of a warp's output: two buffers of 32 rows x 32 columns, 64-byte
+// rows whose 16-byte pieces are swizzled like the output's tensor map, so
+// that one block's TMA store reads its buffer while the next fills the other.
 template <typename T>
-__device__ __forceinline__ void epilogue_block(const TileArgs& p, uint32_t acc, int row0, int col0, char* block,
-                                               T* bias) {
-    const int lane = threadIdx.x & 31;
-    const GemmArgs& g = p.g;
-    const int row = row0 + lane;
-    const bool has_row = row < g.m;
-    if (g.bias) {
-        const T* b = static_cast<const T*>(g.bias) + col0;
-        bias[lane] = col0 + lane < g.n ? b[lane] : from_f32<T>(0.f);
-        bias[lane + 32] = col0 + lane + 32 < g.n ? b[lane + 32] : from_f32<T>(0.f);
-    }
-    __syncwarp();
-    char* mine = block + lane * 128;
-    const int sw = lane & 7;
-    const T* res = g.residual ? static_cast<const T*>(g.residual) + (int64_t)row * g.residual_stride + col0 : nullptr;
-    const bool res_vec = g.residual && ((uintptr_t)g.residual % 16 == 0) && g.residual_stride % 8 == 0;
-    // pass 0 writes z, pass 1 writes out
-    for (int pass = g.z_out ? 0 : 1; pass < 2; ++pass) {
-        // the previous block's store has read the staging rows
-        if (lane == 0) tma_store_wait_read();
+struct Stager {
+    char* buffers;
+    int turn, row0, m, n;
+    // Packs this lane's row of 32 values and stores the block at (row0, col0).
+    __device__ __forceinline__ void store(const float (&x)[32], int col0, const CUtensorMap* map, bool tma, T* out,
+                                          int64_t stride) {
+        const int lane = threadIdx.x & 31;
+        char* block = buffers + turn * 2048;
+        turn ^= 1;
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the store before last
         __syncwarp();
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            uint32_t raw[32];
-            tmem_ld32(acc + half * 32, raw);
-            tmem_ld_wait(raw);
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                float x[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(raw[v * 8 + i]);
-                const int c = half * 32 + v * 8;
-                if (g.bias) {
-                    add8<T>(x, *reinterpret_cast<const uint4*>(bias + c));
-                }
-                if (pass == 1) {
-                    if (g.act != SOMA_ACT_NONE) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) x[i] = activate(x[i], g.act);
-                    }
-                    if (res && has_row) {
-                        if (res_vec && col0 + c + 8 <= g.n) {
-                            add8<T>(x, *reinterpret_cast<const uint4*>(res + c));
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                if (col0 + c + i < g.n) x[i] += to_f32(res[c + i]);
-                        }
-                    }
-                }
-                uint4 w;
-                w.x = pack2<T>(x[0], x[1]);
-                w.y = pack2<T>(x[2], x[3]);
-                w.z = pack2<T>(x[4], x[5]);
-                w.w = pack2<T>(x[6], x[7]);
-                *reinterpret_cast<uint4*>(mine + (((half * 4 + v) ^ sw) << 4)) = w;
-            }
+        for (int v = 0; v < 4; ++v) {
+            uint4 w;
+            w.x = pack2<T>(x[8 * v], x[8 * v + 1]);
+            w.y = pack2<T>(x[8 * v + 2], x[8 * v + 3]);
+            w.z = pack2<T>(x[8 * v + 4], x[8 * v + 5]);
+            w.w = pack2<T>(x[8 * v + 6], x[8 * v + 7]);
+            *reinterpret_cast<uint4*>(block + lane * 64 + ((v ^ ((lane >> 1) & 3)) << 4)) = w;
         }
-        if (pass == 0 ? p.tma_z : p.tma_out) {
+        if (tma) {
             fence_to_async();
             __syncwarp();
-            if (lane == 0) tma_store(pass == 0 ? &p.z : &p.out, smem_addr(block), col0, row0);
+            if (lane == 0) tma_store(map, smem_addr(block), col0, row0);
         } else {
             __syncwarp();
-            T* out = static_cast<T*>(pass == 0 ? g.z_out : g.out);
-            const int64_t stride = pass == 0 ? g.z_stride : g.out_stride;
-            for (int r = 0; r < 32 && row0 + r < g.m; ++r) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int c = h * 32 + lane;
-                    const T v = *reinterpret_cast<const T*>(block + r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2);
-                    if (col0 + c < g.n) out[(row0 + r) * stride + col0 + c] = v;
-                }
+            if (col0 + lane < n) {
+#pragma unroll 4
+                for (int r = 0; r < 32 && row0 + r < m; ++r)
+                    out[(row0 + r) * stride + col0 + lane] = *reinterpret_cast<const T*>(
+                        block + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
             }
+        }
+    }
+};
+
+// One warp's 32 rows x `cols` columns (a multiple of 32) at (row0, col0):
+// out of TMEM at `acc`, through the epilogue, into out (and z_out).
+template <typename T>
+__device__ __forceinline__ void epilogue(const TileArgs& p, uint32_t acc, int row0, int col0, int cols, Stager<T>& stager,
+                                         T* bias) {
+    const int lane = threadIdx.x & 31;
+    const GemmArgs& g = p.g;
+    const bool has_row = row0 + lane < g.m;
+    const T* res =
+        g.residual && has_row ? static_cast<const T*>(g.residual) + (int64_t)(row0 + lane) * g.residual_stride : nullptr;
+    const bool res_vec = ((uintptr_t)g.residual % 16 == 0) && g.residual_stride % 8 == 0;
+    stager.row0 = row0;
+    for (int c0 = 0; c0 < cols && col0 + c0 < g.n; c0 += 32) {
+        const int col = col0 + c0;
+        uint32_t raw[32];
+        tmem_ld32(acc + c0, raw);
+        uint4 r4[4] = {};
+        const bool whole = res && res_vec && col + 32 <= g.n;
+        if (whole) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) r4[v] = *reinterpret_cast<const uint4*>(res + col + 8 * v);
+        }
+        if (g.bias) {
+            __syncwarp();
+            bias[lane] = col + lane < g.n ? static_cast<const T*>(g.bias)[col + lane] : from_f32<T>(0.f);
             __syncwarp();
         }
+        tmem_ld_wait(raw);
+        float x[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(raw[i]);
+        if (g.bias) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) add8<T>(x + 8 * v, *reinterpret_cast<const uint4*>(bias + 8 * v));
+        }
+        if (g.z_out) stager.store(x, col, &p.z, p.tma_z, static_cast<T*>(g.z_out), g.z_stride);
+        if (g.act != SOMA_ACT_NONE)
+            with_act(g.act, [&](auto act) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = activate<decltype(act)::value>(x[i]);
+            });
+        if (whole) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) add8<T>(x + 8 * v, r4[v]);
+        } else if (res) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (col + i < g.n) x[i] += to_f32(res[col + i]);
+        }
+        stager.store(x, col, &p.out, p.tma_out, static_cast<T*>(g.out), g.out_stride);
     }
 }
 
@@ -333,7 +387,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
             if (i == 0) acc_parity ^= 1;
         }
     } else if (warp < kEpilogueWarps) {
-        char* block = staging + warp * (32 * 128);
+        Stager<T> stager{staging + warp * (32 * 128), 0, 0, g.m, g.n};
         T* bias = reinterpret_cast<T*>(staging + kEpilogueWarps * (32 * 128)) + warp * 64;
         const int quarter = warp & 3, half = warp >> 2;
         int i = 0;
@@ -344,10 +398,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
             if (!mbar_wait(acc_full(i), parity, &gave_up)) break;
             __syncwarp();
             tcgen05_after_sync();
-            for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 64)
-                if (row0 + quarter * 32 < g.m && col0 + c < g.n)
-                    epilogue_block<T>(p, tmem + i * BN + c + ((uint32_t)(quarter * 32) << 16), row0 + quarter * 32,
-                                      col0 + c, block, bias);
+            if (row0 + quarter * 32 < g.m)
+                epilogue<T>(p, tmem + i * BN + half * (BN / 2) + ((uint32_t)(quarter * 32) << 16), row0 + quarter * 32,
+                            col0 + half * (BN / 2), BN / 2, stager, bias);
             tcgen05_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(CG == 2 ? cluster_map(acc_empty(i), 0) : acc_empty(i));
@@ -497,7 +550,8 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
             for (int r = 0; r < splits; ++r) z += exchange[(r * share + c) * kBM + warp * 32 + lane];
             z += bias;
             if (g.z_out) static_cast<T*>(g.z_out)[m * g.z_stride + n] = from_f32<T>(z);
-            float y = activate(z, g.act);
+            float y = z;
+            with_act(g.act, [&](auto act) { y = activate<decltype(act)::value>(z); });
             if (g.residual) y += to_f32(static_cast<const T*>(g.residual)[m * g.residual_stride + n]);
             static_cast<T*>(g.out)[m * g.out_stride + n] = from_f32<T>(y);
         }
@@ -532,16 +586,18 @@ bool aligned_rows(const void* p, int64_t stride, int64_t rows) {
     return (uintptr_t)p % 16 == 0 && (rows <= 1 || stride % 8 == 0);
 }
 
-// Tensor map of a 16-bit matrix with boxes of box_rows x 64 columns.
-int make_map(CUtensorMap* map, int dtype, const void* p, int64_t stride, int64_t rows, int64_t cols, int box_rows) {
+// Tensor map of a 16-bit matrix with boxes of box_rows rows x 64 or 32
+// columns, swizzled over the box's 128- or 64-byte rows.
+int make_map(CUtensorMap* map, int dtype, const void* p, int64_t stride, int64_t rows, int64_t cols, int box_rows,
+             int box_cols = 64) {
     const EncodeTiled fn = encode_tiled();
     if (!fn) return cudaErrorNotSupported;
     if (rows <= 1) stride = (cols + 7) / 8 * 8;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, steps[2] = {1, 1};
+    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, steps[2] = {1, 1};
     const CUresult r = fn(map, dtype == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
                           const_cast<void*>(p), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -579,8 +635,8 @@ int launch_tile(TileArgs& p, int sm_count, void* stream) {
         return e;
     p.tma_out = aligned_rows(g.out, g.out_stride, g.m);
     p.tma_z = g.z_out && aligned_rows(g.z_out, g.z_stride, g.m);
-    if (p.tma_out && (e = make_map(&p.out, g.dtype, g.out, g.out_stride, g.m, g.n, 32))) return e;
-    if (p.tma_z && (e = make_map(&p.z, g.dtype, g.z_out, g.z_stride, g.m, g.n, 32))) return e;
+    if (p.tma_out && (e = make_map(&p.out, g.dtype, g.out, g.out_stride, g.m, g.n, 32, 32))) return e;
+    if (p.tma_z && (e = make_map(&p.z, g.dtype, g.z_out, g.z_stride, g.m, g.n, 32, 32))) return e;
     p.tiles_m = (g.m + kBM * CG - 1) / (kBM * CG);
     p.tiles_n = (g.n + BN - 1) / BN;
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
@@ -605,32 +661,87 @@ int launch_few(TileArgs& p, int sm_count, void* stream) {
     return launch((const void*)few_kernel<BN, T>, args, tiles * splits, kFewThreads, S::kSmem, splits, stream);
 }
 
-constexpr int kBlock = 256;
+// ---- the activation's backward pass -------------------------------------------
 
-template <typename T>
-__global__ void __launch_bounds__(kBlock) act_bwd_kernel(const __grid_constant__ ActBwdArgs a, int parts) {
-    const int c = blockIdx.x * kBlock + threadIdx.x;
-    if (c >= a.cols) return;
-    float db = 0.f;
-    for (int64_t r = blockIdx.y; r < a.rows; r += parts) {
-        float g = to_f32(static_cast<const T*>(a.dy)[r * a.dy_stride + c]);
-        if (a.act != SOMA_ACT_NONE) g *= act_slope(to_f32(static_cast<const T*>(a.z)[r * a.z_stride + c]), a.act);
-        if (a.dz) static_cast<T*>(a.dz)[r * a.dz_stride + c] = from_f32<T>(g);
-        db += g;
+// A warp takes 256 columns, a vector of 8 per lane; the CTA's warps, and the
+// CTAs of a column block, take rows in turn.  dz is rounded and stored, the
+// column sums of the unrounded dz stay in registers and end as one partial
+// row per CTA.  Reads dy and z, writes dz: HBM (or L2) bound.
+constexpr int kActWarps = 8, kActCols = 256;
+
+template <typename T, int kAct>
+__global__ void __launch_bounds__(32 * kActWarps) act_bwd_kernel(const __grid_constant__ ActBwdArgs a) {
+    __shared__ float sums[kActWarps][kActCols];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int i = blockIdx.x * 32 + lane, c0 = i * 8;  // this lane's vector
+    const int64_t step = (int64_t)gridDim.y * kActWarps;
+    float db[8] = {};
+    auto fetch = [&](const void* base, int64_t stride, int64_t r, float (&x)[8]) {
+        const RowReader<T, false> row(static_cast<const T*>(base), stride, a.rows, r, a.cols);
+        if (i >= row.inner_begin && i < row.inner_end) {
+            uint4 u[1], v[1];
+            if (row.phase) {
+                row.template load<true, 1>(i, 0, u, v);
+                row.template widen<true>(u[0], v[0], x);
+            } else {
+                row.template load<false, 1>(i, 0, u, v);
+                row.template widen<false>(u[0], v[0], x);
+            }
+        } else {
+            row.gather(i, x, 0.f);
+        }
+    };
+    for (int64_t r = (int64_t)blockIdx.y * kActWarps + warp; r < a.rows; r += step) {
+        float g[8], z[8];
+        fetch(a.dy, a.dy_stride, r, g);
+        if (kAct != SOMA_ACT_NONE) {
+            fetch(a.z, a.z_stride, r, z);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) g[q] *= act_slope<kAct>(z[q]);
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (c0 + q < a.cols) db[q] += g[q];
+        // (dz's rows are padded to whole vectors)
+        if (a.dz && c0 < a.cols) *reinterpret_cast<uint4*>(static_cast<T*>(a.dz) + r * a.dz_stride + c0) = narrow16(g, T{});
     }
-    if (a.dbias) a.partials[(int64_t)blockIdx.y * a.cols + c] = db;
+    if (!a.dbias) return;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) sums[warp][lane * 8 + q] = db[q];
+    __syncthreads();
+    const int c = blockIdx.x * kActCols + threadIdx.x;
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kActWarps; ++w) s += sums[w][threadIdx.x];
+    if (c < a.cols) a.partials[(int64_t)blockIdx.y * a.cols + c] = s;
 }
 
+// dbias: the partial rows added in a fixed order, 32 columns per CTA.
 template <typename T>
-__global__ void __launch_bounds__(kBlock) bias_grad_kernel(const __grid_constant__ ActBwdArgs a, int parts) {
-    const int c = blockIdx.x * kBlock + threadIdx.x;
-    if (c >= a.cols) return;
+__global__ void __launch_bounds__(32 * kActWarps) bias_grad_kernel(const __grid_constant__ ActBwdArgs a, int parts) {
+    __shared__ float scratch[kActWarps][32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float db = 0.f;
-    for (int p = 0; p < parts; ++p) db += a.partials[(int64_t)p * a.cols + c];
-    static_cast<T*>(a.dbias)[c] = from_f32<T>(db);
+    if (c < a.cols) {
+#pragma unroll 4
+        for (int p = warp; p < parts; p += kActWarps) db += a.partials[(int64_t)p * a.cols + c];
+    }
+    scratch[warp][lane] = db;
+    __syncthreads();
+    if (warp || c >= a.cols) return;
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kActWarps; ++w) s += scratch[w][lane];
+    static_cast<T*>(a.dbias)[c] = from_f32<T>(s);
 }
 
-int row_parts(int64_t rows) { return (int)(rows < 64 ? (rows > 0 ? rows : 1) : 64); }
+// CTAs of a column block: about six CTAs per SM in all, eight rows each at least.
+int row_parts(int64_t rows, int64_t cols, int sm_count) {
+    const int64_t blocks = (cols + kActCols - 1) / kActCols, by_rows = (rows + kActWarps - 1) / kActWarps;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(by_rows, 6 * (int64_t)sm_count / blocks));
+}
 
 template <typename F>
 int with_type16(int dtype, F&& f) {
@@ -676,15 +787,30 @@ int take_linear_gave_up(int* value) {
     return e;
 }
 
-int64_t act_bwd_workspace(int64_t rows, int64_t cols, int) { return (int64_t)row_parts(rows) * cols * 4; }
+int64_t act_bwd_workspace(int64_t rows, int64_t cols, int sm_count) {
+    return (int64_t)row_parts(rows, cols, sm_count) * cols * 4;
+}
 
-int launch_act_bwd(const ActBwdArgs& a, int, void* stream) {
+int launch_act_bwd(const ActBwdArgs& a, int sm_count, void* stream) {
     return with_type16(a.dtype, [&](auto t) {
         using T = decltype(t);
-        const int cblocks = (a.cols + kBlock - 1) / kBlock, parts = row_parts(a.rows);
-        act_bwd_kernel<T><<<dim3(cblocks, parts), kBlock, 0, (cudaStream_t)stream>>>(a, parts);
-        if (a.dbias) bias_grad_kernel<T><<<cblocks, kBlock, 0, (cudaStream_t)stream>>>(a, parts);
-        return (int)cudaGetLastError();
+        const int blocks = (a.cols + kActCols - 1) / kActCols, parts = row_parts(a.rows, a.cols, sm_count);
+        cudaStream_t st = (cudaStream_t)stream;
+        with_act(a.act, [&](auto act) {
+            act_bwd_kernel<T, decltype(act)::value><<<dim3(blocks, parts), 32 * kActWarps, 0, st>>>(a);
+        });
+        int e = (int)cudaGetLastError();
+        if (e != cudaSuccess || !a.dbias) return e;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((a.cols + 31) / 32);
+        cfg.blockDim = dim3(32 * kActWarps);
+        cfg.stream = st;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return (int)cudaLaunchKernelEx(&cfg, bias_grad_kernel<T>, a, parts);
     });
 }
 

@@ -4,6 +4,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <math.h>
 
 #include <cstdint>
 
@@ -149,6 +150,58 @@ __device__ __forceinline__ void store_vector(T* row, int64_t c, int64_t cols, in
             if (c + i < cols && (i < head ? !joined : !joins)) row[c + i] = from_f32<T>(x[i]);
     }
 }
+
+// A row as vectors of kVec elements, vector i from element kVec i
+// on, wherever the row starts: where that is inside a 16-byte word, a vector
+// is shifted out of two words.
+template <typename T, bool kKeep>
+struct RowReader {
+    static constexpr int kVec = 16 / sizeof(T);
+    const T* row;
+    const uint4* words;  // the word that holds the row's first element
+    int phase, cols;
+    // Vectors [inner_begin, inner_end) are whole and lie in words inside the
+    // matrix, whose first and last rows may end inside a word.
+    int inner_begin, inner_end;
+
+    __device__ __forceinline__ RowReader(const T* base, int64_t stride, int64_t rows, int64_t r, int n)
+        : row(base + r * stride), phase((int)((uintptr_t)row & 15)), cols(n) {
+        words = reinterpret_cast<const uint4*>((uintptr_t)row & ~(uintptr_t)15);
+        inner_begin = (uintptr_t)words < (uintptr_t)base ? 1 : 0;
+        const uintptr_t end = (uintptr_t)(base + (rows - 1) * stride + cols) & ~(uintptr_t)15;
+        // vector i takes bytes up to 16 (i + 1), or 16 (i + 2) when shifted
+        const int64_t fit = ((int64_t)(end - (uintptr_t)words) >> 4) - (phase ? 1 : 0);
+        inner_end = (int)min(fit < 0 ? (int64_t)0 : fit, (int64_t)(cols / kVec));
+    }
+    // One vector anywhere in the row; elements past the row's end are `missing`.
+    __device__ __forceinline__ void gather(int i, float (&x)[kVec], float missing = -INFINITY) const {
+#pragma unroll
+        for (int q = 0; q < kVec; ++q) x[q] = kVec * i + q < cols ? to_f32(row[kVec * i + q]) : missing;
+    }
+    // Vectors [i, i + n step) of whole words, step apart.
+    template <bool kShift, int kN>
+    __device__ __forceinline__ void load(int i, int step, uint4 (&u)[kN], uint4 (&v)[kShift ? kN : 1]) const {
+#pragma unroll
+        for (int q = 0; q < kN; ++q) {
+            const uint4* w = words + i + q * step;
+            if (kShift) {  // the neighbouring vector's word comes out of L1
+                u[q] = w[0];
+                v[kShift ? q : 0] = w[1];
+            } else if (kKeep) {  // read again, from L2
+                asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(u[q].x), "=r"(u[q].y), "=r"(u[q].z), "=r"(u[q].w)
+                             : "l"(w)
+                             : "memory");
+            } else {
+                u[q] = __ldcs(w);
+            }
+        }
+    }
+    template <bool kShift>
+    __device__ __forceinline__ void widen(const uint4& u, const uint4& v, float (&x)[kVec]) const {
+        widen16(kShift ? shifted<T>(u, v, phase) : u, x, T{});
+    }
+};
 
 // Calls f with a value of the C++ type that a dtype code stands for.
 template <typename F>
