@@ -16,6 +16,7 @@
 
 #include <algorithm>
 
+#include "mbarrier.cuh"
 #include "ops_device.cuh"
 #include "ops_kernels.h"
 #include "soma_ops.h"
@@ -368,6 +369,373 @@ __global__ void __launch_bounds__(kBlock, 1536 / kBlock) distill_kernel(const __
     if (cluster > 1 && PASS != kDistillBackward) cluster_sync_all();  // no CTA leaves while another may read its part
 }
 
+// ---- many rows: a persistent CTA per SM -----------------------------------------
+//
+// A row passes through a ring of chunks in shared memory, filled by bulk
+// copies.  For loss and gradient together, the last chunks of the row stay in
+// the ring from the first pass (maximum and sum) to the second (gradient), so
+// that a row that fits is read once, from HBM; of a longer one, the first
+// chunks are copied again, from L2.  Each chunk that the second pass frees is
+// refilled at once, with the next row's: the copies never pause.  Sixteen
+// warps compute, one fills the ring, four work on the teacher's entries.
+
+constexpr int kRingBlock = 512;                 // computing threads
+constexpr int kTeachers = 128;
+constexpr int kRingThreads = kRingBlock + 32 + kTeachers;
+constexpr int kChunkVecs = 1024;                // two vectors per computing thread
+constexpr int kSlotBytes = kChunkVecs * 16 + 32;
+constexpr int kSlots = 12;
+
+__device__ int g_gave_up;  // a bounded wait ran out on this device
+
+struct RingShared {
+    uint64_t full[kSlots], empty[kSlots], taught, normalized, done;
+    float2 warp_part[2][kRingBlock / 32];
+    float lse;
+    int any, gave_up;
+    __align__(16) float p[SOMA_DISTILL_MAX_TOP];
+    __align__(16) int at[SOMA_DISTILL_MAX_TOP];
+};
+
+// Chunk c of row r in memory.  The first and last words of the matrix's own
+// span may not be whole: those are left out of the copy and patched.
+template <typename T>
+struct Chunks {
+    static constexpr int kVec = 16 / sizeof(T), kCols = kChunkVecs * kVec;
+    const T* base;
+    int64_t stride, rows;
+    int cols, count;
+    __device__ __forceinline__ const T* first(int64_t r, int c) const { return base + r * stride + (int64_t)c * kCols; }
+    __device__ __forceinline__ int size(int c) const { return min(kCols, cols - c * kCols); }
+    __device__ __forceinline__ bool cut(int64_t r, int c) const {
+        const uintptr_t s = (uintptr_t)first(r, c), e = s + (uintptr_t)size(c) * sizeof(T);
+        return (s & ~(uintptr_t)15) < (uintptr_t)base ||
+               ((e + 15) & ~(uintptr_t)15) > (uintptr_t)(base + (rows - 1) * stride + cols);
+    }
+    __device__ __forceinline__ void copy(int64_t r, int c, uint32_t slot, uint32_t bar) const {
+        const uintptr_t s = (uintptr_t)first(r, c), e = s + (uintptr_t)size(c) * sizeof(T), a = s & ~(uintptr_t)15;
+        uintptr_t lo = a, hi = (e + 15) & ~(uintptr_t)15;
+        if (lo < (uintptr_t)base) lo += 16;
+        if (hi > (uintptr_t)(base + (rows - 1) * stride + cols)) hi -= 16;
+        const uint32_t bytes = hi > lo ? (uint32_t)(hi - lo) : 0;
+        mbar_expect(bar, bytes);
+        if (bytes) bulk_load(slot + (uint32_t)(lo - a), reinterpret_cast<const void*>(lo), bytes, bar);
+    }
+    // The elements of the chunk's first and last word, one by one.
+    __device__ __forceinline__ void patch(int64_t r, int c, char* slot, int t) const {
+        const T* from = first(r, c);
+        T* to = reinterpret_cast<T*>(slot + ((uintptr_t)from & 15));
+        const int n = size(c);
+        if (t >= 2 * kVec) return;
+        const int i = t < kVec ? t : n - 1 - (t - kVec);
+        if (i >= 0 && i < n) to[i] = from[i];
+    }
+};
+
+template <typename T, int PASS>
+__global__ void __launch_bounds__(kRingThreads) distill_ring_kernel(const __grid_constant__ DistillArgs a) {
+    constexpr int kVec = 16 / sizeof(T), kWarps = kRingBlock / 32, kPasses = kChunkVecs / kRingBlock;
+    constexpr bool kBoth = PASS == kDistillLossGrad;
+    extern __shared__ __align__(128) char dynamic[];
+    RingShared& sh = *reinterpret_cast<RingShared*>(dynamic + kSlots * kSlotBytes);
+    const int t = threadIdx.x, lane = t & 31;
+    const Chunks<T> z{static_cast<const T*>(a.logits), a.logits_stride, a.rows, a.vocab,
+                      (a.vocab + kChunkVecs * kVec - 1) / (kChunkVecs * kVec)};
+    // chunks that do not stay in the ring until the second pass
+    const int spilled = kBoth ? max(0, z.count - kSlots) : 0;
+    const uint32_t full = smem_addr(sh.full), empty = smem_addr(sh.empty);
+    const uint32_t taught = smem_addr(&sh.taught), normalized = smem_addr(&sh.normalized), done = smem_addr(&sh.done);
+    if (t == 0) {
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, kWarps);
+        }
+        mbar_init(taught, kTeachers);
+        mbar_init(normalized, 1);
+        mbar_init(done, kWarps);
+        mbar_init_fence();
+        sh.gave_up = 0;
+    }
+    __syncthreads();
+    auto scale_of = [&](int64_t r) {
+        const float w = a.row_weight ? a.row_weight[r] : 1.f;
+        return kBoth ? w : a.grad_loss[r] * w;
+    };
+
+    if (t >= kRingBlock && t < kRingBlock + 32) {  // fills the ring
+        if (lane == 0) {
+            int slot = 0;
+            uint32_t parity = 1;  // a fresh barrier's previous phase counts as done
+            float next = blockIdx.x < a.rows ? scale_of(blockIdx.x) : 0.f;
+            for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+                const float scale = next;
+                if (r + gridDim.x < a.rows) next = scale_of(r + gridDim.x);
+                if (scale == 0.f) continue;
+                for (int j = 0; j < z.count + spilled; ++j) {
+                    mbar_wait(empty + 8 * slot, parity, &sh.gave_up);
+                    z.copy(r, j < z.count ? j : j - z.count, smem_addr(dynamic + slot * kSlotBytes), full + 8 * slot);
+                    if (++slot == kSlots) {
+                        slot = 0;
+                        parity ^= 1;
+                    }
+                }
+            }
+        }
+    } else if (t >= kRingBlock + 32) {  // the teacher's entries
+        const int u = t - kRingBlock - 32;
+        uint32_t parity = 0;
+        auto sync = [] { asm volatile("bar.sync 2, %0;" ::"n"(kTeachers) : "memory"); };
+        constexpr int kMine = SOMA_DISTILL_MAX_TOP / kTeachers;
+        for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+            const float w = a.row_weight ? a.row_weight[r] : 1.f, scale = scale_of(r);
+            if (scale == 0.f) {
+                if (kBoth && u == 0) {
+                    a.loss[r] = 0.f;
+                    if (a.lse) a.lse[r] = 0.f;
+                }
+                continue;
+            }
+            const T* row = z.first(r, 0);
+            float zt[kMine];  // the student's logits at this thread's entries
+            bool any = false;
+#pragma unroll
+            for (int q = 0; q < kMine; ++q) {
+                const int j = q * kTeachers + u;
+                if (j >= (a.top + 3) / 4 * 4) break;
+                int64_t i = -1;
+                if (j < a.top)
+                    i = a.index_type == SOMA_INDEX_I64 ? static_cast<const int64_t*>(a.index)[r * a.index_stride + j]
+                                                       : static_cast<const int32_t*>(a.index)[r * a.index_stride + j];
+                const bool ok = i >= 0 && i < a.vocab;
+                float x = -INFINITY;
+                zt[q] = 0.f;
+                if (ok) {
+                    x = a.teacher_dtype == kF32    ? teacher_at<float>(a, r, j)
+                        : a.teacher_dtype == kBF16 ? teacher_at<__nv_bfloat16>(a, r, j)
+                                                   : teacher_at<__half>(a, r, j);
+                    zt[q] = to_f32(row[i]);
+                }
+                sh.at[j] = ok ? (int)i : -1;
+                sh.p[j] = x;
+                any |= x != -INFINITY;
+            }
+            if (u == 0) sh.any = 0;
+            sync();
+            if (any) sh.any = 1;
+            sync();
+            any = sh.any != 0;
+            // every warp forms the same statistics; each thread then its own entries' p
+            float top = -INFINITY, total = 0.f;
+            for (int j = lane; j < a.top; j += 32) top = larger(top, sh.p[j]);
+            top = warp_max(top);
+            for (int j = lane; j < a.top; j += 32)
+                if (sh.p[j] != -INFINITY) total += expf((sh.p[j] - top) * a.inv_temperature);
+            total = warp_sum(total);
+            const float log_total = logf(total);
+            sync();
+            float logp[kMine], p[kMine];
+#pragma unroll
+            for (int q = 0; q < kMine; ++q) {
+                const int j = q * kTeachers + u;
+                if (j >= a.top) break;
+                logp[q] = (sh.p[j] - top) * a.inv_temperature - log_total;
+                p[q] = any && sh.at[j] >= 0 ? expf(logp[q]) : 0.f;
+                sh.p[j] = p[q];
+            }
+            sync();
+            mbar_arrive(taught);  // zt is read and sh.any is set: the gradient may be written
+            float sums[kMine];
+            unsigned firsts = 0;
+#pragma unroll
+            for (int q = 0; q < kMine; ++q) {
+                const int j = q * kTeachers + u;
+                if (j >= a.top) break;
+                const int v = sh.at[j];
+                float sum = 0.f;
+                bool first = v >= 0;
+                for (int i = 0; i < a.top; i += 4) {  // (entries past top are at -1)
+                    const int4 i4 = *reinterpret_cast<const int4*>(sh.at + i);
+                    const float4 p4 = *reinterpret_cast<const float4*>(sh.p + i);
+                    if (i4.x == v) { first &= i >= j; sum += p4.x; }
+                    if (i4.y == v) { first &= i + 1 >= j; sum += p4.y; }
+                    if (i4.z == v) { first &= i + 2 >= j; sum += p4.z; }
+                    if (i4.w == v) { first &= i + 3 >= j; sum += p4.w; }
+                }
+                sums[q] = sum;
+                firsts |= (unsigned)first << q;
+            }
+            float lse;
+            if (kBoth) {
+                mbar_wait(normalized, parity, &sh.gave_up);
+                lse = sh.lse;
+                float loss = 0.f;
+#pragma unroll
+                for (int q = 0; q < kMine; ++q)
+                    if (q * kTeachers + u < a.top && p[q] != 0.f) loss += p[q] * (logp[q] - fmaf(zt[q], a.inv_temperature, -lse));
+                loss = warp_sum(loss);
+                sync();  // sh.p has been read by all
+                if (lane == 0) sh.p[u >> 5] = loss;
+                sync();
+                if (u == 0) {
+                    loss = (sh.p[0] + sh.p[1]) + (sh.p[2] + sh.p[3]);
+                    a.loss[r] = any ? w * a.temperature * a.temperature * loss : 0.f;
+                    if (a.lse) a.lse[r] = lse;
+                }
+            } else {
+                lse = a.lse_in[r];
+            }
+            mbar_wait(done, parity, &sh.gave_up);
+            T* dz = static_cast<T*>(a.dlogits) + r * a.dlogits_stride;
+            const float g = scale * a.temperature;
+#pragma unroll
+            for (int q = 0; q < kMine; ++q)
+                if (any && (firsts >> q & 1))
+                    dz[sh.at[q * kTeachers + u]] =
+                        from_f32<T>(g * (exp2_fast(fmaf(zt[q], a.inv_temperature, -lse) * kLog2e) - sums[q]));
+            sync();  // sh.at has been read by all
+            parity ^= 1;
+        }
+    } else {
+        const float c = a.inv_temperature * kLog2e;
+        const int warp = t >> 5;
+        int slot = 0, turn = 0;
+        uint32_t parity = 0, row_parity = 0;
+        auto advance = [&] {
+            if (++slot == kSlots) {
+                slot = 0;
+                parity ^= 1;
+            }
+        };
+        auto release = [&](int s) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty + 8 * s);
+        };
+        float next = blockIdx.x < a.rows ? scale_of(blockIdx.x) : 0.f;
+        float next_lse = !kBoth && blockIdx.x < a.rows ? a.lse_in[blockIdx.x] : 0.f;
+        for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+            const float scale = next;
+            float lse = next_lse;
+            if (r + gridDim.x < a.rows) {
+                next = scale_of(r + gridDim.x);
+                if (!kBoth) next_lse = a.lse_in[r + gridDim.x];
+            }
+            T* dz = static_cast<T*>(a.dlogits) + r * a.dlogits_stride;
+            if (scale == 0.f) {
+                stream_zeros<T, kRingBlock>(dz, 0, (a.vocab + kVec - 1) / kVec, a.vocab);
+                continue;
+            }
+            const int phase = (int)((uintptr_t)z.first(r, 0) & 15), out_phase = (int)((uintptr_t)dz & 15);
+            auto arrived = [&](int j) {  // chunk j is in the current slot
+                mbar_wait(full + 8 * slot, parity, &sh.gave_up);
+                if (z.cut(r, j)) {
+                    z.patch(r, j, dynamic + slot * kSlotBytes, t);
+                    fence_to_async();  // (before a later copy into the slot)
+                    asm volatile("bar.sync 1, %0;" ::"n"(kRingBlock) : "memory");
+                }
+            };
+            auto vector = [&](int s, int i, int n, float (&x)[kVec]) {  // vector i of a chunk of n elements
+                const char* at = dynamic + s * kSlotBytes + i * 16;
+                const uint4 u0 = *reinterpret_cast<const uint4*>(at);
+                widen16(phase ? shifted<T>(u0, *reinterpret_cast<const uint4*>(at + 16), phase) : u0, x, T{});
+                if (kVec * (i + 1) > n) {
+#pragma unroll
+                    for (int q = 0; q < kVec; ++q)
+                        if (kVec * i + q >= n) x[q] = -INFINITY;
+                }
+            };
+            const int first_slot = slot;
+            if (kBoth) {
+                MaxSum mine{kLowest, 0.f};
+                for (int j = 0; j < z.count; ++j) {
+                    arrived(j);
+                    const int n = z.size(j);
+#pragma unroll
+                    for (int q = 0; q < kPasses; ++q) {
+                        float x[kVec];
+                        if ((t + q * kRingBlock) * kVec < n) {
+                            vector(slot, t + q * kRingBlock, n, x);
+                            take<T>(mine, x, c);
+                        }
+                    }
+                    if (j < spilled) release(slot);
+                    advance();
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+                    mine = join(mine, {__shfl_xor_sync(0xffffffffu, mine.m, o), __shfl_xor_sync(0xffffffffu, mine.s, o)}, c);
+                if (lane == 0) sh.warp_part[turn][warp] = make_float2(mine.m, mine.s);
+                asm volatile("bar.sync 1, %0;" ::"n"(kRingBlock) : "memory");
+                const float2 part = sh.warp_part[turn][lane % kWarps];
+                turn ^= 1;
+                mine = {part.x, part.y};
+#pragma unroll
+                for (int o = kWarps / 2; o > 0; o >>= 1)
+                    mine = join(mine, {__shfl_xor_sync(0xffffffffu, mine.m, o), __shfl_xor_sync(0xffffffffu, mine.s, o)}, c);
+                lse = fmaf(mine.m, a.inv_temperature, logf(mine.s));
+            }
+            // the teachers are done with the row before, and have read what the gradient may replace
+            mbar_wait(taught, row_parity, &sh.gave_up);
+            if (kBoth && t == 0) {
+                sh.lse = lse;
+                mbar_arrive(normalized);
+            }
+            const float g = sh.any ? scale * a.temperature : 0.f;
+            auto gradient = [&](int s, int j) {  // of chunk j in slot s
+                const int n = z.size(j);
+                T* out = dz + (int64_t)j * Chunks<T>::kCols;
+#pragma unroll
+                for (int q = 0; q < kPasses; ++q) {
+                    const int i = t + q * kRingBlock, whole = (t & ~31) + q * kRingBlock;
+                    if (whole * kVec >= n) break;  // (all lanes of a warp store together)
+                    float x[kVec];
+                    if (i * kVec < n) vector(s, i, n, x);
+                    else
+#pragma unroll
+                        for (int k = 0; k < kVec; ++k) x[k] = -INFINITY;
+                    scaled_softmax<T>(x, a.inv_temperature, lse, g);
+                    if (g == 0.f) {
+#pragma unroll
+                        for (int k = 0; k < kVec; ++k) x[k] = 0.f;
+                    }
+                    if (out_phase == 0 && kVec * (i + 1) <= n) __stcs(reinterpret_cast<uint4*>(out) + i, narrow16(x, T{}));
+                    else store_vector<T, false>(out, (int64_t)kVec * i, n, out_phase, x);
+                }
+                release(s);
+            };
+            if (kBoth) {
+                // the chunks that stayed, then those copied again
+                int s = (first_slot + spilled) % kSlots;
+                for (int j = spilled; j < z.count; ++j) {
+                    gradient(s, j);
+                    if (++s == kSlots) s = 0;
+                }
+            }
+            for (int j = 0; j < (kBoth ? spilled : z.count); ++j) {
+                arrived(j);
+                gradient(slot, j);
+                advance();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(done);
+            row_parity ^= 1;
+        }
+    }
+    if (sh.gave_up) {
+        g_gave_up = 1;
+        outlast_copies();
+    }
+}
+
+template <typename T>
+int launch_ring(const DistillArgs& a, DistillPass pass, int sm_count, cudaStream_t stream) {
+    auto kernel = pass == kDistillBackward ? distill_ring_kernel<T, kDistillBackward> : distill_ring_kernel<T, kDistillLossGrad>;
+    const int smem = kSlots * kSlotBytes + (int)sizeof(RingShared);
+    const int e = allow_smem((const void*)kernel, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)std::min<int64_t>(a.rows, sm_count), kRingThreads, smem, stream>>>(a);
+    return (int)cudaGetLastError();
+}
+
 // CTAs that share a row: enough to fill the device with few rows, each with
 // at least 16 KB of logits.
 int cluster_of(const DistillArgs& a, int64_t row_bytes, int64_t ctas) {
@@ -419,9 +787,20 @@ int launch_rows(const DistillArgs& a, DistillPass pass, int sm_count, cudaStream
 int launch_distill(const DistillArgs& a, DistillPass pass, int sm_count, void* stream) {
     return with_type(a.dtype, [&](auto t) {
         using T = decltype(t);
+        if (pass != kDistillForward && a.rows >= 4 * sm_count && (int64_t)a.vocab * (int)sizeof(T) > 32768)
+            return launch_ring<T>(a, pass, sm_count, (cudaStream_t)stream);
         if ((int64_t)a.vocab * (int)sizeof(T) <= 32768) return launch_rows<T, 128>(a, pass, sm_count, (cudaStream_t)stream);
         return launch_rows<T, 512>(a, pass, sm_count, (cudaStream_t)stream);
     });
+}
+
+int take_distill_gave_up(int* value) {
+    int e = cudaMemcpyFromSymbol(value, g_gave_up, sizeof(int));
+    if (e == cudaSuccess && *value) {
+        const int zero = 0;
+        e = cudaMemcpyToSymbol(g_gave_up, &zero, sizeof(int));
+    }
+    return e;
 }
 
 }  // namespace soma

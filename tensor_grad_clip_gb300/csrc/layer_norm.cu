@@ -82,6 +82,7 @@ struct Rows {
         if (t >= 2 * kVec) return;
         const int c = t < kVec ? t : cols - 1 - (t - kVec);
         if (c >= 0 && c < cols) to[c] = row[c];
+        fence_to_async();  // (before a later copy into the slot)
     }
 };
 
@@ -228,7 +229,7 @@ __global__ void __maxnreg__(kPer == 32 ? 128 : kWarps ? 96 : 80)
     int turn = 0, slot = 0;
     uint32_t parity = 0;
     for (int it = 0; it < walk.count; ++it, y += walk.step * a.y_stride) {
-        if (!mbar_wait(ring.full + 8 * slot, parity, &gave_up)) break;
+        mbar_wait(ring.full + 8 * slot, parity, &gave_up);  // (after giving up, garbage follows)
         char* window = ring.window(slot, 0);
         if (it < inner_begin || it >= inner_end) {
             x[0].patch(walk.row(it), window, t);
@@ -369,7 +370,7 @@ __global__ void __maxnreg__(128)
             next_mean = a.mean[walk.row(it + 1)];
             next_rstd = a.rstd[walk.row(it + 1)];
         }
-        if (!mbar_wait(ring.full + 8 * slot, parity, &gave_up)) break;
+        mbar_wait(ring.full + 8 * slot, parity, &gave_up);  // (after giving up, garbage follows)
         char *window_x = ring.window(slot, 0), *window_dy = ring.window(slot, 1);
         if (it < inner_begin || it >= inner_end) {
             m[0].patch(walk.row(it), window_x, t);
@@ -644,14 +645,14 @@ int launch_rows(void (*kernel)(Args, int, int), const Args& a, int operands, int
     // a window is up to 15 bytes longer than its row at either end; a vector read may run 16 bytes past it
     const int slot = (a.cols * esize + 15) / 16 * 16 + 32, bytes = groups * operands * slot;
     int per_sm = 0;
-    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, block, 0);
-    if (e != cudaSuccess) return (int)e;
+    int e = resident_ctas((const void*)kernel, block, 0, &per_sm);
+    if (e != cudaSuccess) return e;
     per_sm = std::min(kCtasMost, std::max(1, per_sm));
     while (per_sm > 1 && kRingBytes / per_sm / bytes < 2) --per_sm;
     const int depth = std::max(1, std::min(kMaxDepth, kRingBytes / per_sm / bytes));
     const size_t smem = (size_t)bytes * depth;
-    if (smem > 40 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return (int)e;
+    if (smem > 40 * 1024) e = allow_smem((const void*)kernel, (int)smem);
+    if (e != cudaSuccess) return e;
     const int64_t work = (a.rows + groups - 1) / groups;
     *ctas = (int)std::max<int64_t>(1, std::min<int64_t>(work, (int64_t)sm_count * per_sm));
     kernel<<<*ctas, block, smem, st>>>(a, depth, slot);

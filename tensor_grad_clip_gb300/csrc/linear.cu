@@ -421,13 +421,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
     if (warp == kEpilogueWarps + 1) tmem_free<CG>(tmem, S::kTmemCols);
 }
 
-// ---- few rows: the weight's rows are the tile's 128 TMEM lanes ---------------
+// ---- few tiles: k split over a cluster ------------------------------------------
 //
-// out^T = B' A'^T with the roles swapped: `a` of the arguments is the operand
-// with few rows (k-major, at most BN), `b` the weight.  A cluster of S CTAs
-// splits k; each CTA leaves a partial 128 x BN sum in TMEM, sends every CTA
-// its share of the columns through distributed shared memory, and finishes
-// its own share, adding the partial sums in rank order.
+// For products that have too few 128 x 128 tiles for the SMs, those with few
+// rows above all.  The roles are swapped, out^T = B A^T: the rows of `b` (the
+// weight, in the forward pass) are the tile's 128 TMEM lanes and up to BN rows
+// of `a` its columns, so that one row of x costs no more than it must.  A
+// cluster of CTAs splits k; each leaves a partial 128 x BN sum in TMEM, sends
+// every CTA its share of the columns through distributed shared memory, and
+// finishes its own share, adding the partial sums in rank order.
 
 constexpr int kFewThreads = 32 * 6;
 
@@ -436,7 +438,8 @@ struct FewShape {
     static constexpr uint32_t kBytesW = kBM * kBK * 2, kBytesX = BN * kBK * 2, kStage = kBytesW + kBytesX;
     static constexpr uint32_t kExchange = kBM * BN * 4;
     // two CTAs per SM where the columns are few
-    static constexpr uint32_t kBudget = (BN <= 64 ? 113 * 1024 : kMaxSmem) - 1024 - 512 - kExchange;
+    static constexpr int kCtasPerSm = BN <= 64 ? 2 : 1;
+    static constexpr uint32_t kBudget = (kCtasPerSm == 2 ? 113 * 1024 : kMaxSmem) - 1024 - 512 - kExchange;
     static constexpr int kStages = (int)(kBudget / kStage) > 8 ? 8 : (int)(kBudget / kStage);
     static constexpr uint32_t kSmem = 1024 + kStages * kStage + kExchange + 512;
     static constexpr uint32_t kTmemCols = BN < 32 ? 32 : BN;
@@ -459,7 +462,8 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
     const GemmArgs& g = p.g;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)blockIdx.x % splits;
-    const int n0 = (int)(blockIdx.x / splits) * kBM;
+    const int64_t tile = blockIdx.x / splits;
+    const int n0 = (int)(tile % p.tiles_n) * kBM, m0 = (int)(tile / p.tiles_n) * BN;
     const int kts = (g.k + kBK - 1) / kBK;
     const int kt0 = (int)((int64_t)rank * kts / splits), kt1 = (int)((int64_t)(rank + 1) * kts / splits);
     if (threadIdx.x == 0) {
@@ -487,21 +491,21 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
             mbar_expect(full(s), S::kStage);
             const uint32_t dst = stages + s * S::kStage;
             load_operand<1>(dst, &p.b, g.b_kmajor, kBM, n0, kt * kBK, full(s));
-            load_operand<1>(dst + S::kBytesW, &p.a, true, BN, 0, kt * kBK, full(s));
+            load_operand<1>(dst + S::kBytesW, &p.a, g.a_kmajor, BN, m0, kt * kBK, full(s));
             if (++s == S::kStages) {
                 s = 0;
                 parity ^= 1;
             }
         }
     } else if (warp == 5 && lane == 0) {
-        const uint32_t idesc = instruction_desc(kIsBf16<T>, g.b_kmajor, true, kBM, BN);
+        const uint32_t idesc = instruction_desc(kIsBf16<T>, g.b_kmajor, g.a_kmajor, kBM, BN);
         int s = 0;
         uint32_t parity = 0;
         for (int kt = kt0; kt < kt1; ++kt) {
             if (!mbar_wait(full(s), parity, &gave_up)) break;
             tcgen05_after_sync();
             const uint32_t src = stages + s * S::kStage;
-            stage_mma<1>(tmem, src, src + S::kBytesW, g.b_kmajor, true, idesc, kt == kt0);
+            stage_mma<1>(tmem, src, src + S::kBytesW, g.b_kmajor, g.a_kmajor, idesc, kt == kt0);
             mma_commit<1>(empty(s));
             if (++s == S::kStages) {
                 s = 0;
@@ -511,12 +515,13 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
         mma_commit<1>(done);
     }
     __syncwarp();
-    const int share = BN / splits;  // columns that each CTA finishes
+    // columns that each CTA finishes (splits is a power of two)
+    const int log_share = __ffs(BN) - __ffs(splits), share = 1 << log_share;
     if (warp < 4) {
         if (mbar_wait(done, 0, &gave_up)) {
             __syncwarp();
             tcgen05_after_sync();
-            const int lane_n = warp * 32 + lane;
+            const uint32_t mine = smem_addr(exchange) + (rank * share * kBM + warp * 32 + lane) * 4;
 #pragma unroll
             for (int c0 = 0; c0 < BN; c0 += 16) {
                 uint32_t raw[16];
@@ -524,10 +529,9 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
                 tmem_ld_wait(raw);
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
-                    const int col = c0 + c, to = col / share;
-                    const uint32_t at = smem_addr(exchange + ((rank * share + col % share) * kBM + lane_n));
-                    if (splits == 1) exchange[col * kBM + lane_n] = __uint_as_float(raw[c]);
-                    else st_cluster_f32(cluster_map(at, to), __uint_as_float(raw[c]));
+                    const int col = c0 + c;
+                    const uint32_t at = mine + (col & (share - 1)) * (kBM * 4);
+                    st_cluster_f32(splits == 1 ? at : cluster_map(at, col >> log_share), __uint_as_float(raw[c]));
                 }
             }
         }
@@ -542,18 +546,26 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
     else __syncthreads();
     if (warp < 4) {
         const int n = n0 + warp * 32 + lane;
-        const float bias = g.bias && n < g.n ? to_f32(static_cast<const T*>(g.bias)[n]) : 0.f;
-        for (int c = 0; c < share; ++c) {
-            const int m = rank * share + c;
-            if (m >= g.m || n >= g.n) break;
-            float z = 0.f;
-            for (int r = 0; r < splits; ++r) z += exchange[(r * share + c) * kBM + warp * 32 + lane];
-            z += bias;
-            if (g.z_out) static_cast<T*>(g.z_out)[m * g.z_stride + n] = from_f32<T>(z);
-            float y = z;
-            with_act(g.act, [&](auto act) { y = activate<decltype(act)::value>(z); });
-            if (g.residual) y += to_f32(static_cast<const T*>(g.residual)[m * g.residual_stride + n]);
-            static_cast<T*>(g.out)[m * g.out_stride + n] = from_f32<T>(y);
+        const int count = min(share, g.m - m0 - rank * share);
+        if (n < g.n && count > 0) {
+            const float bias = g.bias ? to_f32(static_cast<const T*>(g.bias)[n]) : 0.f;
+            const float* from = exchange + warp * 32 + lane;
+            const int64_t m = m0 + rank * share;
+            const T* res = g.residual ? static_cast<const T*>(g.residual) + m * g.residual_stride + n : nullptr;
+            T* out = static_cast<T*>(g.out) + m * g.out_stride + n;
+            T* z_out = g.z_out ? static_cast<T*>(g.z_out) + m * g.z_stride + n : nullptr;
+            with_act(g.act, [&](auto act) {
+#pragma unroll 4
+                for (int c = 0; c < count; ++c) {
+                    float z = 0.f;
+                    for (int r = 0; r < splits; ++r) z += from[(r * share + c) * kBM];
+                    z += bias;
+                    if (z_out) z_out[c * g.z_stride] = from_f32<T>(z);
+                    float y = activate<decltype(act)::value>(z);
+                    if (res) y += to_f32(res[c * g.residual_stride]);
+                    out[c * g.out_stride] = from_f32<T>(y);
+                }
+            });
         }
     }
     if (warp == 5) {
@@ -609,7 +621,7 @@ int operand_map(CUtensorMap* map, const GemmArgs& g, const void* p, int64_t stri
 }
 
 int launch(const void* kernel, void** args, int grid, int threads, uint32_t smem, int cluster, void* stream) {
-    int e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const int e = allow_smem(kernel, (int)smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
@@ -651,12 +663,14 @@ int launch_few(TileArgs& p, int sm_count, void* stream) {
     using S = FewShape<BN>;
     const GemmArgs& g = p.g;
     int e;
-    if ((e = operand_map(&p.a, g, g.a, g.a_stride, true, g.m, BN)) ||
+    if ((e = operand_map(&p.a, g, g.a, g.a_stride, g.a_kmajor, g.m, BN)) ||
         (e = operand_map(&p.b, g, g.b, g.b_stride, g.b_kmajor, g.n, kBM)))
         return e;
-    const int tiles = (g.n + kBM - 1) / kBM, kts = (g.k + kBK - 1) / kBK;
+    p.tiles_n = (g.n + kBM - 1) / kBM;
+    p.tiles_m = (g.m + BN - 1) / BN;
+    const int tiles = p.tiles_n * p.tiles_m, kts = (g.k + kBK - 1) / kBK;
     int splits = 1;
-    while (splits < 8 && 2 * splits <= kts && tiles * splits * 2 <= 2 * sm_count) splits *= 2;
+    while (splits < 8 && 4 * splits <= kts && tiles * splits * 2 <= S::kCtasPerSm * sm_count) splits *= 2;
     void* args[] = {&p, &splits};
     return launch((const void*)few_kernel<BN, T>, args, tiles * splits, kFewThreads, S::kSmem, splits, stream);
 }
@@ -766,9 +780,15 @@ int launch_gemm(const GemmArgs& a, int sm_count, void* stream) {
         using T = decltype(t);
         TileArgs p{};
         p.g = a;
-        if (a.a_kmajor && a.m <= 128) {
-            if (a.m <= 16) return launch_few<16, T>(p, sm_count, stream);
-            if (a.m <= 32) return launch_few<32, T>(p, sm_count, stream);
+        // Few rows, or a long k over too few tiles for the SMs: k is split.
+        // (Joining costs about as much as 26 pipeline stages: 1021 x 1111 x 1003
+        // took 26.8 us split in two and 18.6 us whole, 300 x 300 x 10000 15.5 us
+        // split in eight and 50 us whole.)
+        const int64_t small = (int64_t)((a.m + 127) / 128) * ((a.n + 127) / 128), kts = (a.k + kBK - 1) / kBK;
+        const int64_t splits = small * 8 <= sm_count ? 8 : small * 4 <= sm_count ? 4 : small * 2 <= sm_count ? 2 : 1;
+        if (a.m <= 128 || kts - kts / splits > 26) {
+            if (a.a_kmajor && a.m <= 16) return launch_few<16, T>(p, sm_count, stream);
+            if (a.a_kmajor && a.m <= 32) return launch_few<32, T>(p, sm_count, stream);
             if (a.m <= 64) return launch_few<64, T>(p, sm_count, stream);
             return launch_few<128, T>(p, sm_count, stream);
         }

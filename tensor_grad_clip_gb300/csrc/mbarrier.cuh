@@ -69,6 +69,10 @@ __device__ __forceinline__ void outlast_copies() {
     for (int i = 0; i < 100; ++i) __nanosleep(20000);
 }
 
+// Orders ordinary accesses to shared memory before later asynchronous copies
+// from or to it.
+__device__ __forceinline__ void fence_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
 // `bytes` (a multiple of 16) from global to shared memory, both 16-byte
 // aligned, counted by `bar`.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {

@@ -10,7 +10,10 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <map>
+#include <mutex>
 #include <string>
+#include <tuple>
 
 #include "ops_kernels.h"
 #include "soma_kernels.h"
@@ -67,6 +70,10 @@ int sm_count(int device) {
 }
 
 constexpr int64_t kMaxInt = 0x7fffffff;
+
+std::mutex g_facts_mu;
+// (device, kernel, block or -1, shared memory) -> resident CTAs, or 1 where the shared memory is allowed
+std::map<std::tuple<int, const void*, int, int>, int> g_facts;
 
 bool is_dtype(int32_t d) { return d == SOMA_DTYPE_F32 || d == SOMA_DTYPE_BF16 || d == SOMA_DTYPE_F16; }
 int size_of(int32_t d) { return d == SOMA_DTYPE_F32 ? 4 : 2; }
@@ -206,6 +213,40 @@ soma::DistillArgs distill_args(const void* logits, int64_t logits_stride, const 
 
 }  // namespace
 
+namespace soma {
+
+int allow_smem(const void* kernel, int bytes) {
+    int device = 0;
+    if (const cudaError_t e = cudaGetDevice(&device)) return e;
+    try {
+        std::lock_guard<std::mutex> lk(g_facts_mu);
+        int& most = g_facts[{device, kernel, -1, 0}];
+        if (most >= bytes) return cudaSuccess;
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) most = bytes;
+        return e;
+    } catch (...) {
+        return cudaErrorMemoryAllocation;
+    }
+}
+
+int resident_ctas(const void* kernel, int block, int smem, int* ctas) {
+    int device = 0;
+    if (const cudaError_t e = cudaGetDevice(&device)) return e;
+    try {
+        std::lock_guard<std::mutex> lk(g_facts_mu);
+        int& n = g_facts[{device, kernel, block, smem}];
+        cudaError_t e = cudaSuccess;
+        if (n == 0) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, block, smem);
+        *ctas = n;
+        return e;
+    } catch (...) {
+        return cudaErrorMemoryAllocation;
+    }
+}
+
+}  // namespace soma
+
 extern "C" {
 
 const char* soma_ops_last_error(void) { return g_error.c_str(); }
@@ -213,12 +254,13 @@ const char* soma_ops_last_error(void) { return g_error.c_str(); }
 soma_status_t soma_ops_check(int32_t device) {
     SOMA_ON_DEVICE(device);
     (void)sms;
-    int norm = 0, linear = 0;
+    int norm = 0, linear = 0, distill = 0;
     SOMA_TRY(cuda_status(soma::take_norm_gave_up(&norm), "check"));
     SOMA_TRY(cuda_status(soma::take_linear_gave_up(&linear), "check"));
-    if (norm || linear)
+    SOMA_TRY(cuda_status(soma::take_distill_gave_up(&distill), "check"));
+    if (norm || linear || distill)
         return fail(SOMA_ERR_STATE, "a %s kernel gave up waiting for its own copies: its results are not valid",
-                    norm ? "layer norm" : "linear");
+                    norm ? "layer norm" : linear ? "linear" : "distillation");
     return SOMA_OK;
 }
 

@@ -40,6 +40,12 @@ struct NormBwdArgs {
     int32_t dtype, param_dtype;
 };
 
+// What a kernel needs to know of the current device, looked up once per
+// kernel (and block and shared-memory size) and device: the driver's own
+// answers take microseconds per call.
+int allow_smem(const void* kernel, int bytes);
+int resident_ctas(const void* kernel, int block, int smem, int* ctas);
+
 int launch_norm_fwd(const NormFwdArgs& a, int sm_count, void* stream);
 int64_t norm_bwd_workspace(int64_t rows, int64_t cols, int sm_count);
 int launch_norm_bwd(const NormBwdArgs& a, int sm_count, void* stream);
@@ -122,5 +128,6 @@ int launch_distill(const DistillArgs& a, DistillPass pass, int sm_count, void* s
 // the last call (waits for the device).
 int take_norm_gave_up(int* value);
 int take_linear_gave_up(int* value);
+int take_distill_gave_up(int* value);
 
 }  // namespace soma

@@ -98,6 +98,8 @@ def _matrix(t, name):
 
 def _like(t, name, other, shape, dtype=None):
     """Checks a tensor that has to match `other`'s device, and its shape and dtype."""
+    if t.shape == shape and (dtype is None or t.dtype is dtype) and t.get_device() == other.get_device():
+        return
     if t.device != other.device:
         raise ValueError(f"{name}: on {t.device}, expected {other.device}")
     if tuple(t.shape) != tuple(shape):
@@ -123,9 +125,10 @@ def _empty_rows(like, shape):
     than 16 bytes a row."""
     rows, cols = like.shape
     per = 16 // like.element_size()
-    stride = cols + (like.stride(0) - cols) % per if rows > 1 else cols
-    if stride == cols:
+    stride = like.stride(0)
+    if stride == cols or rows <= 1 or (stride - cols) % per == 0:
         return torch.empty(shape, dtype=like.dtype, device=like.device)
+    stride = cols + (stride - cols) % per
     out = torch.empty((rows, stride), dtype=like.dtype, device=like.device)[:, :cols]
     return out if len(shape) == 2 else out.unflatten(0, shape[:-1])
 

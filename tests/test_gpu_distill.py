@@ -227,6 +227,34 @@ def test_shapes_and_no_rows(ops):
     assert loss.shape == (0,) and d.shape == (0, 640)
 
 
+@pytest.mark.parametrize("dtype,vocab,pad,offset", [
+    (torch.bfloat16, 20000, 0, 0), (torch.bfloat16, 16391, 0, 3), (torch.bfloat16, 110000, 0, 0),
+    (torch.float16, 106499, 3, 1), (torch.float32, 9000, 0, 0), (torch.float32, 9001, 2, 1),
+    (torch.float32, 50003, 0, 2), (torch.float16, 32768, 8, 0)])
+def test_many_long_rows(ops, dtype, vocab, pad, offset):
+    rows = 700  # several rows per SM
+    z, t, index, w, g = problem(rows, vocab, 50, dtype, pad=pad, offset=offset)
+    w[::7] = 0
+    w[-3:] = 0.5
+    index[5] = -1
+    index[11] = index[11, 3]
+    z[600, 17:] = -math.inf
+    z[600].scatter_(0, index[600].long(), 2.0)
+    check(ops, z, t, index, w, g, T=1.5)
+    alone = ops.distill_forward(z[333:334], t[333:334], index[333:334], temperature=1.5, row_weight=w[333:334])[0]
+    together = ops.distill_loss_grad(z, t, index, temperature=1.5, row_weight=w)
+    assert torch.allclose(alone, together[0][333:334], rtol=1e-5)
+    first = ops.distill_backward(g, z, torch.zeros_like(w), t, index, row_weight=w)
+    assert torch.equal(first, ops.distill_backward(g, z, torch.zeros_like(w), t, index, row_weight=w))
+
+
+def test_many_long_rows_and_entries(ops):
+    z, t, index, w, g = problem(650, 17000, 1024, torch.bfloat16, torch.float16, torch.int64)
+    index[3, :] = index[3, 0]
+    check(ops, z, t, index, w, g)
+    check(ops, z, t[:, :0], index[:, :0], w, g)
+
+
 @pytest.mark.parametrize("rows,vocab", [(2, 131072), (40, 50021), (400, 8000)])
 def test_same_bits_again(ops, rows, vocab):
     z, t, index, w, g = problem(rows, vocab, 64, torch.bfloat16)
