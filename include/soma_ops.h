@@ -82,7 +82,7 @@ soma_status_t soma_layer_norm_backward(int32_t device, const void *dy, int64_t d
  * x[m][k], weight[n][k], bias[n] (NULL = 0), residual[m][n] (NULL = 0),
  * y[m][n], all bf16 or all fp16 (products are exact, sums fp32).  z_out[m][n]
  * receives z rounded, for the backward pass (NULL = not wanted).  residual
- * may be y itself (same pointer and stride).  k >= 1. */
+ * may be y itself (same pointer and stride).  1 <= k <= 2^30, m, n <= 2^30. */
 #define SOMA_ACT_NONE      0  /* z */
 #define SOMA_ACT_RELU      1  /* max(z, 0) */
 #define SOMA_ACT_GELU      2  /* z * (1 + erf(z / sqrt(2))) / 2 */
@@ -133,7 +133,7 @@ soma_status_t soma_linear_backward(int32_t device, const void *dy, int64_t dy_st
  *
  * logits[rows][vocab] in dtype, teacher[rows][top] in teacher_dtype,
  * index[rows][top] int32 or int64, 0 <= top <= SOMA_DISTILL_MAX_TOP,
- * 1 <= vocab < 2^31; loss and lse [rows] fp32.
+ * 1 <= vocab <= 2^30; loss and lse [rows] fp32.
  *
  *   forward    loss and lse
  *   backward   dlogits for grad_loss[rows] = dL/dloss: scale = grad_loss * row_weight

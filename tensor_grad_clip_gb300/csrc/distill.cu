@@ -15,6 +15,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "mbarrier.cuh"
 #include "ops_device.cuh"
@@ -90,6 +91,39 @@ __device__ __forceinline__ void take(MaxSum& a, const float (&x)[16 / sizeof(T)]
         const float2 d = mul2(add2(make_float2(x[i], x[i + 1]), back), cc);
         a.s += exp2_fast(d.x) + exp2_fast(d.y);
     }
+}
+
+// Several vectors at once.
+template <typename T, int kN>
+__device__ __forceinline__ void take_many(MaxSum& a, const float (&x)[kN][16 / sizeof(T)], float c) {
+    constexpr int kVec = 16 / sizeof(T);
+    float m[kN];
+#pragma unroll
+    for (int q = 0; q < kN; ++q) {
+        m[q] = x[q][0];
+#pragma unroll
+        for (int i = 1; i < kVec; ++i) m[q] = fmaxf(m[q], x[q][i]);
+    }
+#pragma unroll
+    for (int q = 1; q < kN; ++q) m[0] = fmaxf(m[0], m[q]);
+    if (m[0] > a.m) {
+        a.s *= exp2_fast((a.m - m[0]) * c);
+        a.m = m[0];
+    }
+    const float2 back = both(-a.m), cc = both(c);
+    float2 s[kN];
+#pragma unroll
+    for (int q = 0; q < kN; ++q) {
+        s[q] = both(0.f);
+#pragma unroll
+        for (int i = 0; i < kVec; i += 2) {
+            const float2 d = mul2(add2(make_float2(x[q][i], x[q][i + 1]), back), cc);
+            s[q] = add2(s[q], make_float2(exp2_fast(d.x), exp2_fast(d.y)));
+        }
+    }
+#pragma unroll
+    for (int q = 1; q < kN; ++q) s[0] = add2(s[0], s[q]);
+    a.s += s[0].x + s[0].y;
 }
 
 // Maximum and sum of vectors [begin, end): vector i is thread i - begin mod
@@ -173,30 +207,41 @@ __device__ __forceinline__ void stream_gradient(const RowReader<T, false>& row, 
         for (; i < end; i += kBlock) {
             row.gather(i, x);
             scaled_softmax<T>(x, inv_t, lse, g);
-            store_vector<T, true>(out, (int64_t)kVec * i, row.cols, 0, x);
+            store_vector<T, true>(out, kVec * i, row.cols, 0, x);
         }
         return;
     }
     const float lse = ready();
     const int lane = threadIdx.x & 31;
-    const int cols = min(row.cols, end * kVec);  // (a CTA of a cluster stores nothing past its part)
-    for (int base = begin + (threadIdx.x & ~31); base < end; base += kBlock) {
-        const int i = base + lane;
-        if (base >= row.inner_begin && base + 32 <= inner) {
-            uint4 u[1], v[1];
-            if (row.phase) {
-                row.template load<true, 1>(i, 0, u, v);
-                row.template widen<true>(u[0], v[0], x);
-            } else {
-                row.template load<false, 1>(i, 0, u, v);
-                row.template widen<false>(u[0], v[0], x);
-            }
-        } else {
-            row.gather(i, x);
-        }
+    const int cols = min(row.cols, end * kVec);  // (a CTA stores nothing past its part of the row)
+    int first = begin + (threadIdx.x & ~31);     // the warp's first vector
+    auto general = [&] {
+        row.gather(first + lane, x);
         scaled_softmax<T>(x, inv_t, lse, g);
-        store_vector<T, false>(out, (int64_t)kVec * i, cols, out_phase, x);
-    }
+        store_vector<T, false>(out, kVec * (first + lane), cols, out_phase, x);
+        first += kBlock;
+    };
+    if (first < row.inner_begin && first < end) general();
+    auto whole = [&](auto shift) {
+        constexpr bool kShift = decltype(shift)::value;
+        constexpr int kAhead = 2;
+        for (; first + (kAhead - 1) * kBlock + 32 <= inner; first += kAhead * kBlock) {
+            uint4 u[kAhead], v[kShift ? kAhead : 1];
+            row.template load<kShift, kAhead>(first + lane, kBlock, u, v);
+            float y[kAhead][kVec];
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) {
+                row.template widen<kShift>(u[q], v[kShift ? q : 0], y[q]);
+                scaled_softmax<T>(y[q], inv_t, lse, g);
+            }
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q)
+                store_vector<T, false>(out, kVec * (first + q * kBlock + lane), cols, out_phase, y[q]);
+        }
+    };
+    if (row.phase) whole(std::true_type{});
+    else whole(std::false_type{});
+    while (first < end) general();
 }
 
 template <typename T, int kBlock>
@@ -205,7 +250,7 @@ __device__ __forceinline__ void stream_zeros(T* out, int begin, int end, int col
     const float zero[kVec] = {};
     const int out_phase = (int)((uintptr_t)out & 15);
     for (int base = begin + (threadIdx.x & ~31); base < end; base += kBlock)
-        store_vector<T, false>(out, (int64_t)kVec * (base + (threadIdx.x & 31)), min(cols, end * kVec), out_phase, zero);
+        store_vector<T, false>(out, kVec * (base + (threadIdx.x & 31)), min(cols, end * kVec), out_phase, zero);
 }
 
 // Teacher logit j of row r.
@@ -371,8 +416,8 @@ __global__ void __launch_bounds__(kBlock, 1536 / kBlock) distill_kernel(const __
 
 // ---- many rows: a persistent CTA per SM -----------------------------------------
 //
-// A row passes through a ring of chunks in shared memory, filled by bulk
-// copies.  For loss and gradient together, the last chunks of the row stay in
+// For loss and gradient together, a row passes through a ring of chunks in
+// shared memory, filled by bulk copies.  The last chunks of the row stay in
 // the ring from the first pass (maximum and sum) to the second (gradient), so
 // that a row that fits is read once, from HBM; of a longer one, the first
 // chunks are copied again, from L2.  Each chunk that the second pass frees is
@@ -382,23 +427,40 @@ __global__ void __launch_bounds__(kBlock, 1536 / kBlock) distill_kernel(const __
 constexpr int kRingBlock = 512;                 // computing threads
 constexpr int kTeachers = 128;
 constexpr int kRingThreads = kRingBlock + 32 + kTeachers;
-constexpr int kChunkVecs = 1024;                // two vectors per computing thread
-constexpr int kSlotBytes = kChunkVecs * 16 + 32;
-constexpr int kSlots = 12;
+constexpr int kEach = 4;                        // vectors of a chunk per computing thread
+constexpr int kChunkVecs = kEach * kRingBlock;
+constexpr int kSlotBytes = kChunkVecs * 16;
+constexpr int kSlots = 6;
 
 __device__ int g_gave_up;  // a bounded wait ran out on this device
 
-struct RingShared {
-    uint64_t full[kSlots], empty[kSlots], taught, normalized, done;
-    float2 warp_part[2][kRingBlock / 32];
-    float lse;
-    int any, gave_up;
-    __align__(16) float p[SOMA_DISTILL_MAX_TOP];
+// What the teachers know of a row: entries, their probabilities (then their
+// logarithms), the student's logits there, and for the first entry of each
+// place the sum of the probabilities at that place (-1 for a repeated one).
+struct Lesson {
     __align__(16) int at[SOMA_DISTILL_MAX_TOP];
+    __align__(16) float p[SOMA_DISTILL_MAX_TOP];
+    float zt[SOMA_DISTILL_MAX_TOP], sum[SOMA_DISTILL_MAX_TOP];
 };
 
-// Chunk c of row r in memory.  The first and last words of the matrix's own
-// span may not be whole: those are left out of the copy and patched.
+// Rows that count are numbered 0, 1, ...; row k uses lesson, lse and barriers
+// k % 2.  The teachers prepare row k + 1 while row k streams, and finish row
+// k - 1 (loss and the gradient at its entries) before that.
+struct RingShared {
+    Lesson lesson[2];
+    uint64_t full[kSlots], empty[kSlots];
+    uint64_t taught[2];      // the row's lesson is ready, and zt is read
+    uint64_t normalized[2];  // lse is known
+    uint64_t done[2];        // the row's gradient is written
+    float2 warp_part[2][kRingBlock / 32];
+    float lse[2];
+    float loss[kTeachers / 32];
+    int any[2], gave_up;
+};
+
+// Chunk c of row r in memory.  Rows start on 16-byte boundaries; the words
+// that hold a row's end are copied with it where they lie in the matrix's own
+// span, and patched in where that ends first.
 template <typename T>
 struct Chunks {
     static constexpr int kVec = 16 / sizeof(T), kCols = kChunkVecs * kVec;
@@ -407,60 +469,48 @@ struct Chunks {
     int cols, count;
     __device__ __forceinline__ const T* first(int64_t r, int c) const { return base + r * stride + (int64_t)c * kCols; }
     __device__ __forceinline__ int size(int c) const { return min(kCols, cols - c * kCols); }
+    // The last row's last chunk, where it does not fill its last word.
     __device__ __forceinline__ bool cut(int64_t r, int c) const {
-        const uintptr_t s = (uintptr_t)first(r, c), e = s + (uintptr_t)size(c) * sizeof(T);
-        return (s & ~(uintptr_t)15) < (uintptr_t)base ||
-               ((e + 15) & ~(uintptr_t)15) > (uintptr_t)(base + (rows - 1) * stride + cols);
+        return c == count - 1 && r == rows - 1 && cols % kVec != 0;
     }
     __device__ __forceinline__ void copy(int64_t r, int c, uint32_t slot, uint32_t bar) const {
-        const uintptr_t s = (uintptr_t)first(r, c), e = s + (uintptr_t)size(c) * sizeof(T), a = s & ~(uintptr_t)15;
-        uintptr_t lo = a, hi = (e + 15) & ~(uintptr_t)15;
-        if (lo < (uintptr_t)base) lo += 16;
-        if (hi > (uintptr_t)(base + (rows - 1) * stride + cols)) hi -= 16;
-        const uint32_t bytes = hi > lo ? (uint32_t)(hi - lo) : 0;
-        mbar_expect(bar, bytes);
-        if (bytes) bulk_load(slot + (uint32_t)(lo - a), reinterpret_cast<const void*>(lo), bytes, bar);
+        const uint32_t words = (uint32_t)(size(c) + (cut(r, c) ? 0 : kVec - 1)) / kVec;
+        mbar_expect(bar, words * 16);
+        if (words) bulk_load(slot, first(r, c), words * 16, bar);
     }
-    // The elements of the chunk's first and last word, one by one.
     __device__ __forceinline__ void patch(int64_t r, int c, char* slot, int t) const {
-        const T* from = first(r, c);
-        T* to = reinterpret_cast<T*>(slot + ((uintptr_t)from & 15));
-        const int n = size(c);
-        if (t >= 2 * kVec) return;
-        const int i = t < kVec ? t : n - 1 - (t - kVec);
-        if (i >= 0 && i < n) to[i] = from[i];
+        const int n = size(c), whole = n / kVec * kVec;
+        if (t < n - whole) reinterpret_cast<T*>(slot)[whole + t] = first(r, c)[whole + t];
     }
 };
 
-template <typename T, int PASS>
+template <typename T>
 __global__ void __launch_bounds__(kRingThreads) distill_ring_kernel(const __grid_constant__ DistillArgs a) {
-    constexpr int kVec = 16 / sizeof(T), kWarps = kRingBlock / 32, kPasses = kChunkVecs / kRingBlock;
-    constexpr bool kBoth = PASS == kDistillLossGrad;
+    constexpr int kVec = 16 / sizeof(T), kWarps = kRingBlock / 32;
     extern __shared__ __align__(128) char dynamic[];
     RingShared& sh = *reinterpret_cast<RingShared*>(dynamic + kSlots * kSlotBytes);
     const int t = threadIdx.x, lane = t & 31;
     const Chunks<T> z{static_cast<const T*>(a.logits), a.logits_stride, a.rows, a.vocab,
                       (a.vocab + kChunkVecs * kVec - 1) / (kChunkVecs * kVec)};
     // chunks that do not stay in the ring until the second pass
-    const int spilled = kBoth ? max(0, z.count - kSlots) : 0;
+    const int spilled = max(0, z.count - kSlots);
     const uint32_t full = smem_addr(sh.full), empty = smem_addr(sh.empty);
-    const uint32_t taught = smem_addr(&sh.taught), normalized = smem_addr(&sh.normalized), done = smem_addr(&sh.done);
+    const uint32_t taught = smem_addr(sh.taught), normalized = smem_addr(sh.normalized), done = smem_addr(sh.done);
     if (t == 0) {
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(full + 8 * i, 1);
             mbar_init(empty + 8 * i, kWarps);
         }
-        mbar_init(taught, kTeachers);
-        mbar_init(normalized, 1);
-        mbar_init(done, kWarps);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(taught + 8 * i, kTeachers);
+            mbar_init(normalized + 8 * i, 1);
+            mbar_init(done + 8 * i, kWarps);
+        }
         mbar_init_fence();
         sh.gave_up = 0;
     }
     __syncthreads();
-    auto scale_of = [&](int64_t r) {
-        const float w = a.row_weight ? a.row_weight[r] : 1.f;
-        return kBoth ? w : a.grad_loss[r] * w;
-    };
+    auto scale_of = [&](int64_t r) { return a.row_weight ? a.row_weight[r] : 1.f; };
 
     if (t >= kRingBlock && t < kRingBlock + 32) {  // fills the ring
         if (lane == 0) {
@@ -481,125 +531,135 @@ __global__ void __launch_bounds__(kRingThreads) distill_ring_kernel(const __grid
                 }
             }
         }
-    } else if (t >= kRingBlock + 32) {  // the teacher's entries
+    } else if (t >= kRingBlock + 32) {  // the teachers
         const int u = t - kRingBlock - 32;
-        uint32_t parity = 0;
         auto sync = [] { asm volatile("bar.sync 2, %0;" ::"n"(kTeachers) : "memory"); };
         constexpr int kMine = SOMA_DISTILL_MAX_TOP / kTeachers;
-        for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-            const float w = a.row_weight ? a.row_weight[r] : 1.f, scale = scale_of(r);
-            if (scale == 0.f) {
-                if (kBoth && u == 0) {
+        auto next_row = [&](int64_t r) {  // the next row from r on that counts; the others' results
+            for (; r < a.rows && scale_of(r) == 0.f; r += gridDim.x)
+                if (u == 0) {
                     a.loss[r] = 0.f;
                     if (a.lse) a.lse[r] = 0.f;
                 }
-                continue;
-            }
+            return r;
+        };
+        // Row r into lesson b, up to its probabilities.
+        auto prepare = [&](int64_t r, int b) {
+            Lesson& l = sh.lesson[b];
             const T* row = z.first(r, 0);
-            float zt[kMine];  // the student's logits at this thread's entries
             bool any = false;
+            int64_t index[kMine];
+#pragma unroll
+            for (int q = 0; q < kMine; ++q) {
+                const int j = q * kTeachers + u;
+                index[q] = -1;
+                if (j < a.top)
+                    index[q] = a.index_type == SOMA_INDEX_I64
+                                   ? static_cast<const int64_t*>(a.index)[r * a.index_stride + j]
+                                   : static_cast<const int32_t*>(a.index)[r * a.index_stride + j];
+            }
 #pragma unroll
             for (int q = 0; q < kMine; ++q) {
                 const int j = q * kTeachers + u;
                 if (j >= (a.top + 3) / 4 * 4) break;
-                int64_t i = -1;
-                if (j < a.top)
-                    i = a.index_type == SOMA_INDEX_I64 ? static_cast<const int64_t*>(a.index)[r * a.index_stride + j]
-                                                       : static_cast<const int32_t*>(a.index)[r * a.index_stride + j];
-                const bool ok = i >= 0 && i < a.vocab;
+                const bool ok = index[q] >= 0 && index[q] < a.vocab;
                 float x = -INFINITY;
-                zt[q] = 0.f;
-                if (ok) {
+                if (ok)
                     x = a.teacher_dtype == kF32    ? teacher_at<float>(a, r, j)
                         : a.teacher_dtype == kBF16 ? teacher_at<__nv_bfloat16>(a, r, j)
                                                    : teacher_at<__half>(a, r, j);
-                    zt[q] = to_f32(row[i]);
-                }
-                sh.at[j] = ok ? (int)i : -1;
-                sh.p[j] = x;
+                l.zt[j] = ok ? to_f32(row[index[q]]) : 0.f;
+                l.at[j] = ok ? (int)index[q] : -1;
+                l.p[j] = x;
                 any |= x != -INFINITY;
             }
-            if (u == 0) sh.any = 0;
+            if (u == 0) sh.any[b] = 0;
             sync();
-            if (any) sh.any = 1;
-            sync();
-            any = sh.any != 0;
+            if (any) sh.any[b] = 1;
             // every warp forms the same statistics; each thread then its own entries' p
             float top = -INFINITY, total = 0.f;
-            for (int j = lane; j < a.top; j += 32) top = larger(top, sh.p[j]);
+            for (int j = lane; j < a.top; j += 32) top = larger(top, l.p[j]);
             top = warp_max(top);
             for (int j = lane; j < a.top; j += 32)
-                if (sh.p[j] != -INFINITY) total += expf((sh.p[j] - top) * a.inv_temperature);
+                if (l.p[j] != -INFINITY) total += expf((l.p[j] - top) * a.inv_temperature);
             total = warp_sum(total);
             const float log_total = logf(total);
             sync();
-            float logp[kMine], p[kMine];
+            float logp[kMine];
 #pragma unroll
             for (int q = 0; q < kMine; ++q) {
                 const int j = q * kTeachers + u;
+                logp[q] = -INFINITY;
                 if (j >= a.top) break;
-                logp[q] = (sh.p[j] - top) * a.inv_temperature - log_total;
-                p[q] = any && sh.at[j] >= 0 ? expf(logp[q]) : 0.f;
-                sh.p[j] = p[q];
+                if (sh.any[b] && l.at[j] >= 0) logp[q] = (l.p[j] - top) * a.inv_temperature - log_total;
+                l.p[j] = expf(logp[q]);
             }
             sync();
-            mbar_arrive(taught);  // zt is read and sh.any is set: the gradient may be written
-            float sums[kMine];
-            unsigned firsts = 0;
-#pragma unroll
-            for (int q = 0; q < kMine; ++q) {
-                const int j = q * kTeachers + u;
-                if (j >= a.top) break;
-                const int v = sh.at[j];
+            mbar_arrive(taught + 8 * b);  // zt is read and sh.any is set: the gradient may be written
+#pragma unroll 1
+            for (int j = u; j < a.top; j += kTeachers) {
+                const int v = l.at[j];
                 float sum = 0.f;
                 bool first = v >= 0;
                 for (int i = 0; i < a.top; i += 4) {  // (entries past top are at -1)
-                    const int4 i4 = *reinterpret_cast<const int4*>(sh.at + i);
-                    const float4 p4 = *reinterpret_cast<const float4*>(sh.p + i);
+                    const int4 i4 = *reinterpret_cast<const int4*>(l.at + i);
+                    const float4 p4 = *reinterpret_cast<const float4*>(l.p + i);
                     if (i4.x == v) { first &= i >= j; sum += p4.x; }
                     if (i4.y == v) { first &= i + 1 >= j; sum += p4.y; }
                     if (i4.z == v) { first &= i + 2 >= j; sum += p4.z; }
                     if (i4.w == v) { first &= i + 3 >= j; sum += p4.w; }
                 }
-                sums[q] = sum;
-                firsts |= (unsigned)first << q;
+                l.sum[j] = first ? sum : -1.f;  // (a NaN sum is not -1)
             }
-            float lse;
-            if (kBoth) {
-                mbar_wait(normalized, parity, &sh.gave_up);
-                lse = sh.lse;
-                float loss = 0.f;
-#pragma unroll
-                for (int q = 0; q < kMine; ++q)
-                    if (q * kTeachers + u < a.top && p[q] != 0.f) loss += p[q] * (logp[q] - fmaf(zt[q], a.inv_temperature, -lse));
-                loss = warp_sum(loss);
-                sync();  // sh.p has been read by all
-                if (lane == 0) sh.p[u >> 5] = loss;
-                sync();
-                if (u == 0) {
-                    loss = (sh.p[0] + sh.p[1]) + (sh.p[2] + sh.p[3]);
-                    a.loss[r] = any ? w * a.temperature * a.temperature * loss : 0.f;
-                    if (a.lse) a.lse[r] = lse;
-                }
-            } else {
-                lse = a.lse_in[r];
-            }
-            mbar_wait(done, parity, &sh.gave_up);
-            T* dz = static_cast<T*>(a.dlogits) + r * a.dlogits_stride;
-            const float g = scale * a.temperature;
+            sync();  // (the probabilities make room for their logarithms)
 #pragma unroll
             for (int q = 0; q < kMine; ++q)
-                if (any && (firsts >> q & 1))
-                    dz[sh.at[q * kTeachers + u]] =
-                        from_f32<T>(g * (exp2_fast(fmaf(zt[q], a.inv_temperature, -lse) * kLog2e) - sums[q]));
-            sync();  // sh.at has been read by all
-            parity ^= 1;
+                if (q * kTeachers + u < a.top) l.p[q * kTeachers + u] = logp[q];
+        };
+        // The k-th row that counts: its loss, and the gradient at its entries.
+        auto finish = [&](int64_t r, int k) {
+            const int b = k & 1;
+            const uint32_t parity = (k >> 1) & 1;
+            const Lesson& l = sh.lesson[b];
+            mbar_wait(normalized + 8 * b, parity, &sh.gave_up);
+            const float lse = sh.lse[b];
+            float loss = 0.f;
+            for (int j = u; j < a.top; j += kTeachers) {
+                const float logp = l.p[j], p = expf(logp);
+                if (p != 0.f) loss += p * (logp - fmaf(l.zt[j], a.inv_temperature, -lse));
+            }
+            loss = warp_sum(loss);
+            if (lane == 0) sh.loss[u >> 5] = loss;
+            sync();
+            if (u == 0) {
+                const float w = scale_of(r);
+                loss = (sh.loss[0] + sh.loss[1]) + (sh.loss[2] + sh.loss[3]);
+                a.loss[r] = sh.any[b] ? w * a.temperature * a.temperature * loss : 0.f;
+                if (a.lse) a.lse[r] = lse;
+            }
+            const float g = scale_of(r) * a.temperature;
+            mbar_wait(done + 8 * b, parity, &sh.gave_up);
+            T* dz = static_cast<T*>(a.dlogits) + r * a.dlogits_stride;
+            if (sh.any[b])
+                for (int j = u; j < a.top; j += kTeachers)
+                    if (l.sum[j] != -1.f)
+                        dz[l.at[j]] = from_f32<T>(g * (exp2_fast(fmaf(l.zt[j], a.inv_temperature, -lse) * kLog2e) - l.sum[j]));
+            sync();  // the lesson may go
+        };
+        int64_t r = next_row(blockIdx.x), before = 0;
+        int k = 0;
+        for (; r < a.rows; ++k) {
+            prepare(r, k & 1);
+            if (k > 0) finish(before, k - 1);
+            before = r;
+            r = next_row(r + gridDim.x);
         }
+        if (k > 0) finish(before, k - 1);
     } else {
         const float c = a.inv_temperature * kLog2e;
         const int warp = t >> 5;
-        int slot = 0, turn = 0;
-        uint32_t parity = 0, row_parity = 0;
+        int slot = 0, k = 0;
+        uint32_t parity = 0;
         auto advance = [&] {
             if (++slot == kSlots) {
                 slot = 0;
@@ -611,20 +671,14 @@ __global__ void __launch_bounds__(kRingThreads) distill_ring_kernel(const __grid
             if (lane == 0) mbar_arrive(empty + 8 * s);
         };
         float next = blockIdx.x < a.rows ? scale_of(blockIdx.x) : 0.f;
-        float next_lse = !kBoth && blockIdx.x < a.rows ? a.lse_in[blockIdx.x] : 0.f;
         for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
             const float scale = next;
-            float lse = next_lse;
-            if (r + gridDim.x < a.rows) {
-                next = scale_of(r + gridDim.x);
-                if (!kBoth) next_lse = a.lse_in[r + gridDim.x];
-            }
+            if (r + gridDim.x < a.rows) next = scale_of(r + gridDim.x);
             T* dz = static_cast<T*>(a.dlogits) + r * a.dlogits_stride;
             if (scale == 0.f) {
                 stream_zeros<T, kRingBlock>(dz, 0, (a.vocab + kVec - 1) / kVec, a.vocab);
                 continue;
             }
-            const int phase = (int)((uintptr_t)z.first(r, 0) & 15), out_phase = (int)((uintptr_t)dz & 15);
             auto arrived = [&](int j) {  // chunk j is in the current slot
                 mbar_wait(full + 8 * slot, parity, &sh.gave_up);
                 if (z.cut(r, j)) {
@@ -633,91 +687,95 @@ __global__ void __launch_bounds__(kRingThreads) distill_ring_kernel(const __grid
                     asm volatile("bar.sync 1, %0;" ::"n"(kRingBlock) : "memory");
                 }
             };
-            auto vector = [&](int s, int i, int n, float (&x)[kVec]) {  // vector i of a chunk of n elements
-                const char* at = dynamic + s * kSlotBytes + i * 16;
-                const uint4 u0 = *reinterpret_cast<const uint4*>(at);
-                widen16(phase ? shifted<T>(u0, *reinterpret_cast<const uint4*>(at + 16), phase) : u0, x, T{});
+            // Vector i of the chunk at `at`, of n elements; -inf past its end.
+            auto vector = [&](const char* at, int i, int n, float (&x)[kVec]) {
+                widen16(*reinterpret_cast<const uint4*>(at + i * 16), x, T{});
                 if (kVec * (i + 1) > n) {
 #pragma unroll
                     for (int q = 0; q < kVec; ++q)
                         if (kVec * i + q >= n) x[q] = -INFINITY;
                 }
             };
-            const int first_slot = slot;
-            if (kBoth) {
-                MaxSum mine{kLowest, 0.f};
-                for (int j = 0; j < z.count; ++j) {
-                    arrived(j);
-                    const int n = z.size(j);
+            const int b = k & 1, first_slot = slot;
+            MaxSum mine{kLowest, 0.f};
+            for (int j = 0; j < z.count; ++j) {
+                arrived(j);
+                const int n = z.size(j);
+                const char* at = dynamic + slot * kSlotBytes;
+                if (n == Chunks<T>::kCols) {  // all of the thread's vectors at once
+                    float x[kEach][kVec];
 #pragma unroll
-                    for (int q = 0; q < kPasses; ++q) {
+                    for (int q = 0; q < kEach; ++q) vector(at, t + q * kRingBlock, n, x[q]);
+                    take_many<T>(mine, x, c);
+                } else {
+                    for (int i = t; i * kVec < n; i += kRingBlock) {
                         float x[kVec];
-                        if ((t + q * kRingBlock) * kVec < n) {
-                            vector(slot, t + q * kRingBlock, n, x);
-                            take<T>(mine, x, c);
-                        }
+                        vector(at, i, n, x);
+                        take<T>(mine, x, c);
                     }
-                    if (j < spilled) release(slot);
-                    advance();
                 }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1)
-                    mine = join(mine, {__shfl_xor_sync(0xffffffffu, mine.m, o), __shfl_xor_sync(0xffffffffu, mine.s, o)}, c);
-                if (lane == 0) sh.warp_part[turn][warp] = make_float2(mine.m, mine.s);
-                asm volatile("bar.sync 1, %0;" ::"n"(kRingBlock) : "memory");
-                const float2 part = sh.warp_part[turn][lane % kWarps];
-                turn ^= 1;
-                mine = {part.x, part.y};
-#pragma unroll
-                for (int o = kWarps / 2; o > 0; o >>= 1)
-                    mine = join(mine, {__shfl_xor_sync(0xffffffffu, mine.m, o), __shfl_xor_sync(0xffffffffu, mine.s, o)}, c);
-                lse = fmaf(mine.m, a.inv_temperature, logf(mine.s));
+                if (j < spilled) release(slot);
+                advance();
             }
-            // the teachers are done with the row before, and have read what the gradient may replace
-            mbar_wait(taught, row_parity, &sh.gave_up);
-            if (kBoth && t == 0) {
-                sh.lse = lse;
-                mbar_arrive(normalized);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                mine = join(mine, {__shfl_xor_sync(0xffffffffu, mine.m, o), __shfl_xor_sync(0xffffffffu, mine.s, o)}, c);
+            if (lane == 0) sh.warp_part[b][warp] = make_float2(mine.m, mine.s);
+            asm volatile("bar.sync 1, %0;" ::"n"(kRingBlock) : "memory");
+            const float2 part = sh.warp_part[b][lane % kWarps];
+            mine = {part.x, part.y};
+#pragma unroll
+            for (int o = kWarps / 2; o > 0; o >>= 1)
+                mine = join(mine, {__shfl_xor_sync(0xffffffffu, mine.m, o), __shfl_xor_sync(0xffffffffu, mine.s, o)}, c);
+            const float lse = fmaf(mine.m, a.inv_temperature, logf(mine.s));
+            mbar_wait(taught + 8 * b, (k >> 1) & 1, &sh.gave_up);
+            if (t == 0) {
+                sh.lse[b] = lse;
+                mbar_arrive(normalized + 8 * b);
             }
-            const float g = sh.any ? scale * a.temperature : 0.f;
+            const bool any = sh.any[b] != 0;
+            const float g = scale * a.temperature;
             auto gradient = [&](int s, int j) {  // of chunk j in slot s
                 const int n = z.size(j);
+                const char* at = dynamic + s * kSlotBytes;
                 T* out = dz + (int64_t)j * Chunks<T>::kCols;
+                if (any && n == Chunks<T>::kCols) {
+                    float x[kEach][kVec];
 #pragma unroll
-                for (int q = 0; q < kPasses; ++q) {
-                    const int i = t + q * kRingBlock, whole = (t & ~31) + q * kRingBlock;
-                    if (whole * kVec >= n) break;  // (all lanes of a warp store together)
+                    for (int q = 0; q < kEach; ++q) vector(at, t + q * kRingBlock, n, x[q]);
+                    release(s);
+#pragma unroll
+                    for (int q = 0; q < kEach; ++q) scaled_softmax<T>(x[q], a.inv_temperature, lse, g);
+#pragma unroll
+                    for (int q = 0; q < kEach; ++q)
+                        __stcs(reinterpret_cast<uint4*>(out) + t + q * kRingBlock, narrow16(x[q], T{}));
+                    return;
+                }
+#pragma unroll 1
+                for (int i = t; i * kVec < n; i += kRingBlock) {
                     float x[kVec];
-                    if (i * kVec < n) vector(s, i, n, x);
-                    else
-#pragma unroll
-                        for (int k = 0; k < kVec; ++k) x[k] = -INFINITY;
+                    vector(at, i, n, x);
                     scaled_softmax<T>(x, a.inv_temperature, lse, g);
-                    if (g == 0.f) {
 #pragma unroll
-                        for (int k = 0; k < kVec; ++k) x[k] = 0.f;
-                    }
-                    if (out_phase == 0 && kVec * (i + 1) <= n) __stcs(reinterpret_cast<uint4*>(out) + i, narrow16(x, T{}));
-                    else store_vector<T, false>(out, (int64_t)kVec * i, n, out_phase, x);
+                    for (int q = 0; q < kVec; ++q) x[q] = any ? x[q] : 0.f;
+                    store_vector<T, true>(out, kVec * i, n, 0, x);
                 }
                 release(s);
             };
-            if (kBoth) {
-                // the chunks that stayed, then those copied again
-                int s = (first_slot + spilled) % kSlots;
-                for (int j = spilled; j < z.count; ++j) {
-                    gradient(s, j);
-                    if (++s == kSlots) s = 0;
-                }
+            // the chunks that stayed, then those copied again
+            int s = (first_slot + spilled) % kSlots;
+            for (int j = spilled; j < z.count; ++j) {
+                gradient(s, j);
+                if (++s == kSlots) s = 0;
             }
-            for (int j = 0; j < (kBoth ? spilled : z.count); ++j) {
+            for (int j = 0; j < spilled; ++j) {
                 arrived(j);
                 gradient(slot, j);
                 advance();
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(done);
-            row_parity ^= 1;
+            if (lane == 0) mbar_arrive(done + 8 * b);
+            ++k;
         }
     }
     if (sh.gave_up) {
@@ -727,8 +785,8 @@ __global__ void __launch_bounds__(kRingThreads) distill_ring_kernel(const __grid
 }
 
 template <typename T>
-int launch_ring(const DistillArgs& a, DistillPass pass, int sm_count, cudaStream_t stream) {
-    auto kernel = pass == kDistillBackward ? distill_ring_kernel<T, kDistillBackward> : distill_ring_kernel<T, kDistillLossGrad>;
+int launch_ring(const DistillArgs& a, int sm_count, cudaStream_t stream) {
+    auto kernel = distill_ring_kernel<T>;
     const int smem = kSlots * kSlotBytes + (int)sizeof(RingShared);
     const int e = allow_smem((const void*)kernel, smem);
     if (e != cudaSuccess) return e;
@@ -787,8 +845,12 @@ int launch_rows(const DistillArgs& a, DistillPass pass, int sm_count, cudaStream
 int launch_distill(const DistillArgs& a, DistillPass pass, int sm_count, void* stream) {
     return with_type(a.dtype, [&](auto t) {
         using T = decltype(t);
-        if (pass != kDistillForward && a.rows >= 4 * sm_count && (int64_t)a.vocab * (int)sizeof(T) > 32768)
-            return launch_ring<T>(a, pass, sm_count, (cudaStream_t)stream);
+        auto aligned = [](const void* p, int64_t stride) {
+            return (uintptr_t)p % 16 == 0 && stride * (int64_t)sizeof(T) % 16 == 0;
+        };
+        if (pass == kDistillLossGrad && a.rows >= 4 * sm_count && (int64_t)a.vocab * (int)sizeof(T) > 32768 &&
+            aligned(a.logits, a.logits_stride) && aligned(a.dlogits, a.dlogits_stride))
+            return launch_ring<T>(a, sm_count, (cudaStream_t)stream);
         if ((int64_t)a.vocab * (int)sizeof(T) <= 32768) return launch_rows<T, 128>(a, pass, sm_count, (cudaStream_t)stream);
         return launch_rows<T, 512>(a, pass, sm_count, (cudaStream_t)stream);
     });

@@ -143,6 +143,13 @@ __device__ __forceinline__ void add8(float* x, const uint4& w) {
     t = unpack2<T>(w.w); x[6] += t.x; x[7] += t.y;
 }
 
+// Lets the next kernel of the stream be set up, and waits until the one
+// before it is done and its results are visible.
+__device__ __forceinline__ void follow_stream() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // Copies an operand into rows that start on 16-byte boundaries, as TMA needs.
 template <typename T>
 __global__ void __launch_bounds__(256) repack_kernel(const T* src, int64_t src_stride, T* dst, int64_t dst_stride,
@@ -326,11 +333,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
         mbar_init_fence();
     }
     if (warp == kEpilogueWarps + 1) tmem_alloc<CG>(smem_addr(&tmem_slot), S::kTmemCols);
+    if (threadIdx.x == kEpilogueWarps * 32) {
+        prefetch_map(&p.a);
+        prefetch_map(&p.b);
+    }
     tcgen05_before_sync();
     if (CG == 2) cluster_sync_all();
     else __syncthreads();
     tcgen05_after_sync();
     const uint32_t tmem = tmem_slot;
+    follow_stream();
 
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
     const int64_t first = blockIdx.x / CG, step = gridDim.x / CG;
@@ -341,8 +353,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
     };
 
     if (warp == kEpilogueWarps && lane == 0) {
-        prefetch_map(&p.a);
-        prefetch_map(&p.b);
         int s = 0;
         uint32_t parity = 1;  // a fresh barrier's previous phase counts as done
         bool ok = true;
@@ -476,14 +486,18 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
         mbar_init_fence();
     }
     if (warp == 5) tmem_alloc<1>(smem_addr(&tmem_slot), S::kTmemCols);
-    tcgen05_before_sync();
-    __syncthreads();
-    tcgen05_after_sync();
-    const uint32_t tmem = tmem_slot;
-
-    if (warp == 4 && lane == 0) {
+    if (threadIdx.x == 4 * 32) {
         prefetch_map(&p.a);
         prefetch_map(&p.b);
+    }
+    tcgen05_before_sync();
+    if (splits > 1) cluster_sync_all();  // (no CTA writes into another that has not started)
+    else __syncthreads();
+    tcgen05_after_sync();
+    const uint32_t tmem = tmem_slot;
+    follow_stream();
+
+    if (warp == 4 && lane == 0) {
         int s = 0;
         uint32_t parity = 1;
         for (int kt = kt0; kt < kt1; ++kt) {
@@ -628,12 +642,15 @@ int launch(const void* kernel, void** args, int grid, int threads, uint32_t smem
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = (cudaStream_t)stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = cluster;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    // may be set up while the kernel before it ends (it waits before it reads or writes)
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelExC(&cfg, kernel, args);
 }
 

@@ -70,6 +70,7 @@ int sm_count(int device) {
 }
 
 constexpr int64_t kMaxInt = 0x7fffffff;
+constexpr int64_t kMaxExtent = 1 << 30;  // of a dimension that kernels index with an int, sums of a few included
 
 std::mutex g_facts_mu;
 // (device, kernel, block or -1, shared memory) -> resident CTAs, or 1 where the shared memory is allowed
@@ -152,9 +153,9 @@ soma_status_t check_norm(int64_t rows, int64_t cols, int32_t dtype, int32_t para
 }
 
 soma_status_t check_linear(int64_t m, int64_t n, int64_t k, int32_t dtype, int32_t act) {
-    if (m < 0 || n < 0 || m > kMaxInt || n > kMaxInt) return fail(SOMA_ERR_INVALID_ARG, "m and n must be in [0, 2^31)");
-    if (k < 1 || k > kMaxInt) return fail(SOMA_ERR_INVALID_ARG, "k must be in [1, 2^31)");
-    if (m > 0 && n > INT64_MAX / 16 / m) return fail(SOMA_ERR_LIMIT, "m x n does not fit 64 bits of bytes");
+    if (m < 0 || n < 0 || m > kMaxExtent || n > kMaxExtent)
+        return fail(SOMA_ERR_INVALID_ARG, "m and n must be in [0, 2^30]");
+    if (k < 1 || k > kMaxExtent) return fail(SOMA_ERR_INVALID_ARG, "k must be in [1, 2^30]");
     if (dtype != SOMA_DTYPE_BF16 && dtype != SOMA_DTYPE_F16)
         return fail(SOMA_ERR_DTYPE, "dtype = %d: the linear layer takes bf16 or fp16", (int)dtype);
     if (act < SOMA_ACT_NONE || act > SOMA_ACT_SILU) return fail(SOMA_ERR_INVALID_ARG, "activation = %d", (int)act);
@@ -172,7 +173,7 @@ int64_t backward_bytes(const Operand& dy, const Operand& x, const Operand& weigh
 
 soma_status_t check_distill(const soma::DistillArgs& a, int64_t vocab, int64_t top, double temperature) {
     if (a.rows < 0) return fail(SOMA_ERR_INVALID_ARG, "rows < 0");
-    if (vocab < 1 || vocab > kMaxInt) return fail(SOMA_ERR_INVALID_ARG, "vocab must be in [1, 2^31)");
+    if (vocab < 1 || vocab > kMaxExtent) return fail(SOMA_ERR_INVALID_ARG, "vocab must be in [1, 2^30]");
     if (top < 0) return fail(SOMA_ERR_INVALID_ARG, "top < 0");
     if (top > SOMA_DISTILL_MAX_TOP)
         return fail(SOMA_ERR_LIMIT, "top = %lld, at most %d entries per row", (long long)top, SOMA_DISTILL_MAX_TOP);

@@ -122,7 +122,7 @@ __device__ __forceinline__ uint4 shifted(const uint4& u, const uint4& v, int pha
 // elements at a warp's two ends go one by one.  All lanes of a warp call this
 // together, with consecutive vectors.
 template <typename T, bool kAligned>
-__device__ __forceinline__ void store_vector(T* row, int64_t c, int64_t cols, int phase, const float* x) {
+__device__ __forceinline__ void store_vector(T* row, int c, int cols, int phase, const float* x) {
     constexpr int kVec = 16 / sizeof(T);
     const uint4 own = narrow16(x, T{});
     if (kAligned || phase == 0) {
