@@ -53,18 +53,22 @@ struct Rows {
     int cols;
 
     __device__ __forceinline__ int phase(int64_t r) const { return (int)((uintptr_t)(base + r * stride) & 15); }
-    // Starts the copy of row r's window; returns the bytes that `bar` will count.
-    // Only words inside the matrix's own span are read: at its two ends the
-    // window may stick out of it, and patch() fills in those few elements.
-    __device__ __forceinline__ uint32_t start(int64_t r, uint32_t slot, uint32_t bar, bool issue) const {
-        const uintptr_t s = (uintptr_t)(base + r * stride), e = s + (uintptr_t)cols * sizeof(T);
-        const uintptr_t a = s & ~(uintptr_t)15;
-        uintptr_t lo = a, hi = (e + 15) & ~(uintptr_t)15;
-        if (lo < (uintptr_t)base) lo += 16;
-        if (hi > (uintptr_t)(base + (rows - 1) * stride + cols)) hi -= 16;
-        const uint32_t bytes = hi > lo ? (uint32_t)(hi - lo) : 0;
-        if (issue && bytes) bulk_load(slot + (uint32_t)(lo - a), reinterpret_cast<const void*>(lo), bytes, bar);
-        return bytes;
+    // The window of the row at address s, clipped to the matrix's own span
+    // where it may stick out of it; patch() fills in those few elements.
+    template <bool kAligned>
+    __device__ __forceinline__ void window(uintptr_t s, bool edge, uintptr_t& lo, uint32_t& skip, uint32_t& bytes) const {
+        const uintptr_t e = s + (uint32_t)cols * (uint32_t)sizeof(T);
+        lo = kAligned ? s : s & ~(uintptr_t)15;
+        uintptr_t hi = (e + 15) & ~(uintptr_t)15;
+        skip = 0;
+        if (edge) {
+            if (lo < (uintptr_t)base) {
+                lo += 16;
+                skip = 16;
+            }
+            if (hi > (uintptr_t)(base + (rows - 1) * stride + cols)) hi -= 16;
+        }
+        bytes = hi > lo ? (uint32_t)(hi - lo) : 0;
     }
     // Rows outside [inner_begin, inner_end) may have a window that sticks out.
     __device__ __forceinline__ int64_t edge_rows() const {
@@ -98,6 +102,18 @@ __device__ __forceinline__ uint4 slot_vector(const char* slot, int c, int phase)
 // kN elements of a parameter vector from c on, `missing` where there is none.
 template <typename T, int kN>
 __device__ __forceinline__ void parameter(const void* v, bool f32, int c, int cols, float missing, float* w) {
+    if (v && ((uintptr_t)v & 15) == 0 && c + kN <= cols) {  // (c is a multiple of kN)
+        if (f32) {
+#pragma unroll
+            for (int i = 0; i < kN; i += 4) {
+                const float4 f = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(v) + c + i));
+                w[i] = f.x; w[i + 1] = f.y; w[i + 2] = f.z; w[i + 3] = f.w;
+            }
+        } else {
+            widen16(__ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(v) + c)), w, T{});
+        }
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
         w[i] = missing;
@@ -165,15 +181,23 @@ struct Ring {
     }
 };
 
-template <int kOperands, typename T>
-__device__ __forceinline__ void fill_row(const Ring<kOperands>& ring, const Rows<T> (&m)[kOperands], int64_t r, int slot) {
-    const uint32_t bar = ring.full + 8 * slot;
-    uint32_t bytes = 0;
+// Starts the copies of one row.  Every instruction here delays a row's
+// threads at their next barrier.
+template <bool kAligned, int kOperands, typename T>
+__device__ __forceinline__ void fill_row(const Ring<kOperands>& ring, const Rows<T> (&m)[kOperands], int64_t row,
+                                         bool edge, int slot) {
+    const uint32_t bar = ring.full + 8 * slot, to = smem_addr(ring.slots) + slot * kOperands * ring.slot_bytes;
+    uintptr_t lo[kOperands];
+    uint32_t skip[kOperands], bytes[kOperands], total = 0;
 #pragma unroll
-    for (int o = 0; o < kOperands; ++o) bytes += m[o].start(r, 0, bar, false);
-    mbar_expect(bar, bytes);
+    for (int o = 0; o < kOperands; ++o) {
+        m[o].template window<kAligned>((uintptr_t)(m[o].base + row * m[o].stride), edge, lo[o], skip[o], bytes[o]);
+        total += bytes[o];
+    }
+    mbar_expect(bar, total);
 #pragma unroll
-    for (int o = 0; o < kOperands; ++o) m[o].start(r, smem_addr(ring.window(slot, o)), bar, true);
+    for (int o = 0; o < kOperands; ++o)
+        if (bytes[o]) bulk_load(to + o * ring.slot_bytes + skip[o], reinterpret_cast<const void*>(lo[o]), bytes[o], bar);
 }
 
 // Threads of one row: kWarps warps where that is 1 or 2 (the CTA then has
@@ -206,12 +230,13 @@ __global__ void __maxnreg__(kPer == 32 ? 128 : kWarps ? 96 : 80)
     const Ring<1> ring{dynamic + group * depth * slot_bytes, smem_addr(bars[group]), depth, slot_bytes};
     const Rows<T> x[1] = {{static_cast<const T*>(a.x), a.x_stride, a.rows, a.cols}};
     const Walk walk((int64_t)blockIdx.x * kGroups + group, (int64_t)gridDim.x * kGroups, a.rows);
+    const int inner_begin = walk.below(x[0].inner_begin()), inner_end = walk.below(x[0].inner_end());
     if (threadIdx.x == 0) gave_up = 0;
     if (threadIdx.x < 32) scratch[threadIdx.x >> 4][threadIdx.x & 15] = both(0.f);
     if (t == 0) {
         for (int i = 0; i < depth; ++i) mbar_init(ring.full + 8 * i, 1);
         mbar_init_fence();
-        for (int i = 0; i < min(depth, walk.count); ++i) fill_row(ring, x, walk.row(i), i);
+        for (int i = 0; i < min(depth, walk.count); ++i) fill_row<kAligned>(ring, x, walk.row(i), i < inner_begin || i >= inner_end, i);
     }
     __syncthreads();
     const bool f32 = a.param_dtype == kF32;
@@ -224,7 +249,6 @@ __global__ void __maxnreg__(kPer == 32 ? 128 : kWarps ? 96 : 80)
     const float inv = 1.f / (float)a.cols;
     const int middle = a.cols / 2 / kVec * kVec, middle_n = min(4, a.cols - middle);
     const float inv_middle = 1.f / (float)middle_n;
-    const int inner_begin = walk.below(x[0].inner_begin()), inner_end = walk.below(x[0].inner_end());
     T* y = static_cast<T*>(a.y) + walk.first * a.y_stride;
     int turn = 0, slot = 0;
     uint32_t parity = 0;
@@ -269,7 +293,7 @@ __global__ void __maxnreg__(kPer == 32 ? 128 : kWarps ? 96 : 80)
         }
         const float2 s = row_totals<kWarps>(sum.x + sum.y, square.x + square.y, scratch, group, warps, turn);
         // (every thread has its part of the row in registers now)
-        if (t == 0 && it + depth < walk.count) fill_row(ring, x, walk.row(it + depth), slot);
+        if (t == 0 && it + depth < walk.count) fill_row<kAligned>(ring, x, walk.row(it + depth), it + depth >= inner_end || it + depth < inner_begin, slot);
         const float shift = s.x * inv;
         float var = fmaf(-shift, shift, s.y * inv);
         if (shift * shift > 4.f * var) {  // the same for all threads of the row
@@ -337,12 +361,14 @@ __global__ void __maxnreg__(128)
     const Rows<T> m[2] = {{static_cast<const T*>(a.x), a.x_stride, a.rows, a.cols},
                           {static_cast<const T*>(a.dy), a.dy_stride, a.rows, a.cols}};
     const Walk walk((int64_t)blockIdx.x * kGroups + group, (int64_t)gridDim.x * kGroups, a.rows);
+    const int inner_begin = walk.below(max(m[0].inner_begin(), m[1].inner_begin()));
+    const int inner_end = walk.below(min(m[0].inner_end(), m[1].inner_end()));
     if (threadIdx.x == 0) gave_up = 0;
     if (threadIdx.x < 32) scratch[threadIdx.x >> 4][threadIdx.x & 15] = both(0.f);
     if (t == 0) {
         for (int i = 0; i < depth; ++i) mbar_init(ring.full + 8 * i, 1);
         mbar_init_fence();
-        for (int i = 0; i < min(depth, walk.count); ++i) fill_row(ring, m, walk.row(i), i);
+        for (int i = 0; i < min(depth, walk.count); ++i) fill_row<kAligned>(ring, m, walk.row(i), i < inner_begin || i >= inner_end, i);
     }
     __syncthreads();
     float next_mean = 0.f, next_rstd = 0.f;
@@ -359,8 +385,6 @@ __global__ void __maxnreg__(128)
 #pragma unroll
     for (int i = 0; i < kPer / 2; ++i) dw[i] = db[i] = both(0.f);
     const float inv = 1.f / (float)a.cols;
-    const int inner_begin = walk.below(max(m[0].inner_begin(), m[1].inner_begin()));
-    const int inner_end = walk.below(min(m[0].inner_end(), m[1].inner_end()));
     T* dx = static_cast<T*>(a.dx) + walk.first * a.dx_stride;
     int turn = 0, slot = 0, last_slot = 0;
     uint32_t parity = 0;
@@ -421,7 +445,7 @@ __global__ void __maxnreg__(128)
             // every warp is done with this row's slot (kHold), or with that of the row before it
             const int next = it + depth - (kHold ? 0 : 1);
             if (next < walk.count && (kHold || (depth > 1 && it > 0)))
-                fill_row(ring, m, walk.row(next), kHold ? slot : last_slot);
+                fill_row<kAligned>(ring, m, walk.row(next), next < inner_begin || next >= inner_end, kHold ? slot : last_slot);
         }
         last_slot = slot;
         if (a.dx) {
@@ -446,7 +470,7 @@ __global__ void __maxnreg__(128)
         }
         if (!kHold && depth == 1) {  // the only slot: its next row can start now
             __syncthreads();
-            if (t == 0 && it + 1 < walk.count) fill_row(ring, m, walk.row(it + 1), 0);
+            if (t == 0 && it + 1 < walk.count) fill_row<kAligned>(ring, m, walk.row(it + 1), it + 1 < inner_begin || it + 1 >= inner_end, 0);
         }
         if (++slot == depth) {
             slot = 0;
