@@ -700,7 +700,9 @@ int launch_few(TileArgs& p, int sm_count, void* stream) {
 // row per CTA.  Reads dy and z, writes dz: HBM (or L2) bound.
 constexpr int kActWarps = 8, kActCols = 256;
 
-template <typename T, int kAct>
+// kWhole: the rows of dy and z start on 16-byte boundaries and hold whole
+// vectors; four rows' loads are then in flight per thread.
+template <typename T, int kAct, bool kWhole>
 __global__ void __launch_bounds__(32 * kActWarps) act_bwd_kernel(const __grid_constant__ ActBwdArgs a) {
     __shared__ float sums[kActWarps][kActCols];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -723,19 +725,42 @@ __global__ void __launch_bounds__(32 * kActWarps) act_bwd_kernel(const __grid_co
             row.gather(i, x, 0.f);
         }
     };
-    for (int64_t r = (int64_t)blockIdx.y * kActWarps + warp; r < a.rows; r += step) {
-        float g[8], z[8];
-        fetch(a.dy, a.dy_stride, r, g);
+    int64_t r = (int64_t)blockIdx.y * kActWarps + warp;
+    auto finish = [&](int64_t row, float (&g)[8], const float (&z)[8]) {
         if (kAct != SOMA_ACT_NONE) {
-            fetch(a.z, a.z_stride, r, z);
 #pragma unroll
             for (int q = 0; q < 8; ++q) g[q] *= act_slope<kAct>(z[q]);
         }
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-            if (c0 + q < a.cols) db[q] += g[q];
+            if (kWhole || c0 + q < a.cols) db[q] += g[q];
         // (dz's rows are padded to whole vectors)
-        if (a.dz && c0 < a.cols) *reinterpret_cast<uint4*>(static_cast<T*>(a.dz) + r * a.dz_stride + c0) = narrow16(g, T{});
+        if (a.dz && c0 < a.cols) *reinterpret_cast<uint4*>(static_cast<T*>(a.dz) + row * a.dz_stride + c0) = narrow16(g, T{});
+    };
+    if (kWhole && c0 < a.cols) {
+        constexpr int kAhead = 4;
+        const T *dy = static_cast<const T*>(a.dy) + c0, *z0 = static_cast<const T*>(a.z) + c0;
+        for (; r + (kAhead - 1) * step < a.rows; r += kAhead * step) {
+            uint4 u[kAhead], v[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                u[k] = *reinterpret_cast<const uint4*>(dy + (r + k * step) * a.dy_stride);
+                if (kAct != SOMA_ACT_NONE) v[k] = *reinterpret_cast<const uint4*>(z0 + (r + k * step) * a.z_stride);
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                float g[8], z[8];
+                widen16(u[k], g, T{});
+                if (kAct != SOMA_ACT_NONE) widen16(v[k], z, T{});
+                finish(r + k * step, g, z);
+            }
+        }
+    }
+    for (; r < a.rows; r += step) {
+        float g[8], z[8];
+        fetch(a.dy, a.dy_stride, r, g);
+        if (kAct != SOMA_ACT_NONE) fetch(a.z, a.z_stride, r, z);
+        finish(r, g, z);
     }
     if (!a.dbias) return;
 #pragma unroll
@@ -809,8 +834,12 @@ int launch_gemm(const GemmArgs& a, int sm_count, void* stream) {
             if (a.m <= 64) return launch_few<64, T>(p, sm_count, stream);
             return launch_few<128, T>(p, sm_count, stream);
         }
-        const int64_t big = (int64_t)((a.m + 255) / 256) * ((a.n + 255) / 256);
-        if (big * 2 >= sm_count) return launch_tile<2, 256, T>(p, sm_count, stream);
+        // A 256 x 256 tile on two SMs takes as long as a 128 x 128 tile on one
+        // (0.36 and 0.34 us per 64 k-values: the small one moves twice the
+        // operand bytes per product), so the fewer waves win.
+        const int64_t big = (int64_t)((a.m + 255) / 256) * ((a.n + 255) / 256), pairs = std::max(1, sm_count / 2);
+        const int64_t waves_big = (big + pairs - 1) / pairs, waves_small = (small + sm_count - 1) / sm_count;
+        if (waves_big < waves_small) return launch_tile<2, 256, T>(p, sm_count, stream);
         return launch_tile<1, 128, T>(p, sm_count, stream);
     });
 }
@@ -833,8 +862,12 @@ int launch_act_bwd(const ActBwdArgs& a, int sm_count, void* stream) {
         using T = decltype(t);
         const int blocks = (a.cols + kActCols - 1) / kActCols, parts = row_parts(a.rows, a.cols, sm_count);
         cudaStream_t st = (cudaStream_t)stream;
+        const bool whole = a.cols % 8 == 0 && aligned_rows(a.dy, a.dy_stride, a.rows) &&
+                           (a.act == SOMA_ACT_NONE || aligned_rows(a.z, a.z_stride, a.rows));
         with_act(a.act, [&](auto act) {
-            act_bwd_kernel<T, decltype(act)::value><<<dim3(blocks, parts), 32 * kActWarps, 0, st>>>(a);
+            constexpr int kAct = decltype(act)::value;
+            auto kernel = whole ? act_bwd_kernel<T, kAct, true> : act_bwd_kernel<T, kAct, false>;
+            kernel<<<dim3(blocks, parts), 32 * kActWarps, 0, st>>>(a);
         });
         int e = (int)cudaGetLastError();
         if (e != cudaSuccess || !a.dbias) return e;
