@@ -512,8 +512,8 @@ __global__ void __maxnreg__(128)
 }
 
 // dweight and dbias: the partial sums added in a fixed order.  A CTA takes 32
-// columns; its 16 warps take the parts in turn.
-constexpr int kJoinWarps = 16;
+// columns; its 32 warps take the parts in turn.
+constexpr int kJoinWarps = 32;
 template <typename W>
 __global__ void __launch_bounds__(32 * kJoinWarps) norm_join_kernel(const __grid_constant__ NormBwdArgs a, int parts) {
     __shared__ float scratch[2][kJoinWarps][32];

@@ -34,7 +34,7 @@ from . import SomaError, _ops_abi
 from ._abi import SOMA_DTYPE_BF16, SOMA_DTYPE_F16, SOMA_DTYPE_F32
 
 __all__ = ["layer_norm_forward", "layer_norm_backward", "linear_forward", "linear_backward", "distill_forward",
-           "distill_backward", "distill_loss_grad", "layer_norm", "linear", "distill_loss", "ACTIVATIONS"]
+           "distill_backward", "distill_loss_grad", "layer_norm", "linear", "distill_loss", "check", "ACTIVATIONS"]
 
 ACTIVATIONS = {"none": _ops_abi.SOMA_ACT_NONE, "relu": _ops_abi.SOMA_ACT_RELU, "gelu": _ops_abi.SOMA_ACT_GELU,
                "gelu_tanh": _ops_abi.SOMA_ACT_GELU_TANH, "silu": _ops_abi.SOMA_ACT_SILU}
@@ -47,6 +47,14 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 def _check(status: int):
     if status != 0:
         raise SomaError(status, _ops_abi.soma_ops_last_error().decode())
+
+
+def check(device: int = 0):
+    """Waits for the device and raises SomaError if a kernel of these operators
+    gave up waiting for its own copies since the last check (its results are
+    then not valid; a fault of the library)."""
+    _ops_abi.load()
+    _check(_ops_abi.soma_ops_check(device))
 
 
 def _on_stream(fn):
