@@ -19,7 +19,7 @@
  * memory) is in use until the call's work on `stream` is done.  Nothing is
  * allocated and nothing waits: calls enqueue on `stream` (a cudaStream_t;
  * NULL = the legacy default stream) and return, and may be captured in a CUDA
- * graph.
+ * graph (make a first call of the same kind before: it loads the kernels).
  *
  * Errors: every call returns a status of soma_opt.h; arguments are checked
  * before anything is enqueued, and soma_ops_last_error() has the detail of

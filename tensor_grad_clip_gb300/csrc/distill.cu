@@ -8,6 +8,13 @@
 // with HBM.  The teacher's entries (at most 1024) live in shared memory; one
 // warp works on them while the others stream.
 //
+// Measured (GB300, 6682 GB/s copy; 15 % of the rows do not count): 8192 x
+// 131072 bf16 forward 281 us, 6515 GB/s; backward 638 us, 6235 GB/s; loss and
+// gradient together 722 us, 5507 GB/s (914 us when the second pass re-read
+// the row through L2, which the rows in progress overflow).  2048 x 50021
+// bf16 backward, whose rows start anywhere, 103 us, 3668 GB/s: bound by the
+// instructions that shift vectors on both sides (4987 GB/s for 50024).
+//
 // A cluster of CTAs shares a row when there are fewer rows than CTAs that the
 // device holds; the CTAs' maxima and sums are joined through distributed
 // shared memory, in rank order.  Which thread takes which elements does not depend on where rows
@@ -848,9 +855,14 @@ int launch_distill(const DistillArgs& a, DistillPass pass, int sm_count, void* s
         auto aligned = [](const void* p, int64_t stride) {
             return (uintptr_t)p % 16 == 0 && stride * (int64_t)sizeof(T) % 16 == 0;
         };
+        // The ring for rows that start on 16-byte boundaries, are longer than 32
+        // KB and come at least four to an SM: 4000 rows of 32000 fp32 take 168 to
+        // 192 us with it and 214 without.  Unaligned rows would pay the shifting
+        // with a third of the threads (239 us against 175 for 2000 x 50021 fp16).
         if (pass == kDistillLossGrad && a.rows >= 4 * sm_count && (int64_t)a.vocab * (int)sizeof(T) > 32768 &&
             aligned(a.logits, a.logits_stride) && aligned(a.dlogits, a.dlogits_stride))
             return launch_ring<T>(a, sm_count, (cudaStream_t)stream);
+        // short rows: 16000 x 2000 bf16 in one call 89 us with 128 threads, 214 with 512
         if ((int64_t)a.vocab * (int)sizeof(T) <= 32768) return launch_rows<T, 128>(a, pass, sm_count, (cudaStream_t)stream);
         return launch_rows<T, 512>(a, pass, sm_count, (cudaStream_t)stream);
     });

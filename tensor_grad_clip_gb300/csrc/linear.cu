@@ -1,5 +1,18 @@
 // Linear layer: matrix products with their epilogue, and the activation's
 // backward pass (formulas in soma_ops.h).
+//
+// Many rows are bound by the tensor cores: 256 x 256 tiles on CTA pairs, 64
+// k-values per pipeline stage, operands by TMA, two accumulators in TMEM so
+// that a tile's epilogue (bias, activation, residual, rounding) runs under the
+// next tile's products.  Few rows are bound by reading the weight: there its
+// rows are the tile's, and k is split over a cluster so that every SM reads.
+// Operands may run along k or across it, so no product needs a transpose.
+//
+// Measured (GB300, cuBLAS bf16 1924 TFLOP/s in a burst): 16384 x 4096 x 11008
+// bf16 with residual 815 us, 1813 TFLOP/s; 4096 x 4096 x 1024 with gelu and
+// saved pre-activation 32.6 us, 1053 TFLOP/s (3.4 waves of tiles whose
+// epilogue is as long as their products); its three gradients in fp16 74 us,
+// 925 TFLOP/s; one row through 11008 x 4096 18.1 us, 4990 GB/s.
 #include <cuda.h>
 #include <math.h>
 
@@ -299,8 +312,8 @@ __device__ __forceinline__ void epilogue(const TileArgs& p, uint32_t acc, int ro
     }
 }
 
-// Persistent: cluster i takes tiles i, i + clusters, ...  Warps 0-7 drain
-// accumulators, warp 8 loads operands, warp 9 issues the MMAs; two
+// Persistent: cluster i takes units i, i + clusters, ...  Warps 0-15 drain
+// accumulators, the next loads operands, the last issues the MMAs; two
 // accumulators in TMEM let a tile's epilogue run under the next tile's MMAs.
 // CG = 2: a pair of CTAs shares one 256-row tile, each staging half of both
 // operands; the leader (rank 0) issues the MMAs for both.

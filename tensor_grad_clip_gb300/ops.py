@@ -60,7 +60,8 @@ def check(device: int = 0):
 def _on_stream(fn):
     """Gives an operator its `stream` argument: the call runs with that stream current."""
     @functools.wraps(fn)
-    def call(*args, stream=None, **kwargs):
+    def call(*args, **kwargs):
+        stream = kwargs.pop("stream", None) if kwargs else None
         if stream is None:
             return fn(*args, **kwargs)
         tensors = [t for t in (*args, *kwargs.values()) if isinstance(t, torch.Tensor)]
@@ -84,8 +85,6 @@ def _code(t, name, among=_CODE) -> int:
 
 def _matrix(t, name):
     """t as [rows, last], without a copy."""
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA tensor")
     if t.dim() != 2:
         if t.dim() == 0:
             raise ValueError(f"{name}: expected at least one dimension")
@@ -99,6 +98,8 @@ def _matrix(t, name):
                 t = t.view(rows, last)
             except RuntimeError:
                 raise ValueError(f"{name}: its leading dimensions are not evenly spaced rows") from None
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
     if t.stride(1) != 1 and t.shape[1] > 1 and t.shape[0] > 0:
         raise ValueError(f"{name}: the last dimension must have unit stride")
     return t
@@ -143,6 +144,41 @@ def _empty_rows(like, shape):
 
 def _workspace(nbytes, device):
     return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+# Workspace sizes depend on sizes and alignment alone: asked once per combination.
+
+def _unaligned(t) -> bool:
+    """Whether a 16-bit matrix has rows that do not start on 16-byte boundaries."""
+    return t.data_ptr() % 16 != 0 or (t.stride(0) % 8 != 0 and t.shape[0] > 1)
+
+
+def _operand(unaligned: bool, cols: int):
+    """(address, stride) of some matrix with aligned or unaligned rows, to ask for sizes with."""
+    return (2, cols) if unaligned else (16, (cols + 7) // 8 * 8)
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_bytes(dev, rows, cols):
+    need = ctypes.c_int64()
+    _check(_ops_abi.soma_layer_norm_backward_workspace(dev, rows, cols, ctypes.byref(need)))
+    return need.value
+
+
+@functools.lru_cache(maxsize=1024)
+def _linear_forward_bytes(dev, m, n, k, dt, x, w):
+    need = ctypes.c_int64()
+    _check(_ops_abi.soma_linear_forward_workspace(dev, *_operand(x, k), *_operand(w, k), m, n, k, dt,
+                                                  ctypes.byref(need)))
+    return need.value
+
+
+@functools.lru_cache(maxsize=1024)
+def _linear_backward_bytes(dev, m, n, k, dt, act, dy, x, w):
+    need = ctypes.c_int64()
+    _check(_ops_abi.soma_linear_backward_workspace(dev, *_operand(dy, n), *_operand(x, k), *_operand(w, k), m, n, k,
+                                                   dt, act, ctypes.byref(need)))
+    return need.value
 
 
 def _ptr(t):
@@ -199,9 +235,7 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, input_grad: bool = True, w
     if weight is not None and (weight_grad or bias_grad):
         dweight = torch.empty_like(weight) if weight_grad else None
         dbias = torch.empty_like(weight) if bias_grad else None
-        need = ctypes.c_int64()
-        _check(_ops_abi.soma_layer_norm_backward_workspace(dev, rows, cols, ctypes.byref(need)))
-        work = _workspace(need.value, x.device)
+        work = _workspace(_norm_bytes(dev, rows, cols), x.device)
     _check(_ops_abi.soma_layer_norm_backward(dev, dy2.data_ptr(), dy2.stride(0), x2.data_ptr(), x2.stride(0), w, m, r,
                                              _ptr(dx2), dx2.stride(0) if dx2 is not None else 0, _ptr(dweight),
                                              _ptr(dbias), _ptr(work), work.numel() if work is not None else 0, rows,
@@ -241,13 +275,11 @@ def linear_forward(x, weight, bias=None, *, activation: str = "none", residual=N
     y = torch.empty(shape, dtype=x.dtype, device=x.device)
     z = torch.empty_like(y) if save_preactivation else None
     dev = x.device.index
-    need = ctypes.c_int64()
-    _check(_ops_abi.soma_linear_forward_workspace(dev, x2.data_ptr(), x2.stride(0), w2.data_ptr(), w2.stride(0), m, n,
-                                                  k, dt, ctypes.byref(need)))
-    work = _workspace(need.value, x.device)
+    need = _linear_forward_bytes(dev, m, n, k, dt, _unaligned(x2), _unaligned(w2))
+    work = _workspace(need, x.device)
     _check(_ops_abi.soma_linear_forward(dev, x2.data_ptr(), x2.stride(0), w2.data_ptr(), w2.stride(0), b, _ptr(r2),
                                         r2.stride(0) if r2 is not None else 0, y.data_ptr(), n, _ptr(z), n,
-                                        _ptr(work), need.value, m, n, k, dt, act, _raw_stream(dev)))
+                                        _ptr(work), need, m, n, k, dt, act, _raw_stream(dev)))
     return (y, z) if save_preactivation else y
 
 
@@ -277,14 +309,11 @@ def linear_backward(dy, x, weight, preactivation=None, *, activation: str = "non
     dw = torch.empty((n, k), dtype=x.dtype, device=x.device) if weight_grad else None
     db = torch.empty(n, dtype=x.dtype, device=x.device) if bias_grad else None
     dev = x.device.index
-    need = ctypes.c_int64()
-    _check(_ops_abi.soma_linear_backward_workspace(dev, dy2.data_ptr(), dy2.stride(0), x2.data_ptr(), x2.stride(0),
-                                                   w2.data_ptr(), w2.stride(0), m, n, k, dt, act,
-                                                   ctypes.byref(need)))
-    work = _workspace(need.value, x.device)
+    need = _linear_backward_bytes(dev, m, n, k, dt, act, _unaligned(dy2), _unaligned(x2), _unaligned(w2))
+    work = _workspace(need, x.device)
     _check(_ops_abi.soma_linear_backward(dev, dy2.data_ptr(), dy2.stride(0), x2.data_ptr(), x2.stride(0),
                                          w2.data_ptr(), w2.stride(0), _ptr(z2), z2.stride(0) if z2 is not None else 0,
-                                         _ptr(dx), k, _ptr(dw), k, _ptr(db), _ptr(work), need.value, m, n, k, dt, act,
+                                         _ptr(dx), k, _ptr(dw), k, _ptr(db), _ptr(work), need, m, n, k, dt, act,
                                          _raw_stream(dev)))
     return dx, dw, db
 
