@@ -176,6 +176,7 @@ struct TileArgs {
     CUtensorMap a, b, out, z;
     GemmArgs g;
     int32_t tiles_m, tiles_n;
+    int32_t strip;         // columns of tiles that are walked through together
     int32_t whole;         // tiles from this one on are done in two halves of their columns
     bool tma_out, tma_z;   // rows of out / z start on 16-byte boundaries
 };
@@ -366,8 +367,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
     auto tile_at = [&](int u, int& row0, int& col0) {  // returns the unit's columns
         const bool half = u >= p.whole;
         const int t = half ? p.whole + (u - p.whole) / 2 : u;
-        col0 = t % p.tiles_n * BN + (half && (u - p.whole) % 2 ? BN / 2 : 0);
-        row0 = t / p.tiles_n * (kBM * CG) + (int)rank * kBM;
+        const int strip = t / (p.tiles_m * p.strip) * p.strip, width = min(p.strip, p.tiles_n - strip);
+        const int in_strip = t - strip * p.tiles_m;
+        col0 = (strip + in_strip % width) * BN + (half && (u - p.whole) % 2 ? BN / 2 : 0);
+        row0 = in_strip / width * (kBM * CG) + (int)rank * kBM;
         return half ? BN / 2 : BN;
     };
 
@@ -690,6 +693,13 @@ int launch_tile(TileArgs& p, int sm_count, void* stream) {
     p.tiles_n = (g.n + BN - 1) / BN;
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, workers = std::max(1, sm_count / CG);
     if (tiles > (1 << 29)) return cudaErrorInvalidValue;
+    // Strips of columns of B of at most 48 MB, which stay in L2 while A passes,
+    // are done one after another: 8192^3 605 us instead of 643 in one strip,
+    // 16384 x 4096 x 11008 822 instead of 830 (ncu had 1.9 GB read there for
+    // 0.6 GB of operands).
+    const int64_t fit = std::max<int64_t>(1, (48ll << 20) / ((int64_t)BN * g.k * 2));
+    const int64_t strips = (p.tiles_n + fit - 1) / fit;
+    p.strip = (int32_t)((p.tiles_n + strips - 1) / strips);
     // a last wave that at most half of the workers have is done in half tiles by all
     const int64_t rest = tiles % workers;
     p.whole = (int32_t)(CG == 2 && 2 * rest <= workers ? tiles - rest : tiles);
