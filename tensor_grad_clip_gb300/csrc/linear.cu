@@ -11,8 +11,8 @@
 // Measured (GB300, cuBLAS bf16 1924 TFLOP/s in a burst): 16384 x 4096 x 11008
 // bf16 with residual 815 us, 1813 TFLOP/s; 4096 x 4096 x 1024 with gelu and
 // saved pre-activation 32.6 us, 1053 TFLOP/s (3.4 waves of tiles whose
-// epilogue is as long as their products); its three gradients in fp16 74 us,
-// 925 TFLOP/s; one row through 11008 x 4096 18.1 us, 4990 GB/s.
+// epilogue is as long as their products); its three gradients in fp16 71.5 us,
+// 962 TFLOP/s; one row through 11008 x 4096 18.1 us, 4990 GB/s.
 #include <cuda.h>
 #include <math.h>
 
@@ -164,12 +164,41 @@ __device__ __forceinline__ void follow_stream() {
 }
 
 // Copies an operand into rows that start on 16-byte boundaries, as TMA needs.
+// A thread shifts whole vectors into place, four rows in flight; the new
+// rows' padding is 0.  (T: either 16-bit type, for its size.)
+constexpr int kRepackRows = 4;
 template <typename T>
 __global__ void __launch_bounds__(256) repack_kernel(const T* src, int64_t src_stride, T* dst, int64_t dst_stride,
                                                      int64_t rows, int32_t cols) {
-    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y)
-        for (int c = blockIdx.x * 256 + threadIdx.x; c < cols; c += gridDim.x * 256)
-            dst[r * dst_stride + c] = src[r * src_stride + c];
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    if (i * 8 >= cols) return;
+    const int64_t step = gridDim.y;
+    for (int64_t r0 = blockIdx.y; r0 < rows; r0 += kRepackRows * step) {
+        uint4 u[kRepackRows], v[kRepackRows];
+        int phase[kRepackRows];
+#pragma unroll
+        for (int k = 0; k < kRepackRows; ++k) {
+            const int64_t r = r0 + k * step;
+            if (r >= rows) break;
+            const RowReader<T, false> row(src, src_stride, rows, r, cols);
+            phase[k] = -1;
+            if (i >= row.inner_begin && i < row.inner_end) {
+                phase[k] = row.phase;
+                u[k] = row.words[i];
+                if (row.phase) v[k] = row.words[i + 1];
+            } else {
+                float x[8];
+                row.gather(i, x, 0.f);
+                u[k] = narrow16(x, T{});
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kRepackRows; ++k) {
+            const int64_t r = r0 + k * step;
+            if (r >= rows) break;
+            reinterpret_cast<uint4*>(dst + r * dst_stride)[i] = phase[k] > 0 ? shifted<T>(u[k], v[k], phase[k]) : u[k];
+        }
+    }
 }
 
 struct TileArgs {
@@ -744,20 +773,27 @@ __global__ void __launch_bounds__(32 * kActWarps) act_bwd_kernel(const __grid_co
     const int i = blockIdx.x * 32 + lane, c0 = i * 8;  // this lane's vector
     const int64_t step = (int64_t)gridDim.y * kActWarps;
     float db[8] = {};
-    auto fetch = [&](const void* base, int64_t stride, int64_t r, float (&x)[8]) {
+    struct Raw {
+        uint4 u, v;
+        int phase;  // -1: u is the vector itself
+    };
+    auto fetch = [&](const void* base, int64_t stride, int64_t r) {
         const RowReader<T, false> row(static_cast<const T*>(base), stride, a.rows, r, a.cols);
+        Raw raw;
+        raw.phase = -1;
         if (i >= row.inner_begin && i < row.inner_end) {
-            uint4 u[1], v[1];
-            if (row.phase) {
-                row.template load<true, 1>(i, 0, u, v);
-                row.template widen<true>(u[0], v[0], x);
-            } else {
-                row.template load<false, 1>(i, 0, u, v);
-                row.template widen<false>(u[0], v[0], x);
-            }
+            raw.phase = row.phase;
+            raw.u = row.words[i];
+            if (row.phase) raw.v = row.words[i + 1];
         } else {
+            float x[8];
             row.gather(i, x, 0.f);
+            raw.u = narrow16(x, T{});
         }
+        return raw;
+    };
+    auto expand = [](const Raw& raw, float (&x)[8]) {
+        widen16(raw.phase > 0 ? shifted<T>(raw.u, raw.v, raw.phase) : raw.u, x, T{});
     };
     int64_t r = (int64_t)blockIdx.y * kActWarps + warp;
     auto finish = [&](int64_t row, float (&g)[8], const float (&z)[8]) {
@@ -790,11 +826,23 @@ __global__ void __launch_bounds__(32 * kActWarps) act_bwd_kernel(const __grid_co
             }
         }
     }
-    for (; r < a.rows; r += step) {
-        float g[8], z[8];
-        fetch(a.dy, a.dy_stride, r, g);
-        if (kAct != SOMA_ACT_NONE) fetch(a.z, a.z_stride, r, z);
-        finish(r, g, z);
+    for (; r < a.rows; r += 2 * step) {
+        const bool second = r + step < a.rows;
+        Raw dy[2], zr[2];
+        dy[0] = fetch(a.dy, a.dy_stride, r);
+        if (kAct != SOMA_ACT_NONE) zr[0] = fetch(a.z, a.z_stride, r);
+        if (second) {
+            dy[1] = fetch(a.dy, a.dy_stride, r + step);
+            if (kAct != SOMA_ACT_NONE) zr[1] = fetch(a.z, a.z_stride, r + step);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (k && !second) break;
+            float g[8], z[8];
+            expand(dy[k], g);
+            if (kAct != SOMA_ACT_NONE) expand(zr[k], z);
+            finish(r + k * step, g, z);
+        }
     }
     if (!a.dbias) return;
 #pragma unroll
@@ -843,12 +891,14 @@ int with_type16(int dtype, F&& f) {
 bool gemm_operand_needs_copy(const void* p, int64_t stride, int64_t rows) { return !aligned_rows(p, stride, rows); }
 
 int launch_repack(const void* src, int64_t src_stride, void* dst, int64_t dst_stride, int64_t rows, int64_t cols,
-                  void* stream) {
-    const dim3 grid((unsigned)std::min<int64_t>((cols + 255) / 256, 64), (unsigned)std::min<int64_t>(rows, 2048));
-    repack_kernel<uint16_t><<<grid, 256, 0, (cudaStream_t)stream>>>(static_cast<const uint16_t*>(src), src_stride,
-                                                                   static_cast<uint16_t*>(dst), dst_stride, rows,
-                                                                   (int32_t)cols);
-    return (int)cudaGetLastError();
+                  int dtype, int sm_count, void* stream) {
+    const unsigned blocks = (unsigned)((cols + 2047) / 2048);
+    const int64_t by_rows = (rows + kRepackRows - 1) / kRepackRows;
+    const dim3 grid(blocks, (unsigned)std::max<int64_t>(1, std::min<int64_t>(by_rows, 8 * (int64_t)sm_count / blocks)));
+    auto kernel = dtype == kBF16 ? (const void*)repack_kernel<__nv_bfloat16> : (const void*)repack_kernel<__half>;
+    int32_t n = (int32_t)cols;
+    void* args[] = {&src, &src_stride, &dst, &dst_stride, &rows, &n};
+    return (int)cudaLaunchKernel(kernel, grid, dim3(256), args, 0, (cudaStream_t)stream);
 }
 
 int launch_gemm(const GemmArgs& a, int sm_count, void* stream) {

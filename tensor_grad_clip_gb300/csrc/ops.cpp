@@ -118,10 +118,10 @@ struct Operand {
         : p(q), stride(s), rows(r), cols(c), copy(soma::gemm_operand_needs_copy(q, s, r)) {}
     int64_t bytes() const { return copy ? align256(rows * ((cols + 7) / 8 * 8) * 2) : 0; }
     // Enqueues the copy, if any, and advances the workspace past it.
-    int place(char*& workspace, void* stream) {
+    int place(char*& workspace, int dtype, int sms, void* stream) {
         if (!copy) return cudaSuccess;
         const int64_t to = (cols + 7) / 8 * 8;
-        const int e = soma::launch_repack(p, stride, workspace, to, rows, cols, stream);
+        const int e = soma::launch_repack(p, stride, workspace, to, rows, cols, dtype, sms, stream);
         p = workspace;
         stride = to;
         workspace += align256(rows * to * 2);
@@ -349,8 +349,8 @@ soma_status_t soma_linear_forward(int32_t device, const void* x, int64_t x_strid
     SOMA_TRY(check_workspace(workspace, workspace_bytes, a.bytes() + b.bytes()));
     SOMA_ON_DEVICE(device);
     char* ws = static_cast<char*>(workspace);
-    int e = a.place(ws, stream);
-    if (e == cudaSuccess) e = b.place(ws, stream);
+    int e = a.place(ws, dtype, sms, stream);
+    if (e == cudaSuccess) e = b.place(ws, dtype, sms, stream);
     if (e == cudaSuccess)
         e = soma::launch_gemm({a.p, a.stride, true, b.p, b.stride, true, bias, residual, residual_stride, y, y_stride,
                                z_out, z_stride, (int32_t)m, (int32_t)n, (int32_t)k, dtype, activation},
@@ -414,12 +414,12 @@ soma_status_t soma_linear_backward(int32_t device, const void* dy, int64_t dy_st
             ws = dz + align256(m * dz_stride * 2);
         }
     }
-    if (dx && e == cudaSuccess) e = b.place(ws, stream);
+    if (dx && e == cudaSuccess) e = b.place(ws, dtype, sms, stream);
     if (dx && e == cudaSuccess)
         e = soma::launch_gemm({g.p, g.stride, true, b.p, b.stride, false, nullptr, nullptr, 0, dx, dx_stride, nullptr, 0,
                                (int32_t)m, (int32_t)k, (int32_t)n, dtype, SOMA_ACT_NONE},
                               sms, stream);
-    if (dweight && e == cudaSuccess) e = a.place(ws, stream);
+    if (dweight && e == cudaSuccess) e = a.place(ws, dtype, sms, stream);
     if (dweight && e == cudaSuccess)
         e = soma::launch_gemm({g.p, g.stride, false, a.p, a.stride, false, nullptr, nullptr, 0, dweight, dweight_stride,
                                nullptr, 0, (int32_t)n, (int32_t)k, (int32_t)m, dtype, SOMA_ACT_NONE},

@@ -78,7 +78,7 @@ int launch_gemm(const GemmArgs& a, int sm_count, void* stream);
 // boundaries (needs_copy) are first copied into rows that do.
 bool gemm_operand_needs_copy(const void* p, int64_t stride, int64_t rows);
 int launch_repack(const void* src, int64_t src_stride, void* dst, int64_t dst_stride, int64_t rows, int64_t cols,
-                  void* stream);
+                  int dtype, int sm_count, void* stream);
 
 // dz = dy * act'(z) (dz == nullptr: not stored), and dbias = column sums of
 // the unrounded dz (dbias == nullptr: not wanted).
