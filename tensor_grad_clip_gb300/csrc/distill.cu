@@ -53,11 +53,6 @@ __device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b, float c) {
     return {m, a.s * exp2f((a.m - m) * c) + b.s * exp2f((b.m - m) * c)};
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
 __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
