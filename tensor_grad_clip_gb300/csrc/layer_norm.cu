@@ -218,14 +218,16 @@ __device__ __forceinline__ void group_sync(int group, int warps) {
     else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(warps * 32) : "memory");
 }
 
-// kPer elements per thread; a row belongs to a warp (kOneWarp) or to all
-// consumer warps of the CTA.
+// kPer elements per thread; a row belongs to a warp, to two (kWarps) or to all
+// warps of the CTA (kWarps = 0).
 //
 // The statistics take one pass over the thread's elements and one reduction:
 // sums of d = x - k and of d^2, with k the average of four elements in
 // the middle of the row, which every thread reads.  The variance is then
 // sum d^2 / n - (sum d / n)^2, which loses a few bits when the mean is far
-// from k; where (mean - k)^2 > 4 var, the sum of (x - mean)^2 is taken instead.
+// from k, and d itself is rounded at the size of k.  So where (mean - k)^2 >
+// 4 var (a large channel among the four), both sums are taken again from the
+// row in shared memory with k the mean that the first pass found.
 template <typename T, int kPer, bool kAligned, int kWarps>
 __global__ void __maxnreg__(kPer == 32 ? 128 : kWarps ? 96 : 80)
     norm_fwd_kernel(const __grid_constant__ NormFwdArgs a, int depth, int slot_bytes) {
@@ -280,46 +282,39 @@ __global__ void __maxnreg__(kPer == 32 ? 128 : kWarps ? 96 : 80)
             k *= inv_middle;
         }
         float2 d[kPer / 2];
-        float2 sum = both(0.f), square = both(0.f);
-#pragma unroll
-        for (int p = 0; p < kPieces; ++p) {
-            const int c = (p * threads + t) * kVec;
-            float e[kVec];
-            if (c < a.cols) widen16(slot_vector<T, kAligned>(window, c, phase), e, T{});
-#pragma unroll
-            for (int i = 0; i < kVec / 2; ++i) d[p * kVec / 2 + i] = add2(make_float2(e[2 * i], e[2 * i + 1]), both(-k));
-            if (c + kVec > a.cols) {
-#pragma unroll
-                for (int i = 0; i < kVec / 2; ++i) {
-                    if (c + 2 * i >= a.cols) d[p * kVec / 2 + i].x = 0.f;
-                    if (c + 2 * i + 1 >= a.cols) d[p * kVec / 2 + i].y = 0.f;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kVec / 2; ++i) {
-                sum = add2(sum, d[p * kVec / 2 + i]);
-                square = fma2(d[p * kVec / 2 + i], d[p * kVec / 2 + i], square);
-            }
-        }
-        const float2 s = row_totals<kWarps>(sum.x + sum.y, square.x + square.y, scratch, group, warps, turn);
-        // (every thread has its part of the row in registers now)
-        if (t == 0 && it + depth < walk.count) fill_row<kAligned>(ring, x, walk.row(it + depth), it + depth >= inner_end || it + depth < inner_begin, slot);
-        const float shift = s.x * inv;
-        float var = fmaf(-shift, shift, s.y * inv);
-        if (shift * shift > 4.f * var) {  // the same for all threads of the row
-            square = both(0.f);
+        float shift, var;
+#pragma unroll 1
+        for (bool again = false;; again = true) {
+            float2 sum = both(0.f), square = both(0.f);
 #pragma unroll
             for (int p = 0; p < kPieces; ++p) {
                 const int c = (p * threads + t) * kVec;
+                float e[kVec];
+                if (c < a.cols) widen16(slot_vector<T, kAligned>(window, c, phase), e, T{});
 #pragma unroll
-                for (int i = 0; i < kVec; ++i) {
-                    const float2& at = d[p * kVec / 2 + i / 2];
-                    const float e = c + i < a.cols ? (i % 2 ? at.y : at.x) - shift : 0.f;
-                    square.x = fmaf(e, e, square.x);
+                for (int i = 0; i < kVec / 2; ++i) d[p * kVec / 2 + i] = add2(make_float2(e[2 * i], e[2 * i + 1]), both(-k));
+                if (c + kVec > a.cols) {
+#pragma unroll
+                    for (int i = 0; i < kVec / 2; ++i) {
+                        if (c + 2 * i >= a.cols) d[p * kVec / 2 + i].x = 0.f;
+                        if (c + 2 * i + 1 >= a.cols) d[p * kVec / 2 + i].y = 0.f;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kVec / 2; ++i) {
+                    sum = add2(sum, d[p * kVec / 2 + i]);
+                    square = fma2(d[p * kVec / 2 + i], d[p * kVec / 2 + i], square);
                 }
             }
-            var = row_totals<kWarps>(square.x, 0.f, scratch, group, warps, turn).x * inv;
+            const float2 s = row_totals<kWarps>(sum.x + sum.y, square.x + square.y, scratch, group, warps, turn);
+            shift = s.x * inv;
+            var = fmaf(-shift, shift, s.y * inv);
+            if (again || !(shift * shift > 4.f * var)) break;  // (the same for all threads of the row)
+            k += shift;
         }
+        if (var < 0.f) var = 0.f;  // (the rounding of a constant row)
+        // (every thread has its part of the row in registers now)
+        if (t == 0 && it + depth < walk.count) fill_row<kAligned>(ring, x, walk.row(it + depth), it + depth >= inner_end || it + depth < inner_begin, slot);
         const float rstd = rsqrtf(var + a.eps);
         const int out_phase = kAligned ? 0 : (int)((uintptr_t)y & 15);
         const float2 scale = both(rstd), offset = both(-shift * rstd);
