@@ -12,7 +12,7 @@
 //   up to 16384           a CTA (16 or 32 elements per thread)
 //   more                  a CTA of 256 threads that re-reads it through L2
 //
-// Measured (GB300, 6682 GB/s copy): 16384 x 4096 bf16 forward 50.9 us, 5274
+// Measured (GB300, 6682 GB/s copy): 16384 x 4096 bf16 forward 51.5 us, 5213
 // GB/s; backward 82.1 us, 4909 GB/s; fp32 backward 133 us, 6064 GB/s; 16381 x
 // 4099 fp16 (padded rows) backward 124 us, 3249 GB/s.  The 16-bit passes are
 // bound by the latency of a row's chain (copy, statistics over the CTA,
@@ -226,8 +226,12 @@ __device__ __forceinline__ void group_sync(int group, int warps) {
 // the middle of the row, which every thread reads.  The variance is then
 // sum d^2 / n - (sum d / n)^2, which loses a few bits when the mean is far
 // from k, and d itself is rounded at the size of k.  So where (mean - k)^2 >
-// 4 var (a large channel among the four), both sums are taken again from the
-// row in shared memory with k the mean that the first pass found.
+// 4 var, as with a large channel among the four, both sums are taken again
+// with k the mean that the first pass found.  The thread keeps its x for that,
+// and forms x - k once more for the output: 16384 x 4096 bf16 51.5 us (66 where
+// every row has such a channel), 8192 x 4096 fp32 49.7 (51).  With x - k kept
+// and the row read again from its slot or from L2 they took 52.5 (73) and 50
+// (51), or 52 (92) and 47 (74).
 template <typename T, int kPer, bool kAligned, int kWarps>
 __global__ void __maxnreg__(kPer == 32 ? 128 : kWarps ? 96 : 80)
     norm_fwd_kernel(const __grid_constant__ NormFwdArgs a, int depth, int slot_bytes) {
@@ -281,55 +285,64 @@ __global__ void __maxnreg__(kPer == 32 ? 128 : kWarps ? 96 : 80)
             else if (middle_n > 1) k += middle_n > 2 ? e[1] + e[2] : e[1];
             k *= inv_middle;
         }
-        float2 d[kPer / 2];
-        float shift, var;
-#pragma unroll 1
-        for (bool again = false;; again = true) {
+        float2 e[kPer / 2];
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p) {
+            const int c = (p * threads + t) * kVec;
+            float v[kVec];
+            if (c < a.cols) widen16(slot_vector<T, kAligned>(window, c, phase), v, T{});
+#pragma unroll
+            for (int i = 0; i < kVec / 2; ++i) e[p * kVec / 2 + i] = make_float2(v[2 * i], v[2 * i + 1]);
+        }
+        auto totals = [&] {  // of x - k and its square over the row
             float2 sum = both(0.f), square = both(0.f);
 #pragma unroll
             for (int p = 0; p < kPieces; ++p) {
                 const int c = (p * threads + t) * kVec;
-                float e[kVec];
-                if (c < a.cols) widen16(slot_vector<T, kAligned>(window, c, phase), e, T{});
+                float2 d[kVec / 2];
 #pragma unroll
-                for (int i = 0; i < kVec / 2; ++i) d[p * kVec / 2 + i] = add2(make_float2(e[2 * i], e[2 * i + 1]), both(-k));
+                for (int i = 0; i < kVec / 2; ++i) d[i] = add2(e[p * kVec / 2 + i], both(-k));
                 if (c + kVec > a.cols) {
 #pragma unroll
                     for (int i = 0; i < kVec / 2; ++i) {
-                        if (c + 2 * i >= a.cols) d[p * kVec / 2 + i].x = 0.f;
-                        if (c + 2 * i + 1 >= a.cols) d[p * kVec / 2 + i].y = 0.f;
+                        if (c + 2 * i >= a.cols) d[i].x = 0.f;
+                        if (c + 2 * i + 1 >= a.cols) d[i].y = 0.f;
                     }
                 }
 #pragma unroll
                 for (int i = 0; i < kVec / 2; ++i) {
-                    sum = add2(sum, d[p * kVec / 2 + i]);
-                    square = fma2(d[p * kVec / 2 + i], d[p * kVec / 2 + i], square);
+                    sum = add2(sum, d[i]);
+                    square = fma2(d[i], d[i], square);
                 }
             }
-            const float2 s = row_totals<kWarps>(sum.x + sum.y, square.x + square.y, scratch, group, warps, turn);
-            shift = s.x * inv;
-            var = fmaf(-shift, shift, s.y * inv);
-            if (again || !(shift * shift > 4.f * var)) break;  // (the same for all threads of the row)
-            k += shift;
-        }
-        if (var < 0.f) var = 0.f;  // (the rounding of a constant row)
+            return row_totals<kWarps>(sum.x + sum.y, square.x + square.y, scratch, group, warps, turn);
+        };
+        float2 s = totals();
         // (every thread has its part of the row in registers now)
         if (t == 0 && it + depth < walk.count) fill_row<kAligned>(ring, x, walk.row(it + depth), it + depth >= inner_end || it + depth < inner_begin, slot);
+        float shift = s.x * inv, var = fmaf(-shift, shift, s.y * inv);
+        if (shift * shift > 4.f * var) {  // the same for all threads of the row
+            k += shift;
+            s = totals();
+            shift = s.x * inv;
+            var = fmaf(-shift, shift, s.y * inv);
+            if (var < 0.f) var = 0.f;  // (the rounding of a constant row)
+        }
         const float rstd = rsqrtf(var + a.eps);
         const int out_phase = kAligned ? 0 : (int)((uintptr_t)y & 15);
         const float2 scale = both(rstd), offset = both(-shift * rstd);
 #pragma unroll
         for (int p = 0; p < kPieces; ++p) {
-            float e[kVec];
+            float out[kVec];
 #pragma unroll
             for (int i = 0; i < kVec / 2; ++i) {
                 const int j = p * kVec + 2 * i;
-                const float2 xh = fma2(d[p * kVec / 2 + i], scale, offset);
+                const float2 xh = fma2(add2(e[p * kVec / 2 + i], both(-k)), scale, offset);
                 const float2 v = fma2(xh, make_float2(w[j], w[j + 1]), make_float2(b[j], b[j + 1]));
-                e[2 * i] = v.x;
-                e[2 * i + 1] = v.y;
+                out[2 * i] = v.x;
+                out[2 * i + 1] = v.y;
             }
-            store_vector<T, kAligned>(y, (p * threads + t) * kVec, a.cols, out_phase, e);
+            store_vector<T, kAligned>(y, (p * threads + t) * kVec, a.cols, out_phase, out);
         }
         if (t == 0) {
             if (a.mean) a.mean[walk.row(it)] = k + shift;
