@@ -407,7 +407,7 @@ __global__ void __maxnreg__(128)
     int turn = 0, slot = 0, last_slot = 0;
     uint32_t parity = 0;
     for (int it = 0; it < walk.count; ++it, dx += walk.step * a.dx_stride) {
-        const float rstd = next_rstd, offset = -next_mean * next_rstd;
+        const float rstd = next_rstd, mean = next_mean;
         if (it + 1 < walk.count) {
             next_mean = a.mean[walk.row(it + 1)];
             next_rstd = a.rstd[walk.row(it + 1)];
@@ -421,7 +421,9 @@ __global__ void __maxnreg__(128)
         }
         const int phase_x = kAligned ? 0 : m[0].phase(walk.row(it)), phase_dy = kAligned ? 0 : m[1].phase(walk.row(it));
         float2 xh[kHold ? kPer / 2 : kVec / 2], g[kHold ? kPer / 2 : kVec / 2];
-        // xh and dy of piece p (0 past the row's end), and its weights
+        // xh and dy of piece p (0 past the row's end), and its weights.  x - mean
+        // before the product: x rstd - mean rstd would cancel where the mean is
+        // many standard deviations from 0.
         auto take = [&](int p, float2* to_xh, float2* to_dy) {
             const int c = (p * threads + t) * kVec;
             float ex[kVec], ed[kVec];
@@ -431,7 +433,7 @@ __global__ void __maxnreg__(128)
             }
 #pragma unroll
             for (int i = 0; i < kVec / 2; ++i) {
-                to_xh[i] = fma2(make_float2(ex[2 * i], ex[2 * i + 1]), both(rstd), both(offset));
+                to_xh[i] = mul2(add2(make_float2(ex[2 * i], ex[2 * i + 1]), both(-mean)), both(rstd));
                 to_dy[i] = make_float2(ed[2 * i], ed[2 * i + 1]);
             }
             if (c + kVec > a.cols) {

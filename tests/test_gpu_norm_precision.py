@@ -35,3 +35,21 @@ def test_large_channels_in_the_middle(ops, cols, pad, dtype):
         x[1, cols // 2 - 2:cols // 2 + 3] = size  # several of them
         check_forward(ops, x)
         check_forward(ops, x + 50)
+
+
+@pytest.mark.parametrize("cols", [300, 1000, 4096, 4099, 16384, 20000])
+@pytest.mark.parametrize("dtype,mean", [(torch.float32, 1e3), (torch.float32, 1e4), (torch.bfloat16, 100.0)])
+def test_gradient_of_rows_far_from_zero(ops, cols, dtype, mean):
+    gen = torch.Generator(device="cuda").manual_seed(cols)
+    x = (torch.randn(37, cols, device="cuda", generator=gen) + mean).to(dtype)
+    w = torch.rand(cols, device="cuda", generator=gen) + 0.5
+    _, mu, rstd = ops.layer_norm_forward(x, w)
+    xh = (x.double() - mu.double()[:, None]) * rstd.double()[:, None]
+    dy = (xh + torch.randn(37, cols, device="cuda", generator=gen)).to(dtype)  # mean(g xh) is about 1
+    dx, dw, db = ops.layer_norm_backward(dy, x, w, mu, rstd)
+    rdx, rdw, rdb = R.norm_backward(dy, x, w, mu, rstd)
+    # x - mean rounds to 2^-24 of itself and so does its product with rstd: the errors of xh go with |xh|, not with
+    # |x| + |mean| (centred x and a mean of 0 give such bounds)
+    tdx, tdw, _ = R.norm_backward_bounds(dy, x.double() - mu.double()[:, None], w, torch.zeros_like(mu), rstd)
+    R.assert_close(dx, rdx, tdx + R.rounding(rdx, dtype), "dx")
+    R.assert_close(dw, rdw, tdw + R.rounding(rdw, torch.float32), "dweight")
