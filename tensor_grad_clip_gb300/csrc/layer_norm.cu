@@ -708,7 +708,7 @@ int launch_rows(void (*kernel)(Args, int, int), const Args& a, int operands, int
 template <typename W>
 int launch_join(NormBwdArgs a, int parts, cudaStream_t st) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((a.cols + 31) / 32);
+    cfg.gridDim = dim3((unsigned)(((int64_t)a.cols + 31) / 32));
     cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -756,7 +756,7 @@ int launch_norm_bwd(const NormBwdArgs& a, int sm_count, void* stream) {
             using T = decltype(t);
             if (params) {
                 parts = (int)std::max<int64_t>(1, std::min<int64_t>(a.rows, kLoopParts));
-                const dim3 grid((unsigned)((a.cols + kLoopBlock - 1) / kLoopBlock), parts);
+                const dim3 grid((unsigned)(((int64_t)a.cols + kLoopBlock - 1) / kLoopBlock), parts);
                 norm_dw_loop_kernel<T><<<grid, kLoopBlock, 0, st>>>(a, parts);
             }
             return (int)cudaGetLastError();

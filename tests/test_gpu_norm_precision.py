@@ -53,3 +53,15 @@ def test_gradient_of_rows_far_from_zero(ops, cols, dtype, mean):
     tdx, tdw, _ = R.norm_backward_bounds(dy, x.double() - mu.double()[:, None], w, torch.zeros_like(mu), rstd)
     R.assert_close(dx, rdx, tdx + R.rounding(rdx, dtype), "dx")
     R.assert_close(dw, rdw, tdw + R.rounding(rdw, torch.float32), "dweight")
+
+
+def test_the_longest_row(ops):
+    cols = 2 ** 31 - 1
+    x = torch.empty(0, cols, device="cuda", dtype=torch.bfloat16)
+    w = torch.ones(cols, device="cuda", dtype=torch.bfloat16)
+    none = torch.empty(0, device="cuda")
+    _, dw, db = ops.layer_norm_backward(x, x, w, none, none)
+    assert dw.shape == db.shape == (cols,)
+    assert not dw.view(torch.int16).any() and not db.view(torch.int16).any()
+    del x, w, dw, db
+    torch.cuda.empty_cache()
