@@ -45,9 +45,10 @@ const char *soma_ops_last_error(void);
 
 /* Kernels that wait for their own asynchronous copies bound that wait (about
  * a second; a step of their pipelines takes microseconds).  This call waits
- * for `device` and returns SOMA_ERR_STATE if such a wait ran out since the
- * last check, which leaves that call's outputs invalid: a fault of the
- * library, not of its arguments. */
+ * for all work on `device`, on every stream, and returns SOMA_ERR_STATE if such
+ * a wait ran out since the last check, which leaves that call's outputs
+ * invalid: a fault of the library, not of its arguments.  Not while a stream is
+ * being captured. */
 soma_status_t soma_ops_check(int32_t device);
 
 /* ---- layer norm -------------------------------------------------------------

@@ -434,7 +434,7 @@ constexpr int kChunkVecs = kEach * kRingBlock;
 constexpr int kSlotBytes = kChunkVecs * 16;
 constexpr int kSlots = 6;
 
-__device__ int g_gave_up;  // a bounded wait ran out on this device
+__device__ unsigned g_gave_up;  // threads that saw a bounded wait run out, on this device
 
 // What the teachers know of a row: entries, their probabilities (then their
 // logarithms), the student's logits there, and for the first entry of each
@@ -781,7 +781,7 @@ __global__ void __launch_bounds__(kRingThreads) distill_ring_kernel(const __grid
         }
     }
     if (sh.gave_up) {
-        g_gave_up = 1;
+        atomicAdd(&g_gave_up, 1u);
         outlast_copies();
     }
 }
@@ -863,13 +863,6 @@ int launch_distill(const DistillArgs& a, DistillPass pass, int sm_count, void* s
     });
 }
 
-int take_distill_gave_up(int* value) {
-    int e = cudaMemcpyFromSymbol(value, g_gave_up, sizeof(int));
-    if (e == cudaSuccess && *value) {
-        const int zero = 0;
-        e = cudaMemcpyToSymbol(g_gave_up, &zero, sizeof(int));
-    }
-    return e;
-}
+int read_distill_gave_up(unsigned* count) { return (int)cudaMemcpyFromSymbol(count, g_gave_up, sizeof(*count)); }
 
 }  // namespace soma

@@ -35,7 +35,7 @@
 namespace soma {
 namespace {
 
-__device__ int g_gave_up;  // a bounded wait ran out on this device
+__device__ unsigned g_gave_up;  // threads that saw a bounded wait run out, on this device
 
 // Rows first, first + step, ... of a group of threads, counted by an int.
 struct Walk {
@@ -354,7 +354,7 @@ __global__ void __maxnreg__(kPer == 32 ? 128 : kWarps ? 96 : 80)
         }
     }
     if (gave_up) {
-        g_gave_up = 1;
+        atomicAdd(&g_gave_up, 1u);
         outlast_copies();
     }
 }
@@ -498,7 +498,7 @@ __global__ void __maxnreg__(128)
         }
     }
     if (gave_up) {
-        g_gave_up = 1;
+        atomicAdd(&g_gave_up, 1u);
         outlast_copies();
     }
     if (!a.dweight && !a.dbias) return;
@@ -789,13 +789,6 @@ int launch_norm_bwd(const NormBwdArgs& a, int sm_count, void* stream) {
     return e;
 }
 
-int take_norm_gave_up(int* value) {
-    int e = cudaMemcpyFromSymbol(value, g_gave_up, sizeof(int));
-    if (e == cudaSuccess && *value) {
-        const int zero = 0;
-        e = cudaMemcpyToSymbol(g_gave_up, &zero, sizeof(int));
-    }
-    return e;
-}
+int read_norm_gave_up(unsigned* count) { return (int)cudaMemcpyFromSymbol(count, g_gave_up, sizeof(*count)); }
 
 }  // namespace soma

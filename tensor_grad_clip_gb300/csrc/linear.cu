@@ -112,7 +112,7 @@ constexpr int kBK = 64;                     // k-values of a pipeline stage: one
 constexpr int kOperandRows = 64;            // m- or n-values of an mn-major box
 constexpr uint32_t kMaxSmem = 232448;       // 227 KB
 
-__device__ int g_gave_up;                   // a kernel's bounded wait ran out on this device
+__device__ unsigned g_gave_up;  // threads that saw a bounded wait run out, on this device
 
 template <typename T>
 constexpr bool kIsBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
     }
     __syncwarp();
     if (gave_up) {  // what is still in flight lands before the CTA's memory is given back
-        if (threadIdx.x == 0) g_gave_up = 1;
+        atomicAdd(&g_gave_up, 1u);
         outlast_copies();
     }
     tcgen05_before_sync();
@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
     }
     __syncwarp();
     if (gave_up) {
-        if (threadIdx.x == 0) g_gave_up = 1;
+        atomicAdd(&g_gave_up, 1u);
         outlast_copies();
     }
     if (splits > 1) cluster_sync_all();  // every partial sum has arrived; no CTA's memory is written after this
@@ -928,14 +928,7 @@ int launch_gemm(const GemmArgs& a, int sm_count, void* stream) {
     });
 }
 
-int take_linear_gave_up(int* value) {
-    int e = cudaMemcpyFromSymbol(value, g_gave_up, sizeof(int));
-    if (e == cudaSuccess && *value) {
-        const int zero = 0;
-        e = cudaMemcpyToSymbol(g_gave_up, &zero, sizeof(int));
-    }
-    return e;
-}
+int read_linear_gave_up(unsigned* count) { return (int)cudaMemcpyFromSymbol(count, g_gave_up, sizeof(*count)); }
 
 int64_t act_bwd_workspace(int64_t rows, int64_t cols, int sm_count) {
     return (int64_t)row_parts(rows, cols, sm_count) * cols * 4;

@@ -14,6 +14,7 @@
 #include <mutex>
 #include <string>
 #include <tuple>
+#include <utility>
 
 #include "ops_kernels.h"
 #include "soma_kernels.h"
@@ -75,6 +76,11 @@ constexpr int64_t kMaxExtent = 1 << 30;  // of a dimension that kernels index wi
 std::mutex g_facts_mu;
 // (device, kernel, block or -1, shared memory) -> resident CTAs, or 1 where the shared memory is allowed
 std::map<std::tuple<int, const void*, int, int>, int> g_facts;
+
+// What the last check of a device found its kernels' counts of expired waits
+// at: layer norm, linear, distillation.
+using Counts = std::array<unsigned, 3>;
+std::map<int, Counts> g_gave_up;
 
 bool is_dtype(int32_t d) { return d == SOMA_DTYPE_F32 || d == SOMA_DTYPE_BF16 || d == SOMA_DTYPE_F16; }
 int size_of(int32_t d) { return d == SOMA_DTYPE_F32 ? 4 : 2; }
@@ -255,14 +261,21 @@ const char* soma_ops_last_error(void) { return g_error.c_str(); }
 soma_status_t soma_ops_check(int32_t device) {
     SOMA_ON_DEVICE(device);
     (void)sms;
-    int norm = 0, linear = 0, distill = 0;
-    SOMA_TRY(cuda_status(soma::take_norm_gave_up(&norm), "check"));
-    SOMA_TRY(cuda_status(soma::take_linear_gave_up(&linear), "check"));
-    SOMA_TRY(cuda_status(soma::take_distill_gave_up(&distill), "check"));
-    if (norm || linear || distill)
-        return fail(SOMA_ERR_STATE, "a %s kernel gave up waiting for its own copies: its results are not valid",
-                    norm ? "layer norm" : linear ? "linear" : "distillation");
-    return SOMA_OK;
+    SOMA_TRY(cuda_status(cudaDeviceSynchronize(), "check"));
+    Counts now{};
+    SOMA_TRY(cuda_status(soma::read_norm_gave_up(&now[0]), "check"));
+    SOMA_TRY(cuda_status(soma::read_linear_gave_up(&now[1]), "check"));
+    SOMA_TRY(cuda_status(soma::read_distill_gave_up(&now[2]), "check"));
+    Counts before{};
+    try {
+        std::lock_guard<std::mutex> lk(g_facts_mu);
+        before = std::exchange(g_gave_up[device], now);
+    } catch (...) {
+        return fail(SOMA_ERR_OOM, "no host memory");
+    }
+    if (now == before) return SOMA_OK;
+    return fail(SOMA_ERR_STATE, "a %s kernel gave up waiting for its own copies: its results are not valid",
+                now[0] != before[0] ? "layer norm" : now[1] != before[1] ? "linear" : "distillation");
 }
 
 // ---- layer norm -----------------------------------------------------------

@@ -124,10 +124,11 @@ enum DistillPass : int32_t { kDistillForward, kDistillBackward, kDistillLossGrad
 
 int launch_distill(const DistillArgs& a, DistillPass pass, int sm_count, void* stream);
 
-// Whether a bounded wait inside a kernel of the current device ran out since
-// the last call (waits for the device).
-int take_norm_gave_up(int* value);
-int take_linear_gave_up(int* value);
-int take_distill_gave_up(int* value);
+// How often a bounded wait inside a kernel of the current device has run out:
+// a count that only grows (modulo 2^32).  The copy waits for the legacy default
+// stream alone; kernels on others may still be running.
+int read_norm_gave_up(unsigned* count);
+int read_linear_gave_up(unsigned* count);
+int read_distill_gave_up(unsigned* count);
 
 }  // namespace soma
