@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
         for (int u = first; u < units; u += step) {
             int row0, col0;
             const int cols = tile_at(u, row0, col0) / (kEpilogueWarps / 4), at = (warp >> 2) * cols;  // the warp's
-            if (!mbar_wait(acc_full(i), parity, &gave_up)) break;
+            if (!mbar_wait(acc_full(i), parity, &gave_up, product_limit(kts))) break;
             __syncwarp();
             tcgen05_after_sync();
             if (row0 + quarter * 32 < g.m)
@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
     // columns that each CTA finishes (splits is a power of two)
     const int log_share = __ffs(BN) - __ffs(splits), share = 1 << log_share;
     if (warp < 4) {
-        if (mbar_wait(done, 0, &gave_up)) {
+        if (mbar_wait(done, 0, &gave_up, product_limit(kt1 - kt0))) {
             __syncwarp();
             tcgen05_after_sync();
             const uint32_t mine = smem_addr(exchange) + (rank * share * kBM + warp * 32 + lane) * 4;

@@ -42,25 +42,32 @@ __device__ __forceinline__ uint64_t global_ns() {
     return t;
 }
 
-// Waits for a barrier's phase, at most about a second (a pipeline step takes
-// microseconds).  After that, or once another thread of the CTA has given up,
-// it sets *gave_up and returns false: the caller leaves its loop and the CTA
-// winds down.
-constexpr uint64_t kWaitLimitNs = 1000000000ull;
-static __device__ __noinline__ bool mbar_wait_on(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+// Waits for a barrier's phase, at most `limit` nanoseconds.  After that, or
+// once another thread of the CTA has given up, it sets *gave_up and returns
+// false: the caller leaves its loop and the CTA winds down.
+//
+// A copy or a pipeline stage takes microseconds and a row of layer norm or of
+// the distillation loss, all of which one CTA passes through, milliseconds: a
+// second is far above both.  What waits for a whole sum of products says how
+// many stages that has (product_limit): with 2^24 stages, a sum over 2^30
+// values, an honest wait takes several seconds.
+constexpr uint64_t kWaitLimitNs = 1000000000ull, kStageLimitNs = 20000ull;
+__host__ __device__ constexpr uint64_t product_limit(int stages) { return kWaitLimitNs + (uint64_t)stages * kStageLimitNs; }
+static __device__ __noinline__ bool mbar_wait_on(uint32_t bar, uint32_t parity, volatile int* gave_up, uint64_t limit) {
     const uint64_t start = global_ns();
     while (true) {
         for (int i = 0; i < 64; ++i)
             if (mbar_try(bar, parity)) return true;
-        if (*gave_up || global_ns() - start > kWaitLimitNs) {
+        if (*gave_up || global_ns() - start > limit) {
             *gave_up = 1;
             return false;
         }
     }
 }
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up,
+                                          uint64_t limit = kWaitLimitNs) {
     if (mbar_try(bar, parity)) return true;
-    return mbar_wait_on(bar, parity, gave_up);
+    return mbar_wait_on(bar, parity, gave_up, limit);
 }
 
 // What a thread does after a wait ran out, before its CTA's shared memory is
