@@ -424,6 +424,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
                 }
             }
         }
+        // The MMAs' last arrivals (of a pair, from the other CTA) land before the
+        // CTA's memory is given back: other commits' arrivals do not promise it.
+        for (int i = 0; i < S::kStages && ok; ++i) {
+            ok = mbar_wait(empty(s), parity, &gave_up);
+            if (++s == S::kStages) {
+                s = 0;
+                parity ^= 1;
+            }
+        }
     } else if (warp == kEpilogueWarps + 1 && lane == 0 && rank == 0) {
         int s = 0, i = 0;
         uint32_t parity = 0, acc_parity = 1;
@@ -552,12 +561,21 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
     if (warp == 4 && lane == 0) {
         int s = 0;
         uint32_t parity = 1;
+        bool ok = true;
         for (int kt = kt0; kt < kt1; ++kt) {
-            if (!mbar_wait(empty(s), parity, &gave_up)) break;
+            if (!(ok = mbar_wait(empty(s), parity, &gave_up))) break;
             mbar_expect(full(s), S::kStage);
             const uint32_t dst = stages + s * S::kStage;
             load_operand<1>(dst, &p.b, g.b_kmajor, kBM, n0, kt * kBK, full(s));
             load_operand<1>(dst + S::kBytesW, &p.a, g.a_kmajor, BN, m0, kt * kBK, full(s));
+            if (++s == S::kStages) {
+                s = 0;
+                parity ^= 1;
+            }
+        }
+        // (as in the tile kernel)
+        for (int i = 0; i < S::kStages && ok; ++i) {
+            ok = mbar_wait(empty(s), parity, &gave_up);
             if (++s == S::kStages) {
                 s = 0;
                 parity ^= 1;
