@@ -130,7 +130,8 @@ soma_status_t soma_linear_backward(int32_t device, const void *dy, int64_t dy_st
  * not count; an index may occur more than once.  A masked logit (-inf, or the
  * type's lowest value) has q = 0; where p > 0 there the loss is +inf.
  * row_weight[rows] fp32 (NULL = 1): a row of weight 0 does not count, its
- * logits are not read, and its loss, lse and gradient are 0.
+ * logits are not read, and its loss, lse and gradient are 0, whatever its
+ * grad_loss is.
  *
  * logits[rows][vocab] in dtype, teacher[rows][top] in teacher_dtype,
  * index[rows][top] int32 or int64, 0 <= top <= SOMA_DISTILL_MAX_TOP,

@@ -275,7 +275,8 @@ __global__ void __launch_bounds__(kBlock, 1536 / kBlock) distill_kernel(const __
     const int rank = (int)(blockIdx.x % cluster);
     T* dz = static_cast<T*>(a.dlogits) + r * a.dlogits_stride;
     const float w = a.row_weight ? a.row_weight[r] : 1.f;
-    const float scale = PASS == kDistillBackward ? a.grad_loss[r] * w : w;
+    // (a row of weight 0 does not count, whatever its grad_loss: an infinity or NaN would not give 0)
+    const float scale = PASS == kDistillBackward && w != 0.f ? a.grad_loss[r] * w : w;
 
     // this CTA's vectors of the row
     const int vectors = (a.vocab + kVec - 1) / kVec;

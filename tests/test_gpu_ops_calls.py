@@ -27,3 +27,19 @@ def test_check_waits_for_other_streams(ops):
     assert not last.query()
     ops.check(0)
     assert last.query()
+
+
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_a_row_of_weight_0_whatever_its_loss_gradient(ops, bad):
+    for vocab, dtype in ((500, torch.float32), (40001, torch.bfloat16), (40000, torch.float16)):
+        z = torch.randn(5, vocab, device="cuda").to(dtype)
+        t, index = torch.randn(5, 6, device="cuda"), torch.randint(0, vocab, (5, 6), device="cuda")
+        w, g = torch.ones(5, device="cuda"), torch.ones(5, device="cuda")
+        _, lse = ops.distill_forward(z, t, index)
+        clean = ops.distill_backward(g, z, lse, t, index, row_weight=w)
+        w[1], g[1], z[1] = 0, bad, math.nan
+        w[3], g[3] = 0, bad
+        d = ops.distill_backward(g, z, lse, t, index, row_weight=w)
+        assert not d[1].any() and not d[3].any()
+        for r in (0, 2, 4):
+            assert torch.equal(d[r], clean[r])
