@@ -351,6 +351,12 @@ def _out_rows(z, logits, out):
     return out, o2.data_ptr(), o2.stride(0)
 
 
+def _written(out):
+    """Tells autograd that a tensor of the caller's has changed: a graph that saved it refuses its backward pass."""
+    if out is not None and not out.is_inference():
+        torch.autograd.graph.increment_version(out)
+
+
 @_on_stream
 def distill_forward(logits, teacher_logits, teacher_index, *, temperature: float = 1.0, row_weight=None):
     """(loss, lse), fp32 and one per row: the temperature-scaled divergence of
@@ -375,18 +381,20 @@ def distill_forward(logits, teacher_logits, teacher_index, *, temperature: float
 def distill_backward(grad_loss, logits, lse, teacher_logits, teacher_index, *, temperature: float = 1.0,
                      row_weight=None, out=None):
     """dL/dlogits for grad_loss = dL/dloss; lse is distill_forward's.  out may
-    be `logits`: the gradient then takes the logits' place."""
+    be `logits`: the gradient then takes the logits' place (autograd counts
+    that as a change in place)."""
     _ops_abi.load()
     z, first, middle, last = _distill_inputs(logits, teacher_logits, teacher_index, row_weight)
     for t, name in ((grad_loss, "grad_loss"), (lse, "lse")):
         _like(t, name, logits, logits.shape[:-1], torch.float32)
         if not t.is_contiguous():
             raise ValueError(f"{name}: must be contiguous")
-    out, address, stride = _out_rows(z, logits, out)
+    gradient, address, stride = _out_rows(z, logits, out)
     dev = logits.device.index
     _check(_ops_abi.soma_distill_backward(dev, grad_loss.data_ptr(), *first, lse.data_ptr(), *middle, temperature,
                                           address, stride, *last, _raw_stream(dev)))
-    return out
+    _written(out)
+    return gradient
 
 
 @_on_stream
@@ -397,11 +405,12 @@ def distill_loss_grad(logits, teacher_logits, teacher_index, *, temperature: flo
     _ops_abi.load()
     z, first, middle, last = _distill_inputs(logits, teacher_logits, teacher_index, row_weight)
     loss = torch.empty(logits.shape[:-1], dtype=torch.float32, device=logits.device)
-    out, address, stride = _out_rows(z, logits, out)
+    gradient, address, stride = _out_rows(z, logits, out)
     dev = logits.device.index
     _check(_ops_abi.soma_distill_loss_grad(dev, *first, *middle, temperature, loss.data_ptr(), None, address, stride,
                                            *last, _raw_stream(dev)))
-    return loss, out
+    _written(out)
+    return loss, gradient
 
 
 # ---- autograd -----------------------------------------------------------------

@@ -43,3 +43,22 @@ def test_a_row_of_weight_0_whatever_its_loss_gradient(ops, bad):
         assert not d[1].any() and not d[3].any()
         for r in (0, 2, 4):
             assert torch.equal(d[r], clean[r])
+
+
+def test_autograd_knows_of_logits_that_a_gradient_replaced(ops):
+    t, index = torch.randn(4, 6, device="cuda"), torch.randint(0, 300, (4, 6), device="cuda")
+    for call in ("loss_grad", "backward"):
+        z = torch.randn(4, 300, device="cuda", requires_grad=True)
+        loss = ops.distill_loss(z, t, index)
+        place = z.detach()  # the same memory
+        if call == "loss_grad":
+            ops.distill_loss_grad(place, t, index, out=place)
+        else:
+            ops.distill_backward(torch.ones(4, device="cuda"), place, ops.distill_forward(place, t, index)[1], t, index,
+                                 out=place)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.sum().backward()
+    with torch.inference_mode():  # (such tensors have no version)
+        z = torch.randn(4, 300, device="cuda")
+        want = ops.distill_loss_grad(z, t, index)[1]
+        assert torch.equal(ops.distill_loss_grad(z, t, index, out=z)[1], want)
