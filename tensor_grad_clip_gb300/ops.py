@@ -449,10 +449,11 @@ class _Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, activation, residual):
         z = None
-        if activation != "none":
+        # (the residual's gradient needs no pre-activation)
+        if activation != "none" and any(ctx.needs_input_grad[:3]):
             y, z = linear_forward(x, weight, bias, activation=activation, residual=residual, save_preactivation=True)
         else:
-            y = linear_forward(x, weight, bias, residual=residual)
+            y = linear_forward(x, weight, bias, activation=activation, residual=residual)
         ctx.save_for_backward(x, weight, z)
         ctx.activation = activation
         return y
@@ -462,8 +463,10 @@ class _Linear(torch.autograd.Function):
     def backward(ctx, dy):
         x, weight, z = ctx.saved_tensors
         wants = ctx.needs_input_grad
-        dx, dw, db = linear_backward(_even(dy), x, weight, z, activation=ctx.activation, input_grad=wants[0],
-                                     weight_grad=wants[1], bias_grad=wants[2])
+        dx = dw = db = None
+        if any(wants[:3]):
+            dx, dw, db = linear_backward(_even(dy), x, weight, z, activation=ctx.activation, input_grad=wants[0],
+                                         weight_grad=wants[1], bias_grad=wants[2])
         return dx, dw, db, None, dy if wants[4] else None
 
 
@@ -492,6 +495,8 @@ def layer_norm(x, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Te
 def linear(x, weight, bias: Optional[torch.Tensor] = None, *, activation: str = "none",
            residual: Optional[torch.Tensor] = None):
     """Differentiable act(x weight^T + bias) + residual (see linear_forward)."""
+    if not torch.is_grad_enabled():  # (needs_input_grad does not know)
+        return linear_forward(x, weight, bias, activation=activation, residual=residual)
     return _Linear.apply(x, weight, bias, activation, residual)
 
 

@@ -62,3 +62,29 @@ def test_autograd_knows_of_logits_that_a_gradient_replaced(ops):
         z = torch.randn(4, 300, device="cuda")
         want = ops.distill_loss_grad(z, t, index)[1]
         assert torch.equal(ops.distill_loss_grad(z, t, index, out=z)[1], want)
+
+
+def test_no_preactivation_is_stored_without_a_gradient(ops, monkeypatch):
+    asked = []
+    real = ops.linear_forward
+
+    def spy(*args, **kwargs):
+        asked.append(kwargs.get("save_preactivation", False))
+        return real(*args, **kwargs)
+    monkeypatch.setattr(ops, "linear_forward", spy)
+    x, w, r = (torch.randn(s, device="cuda").half() for s in ((20, 64), (48, 64), (20, 48)))
+    want = real(x, w, activation="gelu", residual=r)
+    wg = w.clone().requires_grad_()
+    with torch.no_grad():
+        assert torch.equal(ops.linear(x, wg, activation="gelu", residual=r), want)
+    assert torch.equal(ops.linear(x, w, activation="gelu", residual=r), want)
+    rg = r.clone().requires_grad_()
+    y = ops.linear(x, w, activation="gelu", residual=rg)  # the residual's gradient is dy itself
+    y.backward(torch.ones_like(y))
+    assert torch.equal(y, want) and torch.equal(rg.grad, torch.ones_like(r))
+    assert asked == [False, False, False]
+    y = ops.linear(x, wg, activation="gelu", residual=r)
+    y.backward(torch.ones_like(y))
+    assert torch.equal(y, want) and asked[3:] == [True]
+    z = real(x, w, activation="gelu", save_preactivation=True)[1]
+    assert torch.equal(wg.grad, ops.linear_backward(torch.ones_like(y), x, w, z, activation="gelu")[1])
