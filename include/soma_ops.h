@@ -119,7 +119,7 @@ soma_status_t soma_linear_backward(int32_t device, const void *dy, int64_t dy_st
 
 /* ---- distillation from a teacher's top logits -------------------------------
  * A teacher answers each row with `top` of its logits and their places in
- * the vocabulary.  With temperature T > 0,
+ * the vocabulary.  With temperature T, 1e-6 <= T <= 1e6,
  *   p_j    = exp(t_j / T) / sum_j exp(t_j / T)      over the row's valid entries
  *   q_v    = exp(z_v / T - lse),  lse = log sum_v exp(z_v / T)
  *   loss_r = row_weight_r * T^2 * sum_j p_j * (log p_j - log q_{index_j})
@@ -127,8 +127,12 @@ soma_status_t soma_linear_backward(int32_t device, const void *dy, int64_t dy_st
  * An entry whose index is outside [0, vocab) is not valid (mark a short
  * teacher row with -1); a row without valid entries, or whose valid teacher
  * logits are all -inf, has loss 0 and gradient 0.  Entries with p_j = 0 do
- * not count; an index may occur more than once.  A masked logit (-inf, or the
- * type's lowest value) has q = 0; where p > 0 there the loss is +inf.
+ * not count; an index may occur more than once.  A logit of -inf has q = 0;
+ * where p > 0 there the loss is +inf.  A row whose logits are all -inf has lse
+ * -inf and, if it has valid entries, loss and gradient NaN.  Every other value
+ * is an ordinary logit, the type's lowest too: beside larger ones its q is 0
+ * by its size, p > 0 there costs p |z| T, and a row wholly at it is uniform.
+ * z / T is taken in fp32; where that overflows, the logit counts as infinite.
  * row_weight[rows] fp32 (NULL = 1): a row of weight 0 does not count, its
  * logits are not read, and its loss, lse and gradient are 0, whatever its
  * grad_loss is.
@@ -140,7 +144,8 @@ soma_status_t soma_linear_backward(int32_t device, const void *dy, int64_t dy_st
  *   forward    loss and lse
  *   backward   dlogits for grad_loss[rows] = dL/dloss: scale = grad_loss * row_weight
  *   loss_grad  loss, lse (may be NULL) and dlogits for grad_loss = 1 in one
- *              kernel that reads a row's logits from HBM once
+ *              kernel; the row's second reading, for the gradient, is from
+ *              shared memory or L2 as far as those hold the rows in progress
  * dlogits[rows][vocab] in dtype may be the logits themselves (same pointer
  * and stride). */
 #define SOMA_INDEX_I32 0
