@@ -3,7 +3,9 @@
 // A row's logits are streamed in 16-byte vectors: the forward pass reads them
 // once (maximum and sum of exponentials together, in fp32), the backward pass
 // reads them once and writes the gradient, and the one-call form reads a row
-// twice, the second time from L2, where the rows in progress all fit.  One
+// twice: many long rows, where they are aligned, pass through a ring in shared
+// memory that keeps most of a row for the second time; of other rows the second
+// reading is from L2 as far as that holds the rows in progress.  One
 // exponential and about six other instructions per element keep the bound
 // with HBM.  The teacher's entries (at most 1024) live in shared memory; one
 // warp works on them while the others stream.
@@ -17,8 +19,10 @@
 //
 // A cluster of CTAs shares a row when there are fewer rows than CTAs that the
 // device holds; the CTAs' maxima and sums are joined through distributed
-// shared memory, in rank order.  Which thread takes which elements does not depend on where rows
-// start in memory, so neither do the results.
+// shared memory, in rank order.  Within a kernel, which thread takes which
+// elements does not depend on where rows start in memory, so neither do the
+// results.  Between the two kernels of the one-call form it does: the ring adds
+// four vectors at a time, and the loss over more threads.
 #include <math.h>
 
 #include <algorithm>

@@ -88,3 +88,38 @@ def test_no_preactivation_is_stored_without_a_gradient(ops, monkeypatch):
     assert torch.equal(y, want) and asked[3:] == [True]
     z = real(x, w, activation="gelu", save_preactivation=True)[1]
     assert torch.equal(wg.grad, ops.linear_backward(torch.ones_like(y), x, w, z, activation="gelu")[1])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_bits_wherever_rows_start(ops, dtype):
+    for rows, cols in ((9, 500), (300, 4099), (20, 16384)):
+        flat = torch.randn(rows, cols, device="cuda").to(dtype)
+        w = torch.rand(cols, device="cuda")
+
+        def norm(x):
+            y, mu, rstd = ops.layer_norm_forward(x, w, w)
+            return y, mu, rstd, *ops.layer_norm_backward(x, x, w, mu, rstd)
+        for other in moved(flat):
+            assert all(torch.equal(a, b) for a, b in zip(norm(flat), norm(other)))
+    for rows, vocab in ((3, 40000), (100, 9000), (700, 17000)):
+        z = torch.randn(rows, vocab, device="cuda").mul(2.5).to(dtype)
+        t, index = torch.randn(rows, 9, device="cuda"), torch.randint(0, vocab, (rows, 9), device="cuda")
+        g = torch.randn(rows, device="cuda")
+
+        def distill(z):
+            loss, lse = ops.distill_forward(z, t, index)
+            # (loss and gradient together too, except of many long rows: these go through shared memory where they are aligned)
+            return loss, lse, ops.distill_backward(g, z, lse, t, index), *(
+                ops.distill_loss_grad(z, t, index) if rows < 600 else ())
+        for other in moved(z):
+            assert all(torch.equal(a, b) for a, b in zip(distill(z), distill(other)))
+
+
+def moved(x):
+    """x's values in rows that start elsewhere."""
+    rows, cols = x.shape
+    for pad, offset in ((0, 3), (3, 1), (8, 0)):
+        buf = torch.zeros(rows * (cols + pad) + offset, device="cuda", dtype=x.dtype)
+        view = buf[offset:].view(rows, cols + pad)[:, :cols]
+        view.copy_(x)
+        yield view
