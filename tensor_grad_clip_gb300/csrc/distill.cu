@@ -37,7 +37,7 @@ namespace soma {
 namespace {
 
 constexpr int kMaxCluster = 8;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float exp2_fast(float x) {
     float r;

@@ -664,7 +664,7 @@ bool vector_rows(const void* p, int64_t stride, int64_t rows, int esize) {
 }
 
 // Calls f(elements per thread, warps per row or 0, warps of a CTA).
-template <bool kForward, typename F>
+template <typename F>
 int with_shape(int cols, F&& f) {
     using std::integral_constant;
     using OneWarp = integral_constant<int, 1>;
@@ -732,7 +732,7 @@ int launch_norm_fwd(const NormFwdArgs& a, int sm_count, void* stream) {
     return with_type(a.dtype, [&](auto t) {
         using T = decltype(t);
         const bool vec = vector_rows(a.x, a.x_stride, a.rows, sizeof(T)) && vector_rows(a.y, a.y_stride, a.rows, sizeof(T));
-        return with_shape<true>(a.cols, [&](auto per, auto row_warps, int warps) {
+        return with_shape(a.cols, [&](auto per, auto row_warps, int warps) {
             constexpr int kPer = decltype(per)::value;
             constexpr int kWarps = decltype(row_warps)::value;
             int ctas;
@@ -767,7 +767,7 @@ int launch_norm_bwd(const NormBwdArgs& a, int sm_count, void* stream) {
             const bool vec = vector_rows(a.x, a.x_stride, a.rows, sizeof(T)) &&
                              vector_rows(a.dy, a.dy_stride, a.rows, sizeof(T)) &&
                              vector_rows(a.dx, a.dx_stride, a.rows, sizeof(T));
-            return with_shape<false>(a.cols, [&](auto per, auto row_warps, int warps) {
+            return with_shape(a.cols, [&](auto per, auto row_warps, int warps) {
                 constexpr int kPer = decltype(per)::value;
                 constexpr int kWarps = decltype(row_warps)::value;
                 return launch_rows(vec ? norm_bwd_kernel<T, kPer, true, kWarps> : norm_bwd_kernel<T, kPer, false, kWarps>,
