@@ -88,7 +88,8 @@ __device__ __forceinline__ float act_slope(float z) {
     }
     if (kAct == SOMA_ACT_GELU_TANH) {
         const float s = logistic(2.f * kSqrt2OverPi * z * fmaf(kCubic * z, z, 1.f));
-        const float du = 2.f * kSqrt2OverPi * fmaf(3.f * kCubic * z, z, 1.f);
+        const float near = fminf(fabsf(z), 64.f);  // s (1 - s) is 0 beyond; z^2 may leave fp32's range
+        const float du = 2.f * kSqrt2OverPi * fmaf(3.f * kCubic * near, near, 1.f);
         return fmaf(z * s * (1.f - s), du, s);
     }
     if (kAct == SOMA_ACT_SILU) {
