@@ -12,7 +12,7 @@
 //   up to 16384           a CTA (16 or 32 elements per thread)
 //   more                  a CTA of 256 threads that re-reads it through L2
 //
-// Measured (GB300, 6682 GB/s copy): 16384 x 4096 bf16 forward 51.5 us, 5213
+// Measured (GB300, 6682 GB/s copy): 16384 x 4096 bf16 forward 50.4 us, 5330
 // GB/s; backward 82.1 us, 4909 GB/s; fp32 backward 133 us, 6064 GB/s; 16381 x
 // 4099 fp16 (padded rows) backward 124 us, 3249 GB/s.  The 16-bit passes are
 // bound by the latency of a row's chain (copy, statistics over the CTA,
@@ -51,7 +51,9 @@ struct Walk {
 };
 
 constexpr int kCtaWarps = 4;    // warps of a CTA whose rows take one or two of them
-constexpr int kMaxDepth = 8;    // rows in flight per warp or CTA
+// Rows in flight per warp or CTA, at most: with eight the forward pass of 16384
+// x 4096 bf16 takes 52.3 us, with four 50.1; the backward pass's rows are two.
+constexpr int kMaxDepth = 8, kForwardDepth = 4;
 
 // A matrix operand as the kernels see it.  Row r's window is the run of whole
 // 16-byte words that covers it; slots hold windows, so a row's first element
@@ -222,16 +224,12 @@ __device__ __forceinline__ void group_sync(int group, int warps) {
 // warps of the CTA (kWarps = 0).
 //
 // The statistics take one pass over the thread's elements and one reduction:
-// sums of d = x - k and of d^2, with k the average of four elements in
-// the middle of the row, which every thread reads.  The variance is then
-// sum d^2 / n - (sum d / n)^2, which loses a few bits when the mean is far
-// from k, and d itself is rounded at the size of k.  So where (mean - k)^2 >
-// 4 var, as with a large channel among the four, both sums are taken again
-// with k the mean that the first pass found.  The thread keeps its x for that,
-// and forms x - k once more for the output: 16384 x 4096 bf16 51.5 us (66 where
-// every row has such a channel), 8192 x 4096 fp32 49.7 (51).  With x - k kept
-// and the row read again from its slot or from L2 they took 52.5 (73) and 50
-// (51), or 52 (92) and 47 (74).
+// mean = sum x / n and var = sum x^2 / n - mean^2.  That loses up to two bits
+// of the variance while mean^2 <= 4 var; beyond, the thread's elements, which
+// it holds, become x - k with k the mean just found, and both sums are taken
+// again of those (16384 x 4096 bf16: 50.1 us, and 63.5 us where every row's
+// mean is that far from 0).  A shift by some element of the row instead would
+// round all others at that one's size, and the mean with them.
 template <typename T, int kPer, bool kAligned, int kWarps>
 __global__ void __maxnreg__(kPer == 32 ? 128 : kWarps ? 96 : 80)
     norm_fwd_kernel(const __grid_constant__ NormFwdArgs a, int depth, int slot_bytes) {
@@ -263,8 +261,6 @@ __global__ void __maxnreg__(kPer == 32 ? 128 : kWarps ? 96 : 80)
         parameter<T, kVec>(a.bias, f32, (p * threads + t) * kVec, a.cols, 0.f, b + p * kVec);
     }
     const float inv = 1.f / (float)a.cols;
-    const int middle = a.cols / 2 / kVec * kVec, middle_n = min(4, a.cols - middle);
-    const float inv_middle = 1.f / (float)middle_n;
     T* y = static_cast<T*>(a.y) + walk.first * a.y_stride;
     int turn = 0, slot = 0;
     uint32_t parity = 0;
@@ -276,16 +272,7 @@ __global__ void __maxnreg__(kPer == 32 ? 128 : kWarps ? 96 : 80)
             group_sync<kWarps>(group, warps);
         }
         const int phase = kAligned ? 0 : x[0].phase(walk.row(it));
-        float k;
-        {
-            float e[kVec];
-            widen16(slot_vector<T, kAligned>(window, middle, phase), e, T{});
-            k = e[0];
-            if (middle_n == 4) k += e[1] + (e[2] + e[3]);
-            else if (middle_n > 1) k += middle_n > 2 ? e[1] + e[2] : e[1];
-            k *= inv_middle;
-        }
-        float2 e[kPer / 2];
+        float2 e[kPer / 2], sum = both(0.f), square = both(0.f);  // x, 0 past the row's end
 #pragma unroll
         for (int p = 0; p < kPieces; ++p) {
             const int c = (p * threads + t) * kVec;
@@ -293,37 +280,45 @@ __global__ void __maxnreg__(kPer == 32 ? 128 : kWarps ? 96 : 80)
             if (c < a.cols) widen16(slot_vector<T, kAligned>(window, c, phase), v, T{});
 #pragma unroll
             for (int i = 0; i < kVec / 2; ++i) e[p * kVec / 2 + i] = make_float2(v[2 * i], v[2 * i + 1]);
+            if (c + kVec > a.cols) {
+#pragma unroll
+                for (int i = 0; i < kVec / 2; ++i) {
+                    if (c + 2 * i >= a.cols) e[p * kVec / 2 + i].x = 0.f;
+                    if (c + 2 * i + 1 >= a.cols) e[p * kVec / 2 + i].y = 0.f;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kVec / 2; ++i) {
+                sum = add2(sum, e[p * kVec / 2 + i]);
+                square = fma2(e[p * kVec / 2 + i], e[p * kVec / 2 + i], square);
+            }
         }
-        auto totals = [&] {  // of x - k and its square over the row
-            float2 sum = both(0.f), square = both(0.f);
+        float2 s = row_totals<kWarps>(sum.x + sum.y, square.x + square.y, scratch, group, warps, turn);
+        // (every thread has its part of the row in registers now)
+        if (t == 0 && it + depth < walk.count) fill_row<kAligned>(ring, x, walk.row(it + depth), it + depth >= inner_end || it + depth < inner_begin, slot);
+        float k = 0.f, shift = s.x * inv, var = fmaf(-shift, shift, s.y * inv);
+        if (shift * shift > 4.f * var) {  // the same for all threads of the row
+            k = shift;
+            sum = square = both(0.f);
 #pragma unroll
             for (int p = 0; p < kPieces; ++p) {
                 const int c = (p * threads + t) * kVec;
-                float2 d[kVec / 2];
 #pragma unroll
-                for (int i = 0; i < kVec / 2; ++i) d[i] = add2(e[p * kVec / 2 + i], both(-k));
+                for (int i = 0; i < kVec / 2; ++i) e[p * kVec / 2 + i] = add2(e[p * kVec / 2 + i], both(-k));
                 if (c + kVec > a.cols) {
 #pragma unroll
                     for (int i = 0; i < kVec / 2; ++i) {
-                        if (c + 2 * i >= a.cols) d[i].x = 0.f;
-                        if (c + 2 * i + 1 >= a.cols) d[i].y = 0.f;
+                        if (c + 2 * i >= a.cols) e[p * kVec / 2 + i].x = 0.f;
+                        if (c + 2 * i + 1 >= a.cols) e[p * kVec / 2 + i].y = 0.f;
                     }
                 }
 #pragma unroll
                 for (int i = 0; i < kVec / 2; ++i) {
-                    sum = add2(sum, d[i]);
-                    square = fma2(d[i], d[i], square);
+                    sum = add2(sum, e[p * kVec / 2 + i]);
+                    square = fma2(e[p * kVec / 2 + i], e[p * kVec / 2 + i], square);
                 }
             }
-            return row_totals<kWarps>(sum.x + sum.y, square.x + square.y, scratch, group, warps, turn);
-        };
-        float2 s = totals();
-        // (every thread has its part of the row in registers now)
-        if (t == 0 && it + depth < walk.count) fill_row<kAligned>(ring, x, walk.row(it + depth), it + depth >= inner_end || it + depth < inner_begin, slot);
-        float shift = s.x * inv, var = fmaf(-shift, shift, s.y * inv);
-        if (shift * shift > 4.f * var) {  // the same for all threads of the row
-            k += shift;
-            s = totals();
+            s = row_totals<kWarps>(sum.x + sum.y, square.x + square.y, scratch, group, warps, turn);
             shift = s.x * inv;
             var = fmaf(-shift, shift, s.y * inv);
             if (var < 0.f) var = 0.f;  // (the rounding of a constant row)
@@ -337,7 +332,7 @@ __global__ void __maxnreg__(kPer == 32 ? 128 : kWarps ? 96 : 80)
 #pragma unroll
             for (int i = 0; i < kVec / 2; ++i) {
                 const int j = p * kVec + 2 * i;
-                const float2 xh = fma2(add2(e[p * kVec / 2 + i], both(-k)), scale, offset);
+                const float2 xh = fma2(e[p * kVec / 2 + i], scale, offset);
                 const float2 v = fma2(xh, make_float2(w[j], w[j + 1]), make_float2(b[j], b[j + 1]));
                 out[2 * i] = v.x;
                 out[2 * i + 1] = v.y;
@@ -693,7 +688,8 @@ int launch_rows(void (*kernel)(Args, int, int), const Args& a, int operands, int
     if (e != cudaSuccess) return e;
     per_sm = std::min(kCtasMost, std::max(1, per_sm));
     while (per_sm > 1 && kRingBytes / per_sm / bytes < 2) --per_sm;
-    const int depth = std::max(1, std::min(kMaxDepth, kRingBytes / per_sm / bytes));
+    const int most = operands == 1 ? kForwardDepth : kMaxDepth;
+    const int depth = std::max(1, std::min(most, kRingBytes / per_sm / bytes));
     const size_t smem = (size_t)bytes * depth;
     if (smem > 40 * 1024) e = allow_smem((const void*)kernel, (int)smem);
     if (e != cudaSuccess) return e;
