@@ -43,8 +43,9 @@ extern "C" {
  * none).  Valid until the thread's next call. */
 const char *soma_ops_last_error(void);
 
-/* Kernels that wait for their own asynchronous copies bound that wait (about
- * a second; a step of their pipelines takes microseconds).  This call waits
+/* Kernels that wait for their own asynchronous copies and products bound that
+ * wait: a second, where a step of their pipelines takes microseconds, and 20 us
+ * more for each 64 values that a sum of products runs over.  This call waits
  * for all work on `device`, on every stream, and returns SOMA_ERR_STATE if such
  * a wait ran out since the last check, which leaves that call's outputs
  * invalid: a fault of the library, not of its arguments.  Not while a stream is

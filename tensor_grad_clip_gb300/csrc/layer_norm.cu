@@ -9,6 +9,7 @@
 //
 //   rows of               a row belongs to
 //   up to 512 elements    a warp (8 or 16 elements per thread, no barriers)
+//   up to 1024            two warps (16 elements per thread)
 //   up to 16384           a CTA (16 or 32 elements per thread)
 //   more                  a CTA of 256 threads that re-reads it through L2
 //

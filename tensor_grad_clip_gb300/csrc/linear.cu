@@ -487,14 +487,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
         if (lane == 0) tma_store_wait();
     }
     __syncwarp();
-    if (gave_up) {  // what is still in flight lands before the CTA's memory is given back
-        atomicAdd(&g_gave_up, 1u);
-        outlast_copies();
-    }
+    if (gave_up) outlast_copies();  // what is still in flight lands before the CTA's memory is given back
     tcgen05_before_sync();
     if (CG == 2) cluster_sync_all();
     else __syncthreads();
     tcgen05_after_sync();
+    if (threadIdx.x == 0 && gave_up) atomicAdd(&g_gave_up, 1u);
     if (warp == kEpilogueWarps + 1) tmem_free<CG>(tmem, S::kTmemCols);
 }
 
@@ -628,12 +626,10 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const __grid_constant_
         tcgen05_before_sync();
     }
     __syncwarp();
-    if (gave_up) {
-        atomicAdd(&g_gave_up, 1u);
-        outlast_copies();
-    }
+    if (gave_up) outlast_copies();
     if (splits > 1) cluster_sync_all();  // every partial sum has arrived; no CTA's memory is written after this
     else __syncthreads();
+    if (threadIdx.x == 0 && gave_up) atomicAdd(&g_gave_up, 1u);
     if (warp < 4) {
         const int n = n0 + warp * 32 + lane;
         const int count = min(share, g.m - m0 - rank * share);
