@@ -13,9 +13,11 @@
 //   up to 16384           a CTA (16 or 32 elements per thread)
 //   more                  a CTA of 256 threads that re-reads it through L2
 //
-// Measured (GB300, 6682 GB/s copy): 16384 x 4096 bf16 forward 50.4 us, 5330
-// GB/s; backward 82.1 us, 4909 GB/s; fp32 backward 133 us, 6064 GB/s; 16381 x
-// 4099 fp16 (padded rows) backward 124 us, 3249 GB/s.  The 16-bit passes are
+// Measured (GB300, 6682 GB/s copy): 16384 x 4096 bf16 forward 49.2 us, 5460
+// GB/s; backward 82.1 us, 4905 GB/s; 8192 x 4096 fp32 forward 50.6 us, 5305
+// GB/s; 16384 x 4096 fp32 backward 126 us, 6402 GB/s; 16381 x 4099 fp16 (padded
+// rows) backward 125 us, 3226 GB/s; rows of 40000 bf16, which take the last
+// path, 206 us forward and 436 us backward for 2000 rows (1553 and 1102 GB/s).  The 16-bit passes are
 // bound by the latency of a row's chain (copy, statistics over the CTA,
 // output) at the two or three rows an SM's registers hold, not by DRAM: ncu
 // has DRAM at 54 to 61 % and the issue slots at 48 to 60 %.  Tried and slower:
@@ -52,9 +54,7 @@ struct Walk {
 };
 
 constexpr int kCtaWarps = 4;    // warps of a CTA whose rows take one or two of them
-// Rows in flight per warp or CTA, at most: with eight the forward pass of 16384
-// x 4096 bf16 takes 52.3 us, with four 50.1; the backward pass's rows are two.
-constexpr int kMaxDepth = 8, kForwardDepth = 4;
+constexpr int kMaxDepth = 8;    // rows in flight per warp or CTA
 
 // A matrix operand as the kernels see it.  Row r's window is the run of whole
 // 16-byte words that covers it; slots hold windows, so a row's first element
@@ -228,7 +228,7 @@ __device__ __forceinline__ void group_sync(int group, int warps) {
 // mean = sum x / n and var = sum x^2 / n - mean^2.  That loses up to two bits
 // of the variance while mean^2 <= 4 var; beyond, the thread's elements, which
 // it holds, become x - k with k the mean just found, and both sums are taken
-// again of those (16384 x 4096 bf16: 50.1 us, and 63.5 us where every row's
+// again of those (16384 x 4096 bf16: 49.2 us, and 62.6 us where every row's
 // mean is that far from 0).  A shift by some element of the row instead would
 // round all others at that one's size, and the mean with them.
 template <typename T, int kPer, bool kAligned, int kWarps>
@@ -288,11 +288,11 @@ __global__ void __maxnreg__(kPer == 32 ? 128 : kWarps ? 96 : 80)
                     if (c + 2 * i + 1 >= a.cols) e[p * kVec / 2 + i].y = 0.f;
                 }
             }
+        }
 #pragma unroll
-            for (int i = 0; i < kVec / 2; ++i) {
-                sum = add2(sum, e[p * kVec / 2 + i]);
-                square = fma2(e[p * kVec / 2 + i], e[p * kVec / 2 + i], square);
-            }
+        for (int i = 0; i < kPer / 2; ++i) {
+            sum = add2(sum, e[i]);
+            square = fma2(e[i], e[i], square);
         }
         float2 s = row_totals<kWarps>(sum.x + sum.y, square.x + square.y, scratch, group, warps, turn);
         // (every thread has its part of the row in registers now)
@@ -646,6 +646,10 @@ constexpr int kCtasMost = 8;   // persistent CTAs per SM; bounds the partial sum
 constexpr int kLoopParts = 64;
 constexpr int kLongest = 512 * 32;  // elements of a row that a CTA takes
 constexpr int kRingBytes = 200 * 1024;  // of an SM's shared memory, for all its CTAs
+// The forward pass is faster with fewer rows in flight, two at least: 100 KB
+// instead of 200 take 16384 x 4096 bf16 from 52.3 to 49.2 us and 8192 x 5000
+// fp32 from 61.3 to 56.7.
+constexpr int kForwardRing = 100 * 1024;
 
 template <typename F>
 int with_types(int dtype, int param_dtype, F&& f) {
@@ -689,8 +693,8 @@ int launch_rows(void (*kernel)(Args, int, int), const Args& a, int operands, int
     if (e != cudaSuccess) return e;
     per_sm = std::min(kCtasMost, std::max(1, per_sm));
     while (per_sm > 1 && kRingBytes / per_sm / bytes < 2) --per_sm;
-    const int most = operands == 1 ? kForwardDepth : kMaxDepth;
-    const int depth = std::max(1, std::min(most, kRingBytes / per_sm / bytes));
+    const int ring = operands == 1 ? kForwardRing : kRingBytes;
+    const int depth = std::max(operands == 1 ? 2 : 1, std::min(kMaxDepth, ring / per_sm / bytes));
     const size_t smem = (size_t)bytes * depth;
     if (smem > 40 * 1024) e = allow_smem((const void*)kernel, (int)smem);
     if (e != cudaSuccess) return e;
