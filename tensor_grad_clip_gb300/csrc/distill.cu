@@ -11,11 +11,12 @@
 // warp works on them while the others stream.
 //
 // Measured (GB300, 6682 GB/s copy; 15 % of the rows do not count): 8192 x
-// 131072 bf16 forward 281 us, 6515 GB/s; backward 638 us, 6235 GB/s; loss and
-// gradient together 722 us, 5507 GB/s (914 us when the second pass re-read
+// 131072 bf16 forward 285 us, 6405 GB/s; backward 639 us, 6225 GB/s; loss and
+// gradient together 715 us, 5560 GB/s (914 us when the second pass re-read
 // the row through L2, which the rows in progress overflow).  2048 x 50021
 // bf16 backward, whose rows start anywhere, 103 us, 3668 GB/s: bound by the
-// instructions that shift vectors on both sides (4987 GB/s for 50024).
+// instructions that shift vectors on both sides (4987 GB/s for 50024).  Loss and
+// gradient together of 2000 x 50021 fp16 133 us, of 2000 x 50024 95 us.
 //
 // A cluster of CTAs shares a row when there are fewer rows than CTAs that the
 // device holds; the CTAs' maxima and sums are joined through distributed
@@ -858,7 +859,8 @@ int launch_distill(const DistillArgs& a, DistillPass pass, int sm_count, void* s
         // The ring for rows that start on 16-byte boundaries, are longer than 32
         // KB and come at least four to an SM: 4000 rows of 32000 fp32 take 168 to
         // 192 us with it and 214 without.  Unaligned rows would pay the shifting
-        // with a third of the threads (239 us against 175 for 2000 x 50021 fp16).
+        // with a third of the threads (2000 x 50021 fp16, all of which count: 144 us
+        // without the ring, 239 when a ring for such rows was tried; 2000 x 50024 92).
         if (pass == kDistillLossGrad && a.rows >= 4 * sm_count && (int64_t)a.vocab * (int)sizeof(T) > 32768 &&
             aligned(a.logits, a.logits_stride) && aligned(a.dlogits, a.dlogits_stride))
             return launch_ring<T>(a, sm_count, (cudaStream_t)stream);

@@ -14,16 +14,17 @@
 //   more                  a CTA of 256 threads that re-reads it through L2
 //
 // Measured (GB300, 6682 GB/s copy): 16384 x 4096 bf16 forward 49.2 us, 5460
-// GB/s; backward 82.1 us, 4905 GB/s; 8192 x 4096 fp32 forward 50.6 us, 5305
-// GB/s; 16384 x 4096 fp32 backward 126 us, 6402 GB/s; 16381 x 4099 fp16 (padded
-// rows) backward 125 us, 3226 GB/s; rows of 40000 bf16, which take the last
-// path, 206 us forward and 436 us backward for 2000 rows (1553 and 1102 GB/s).  The 16-bit passes are
-// bound by the latency of a row's chain (copy, statistics over the CTA,
-// output) at the two or three rows an SM's registers hold, not by DRAM: ncu
-// has DRAM at 54 to 61 % and the issue slots at 48 to 60 %.  Tried and slower:
-// more rows per SM with the parameters read again for every row from L1 (74
-// us forward), a warp of its own to fill the ring (57 us; warps are allocated
-// in fours), 24 or 32 elements per thread for rows of 4099 (206 us backward).
+// GB/s; backward 82.1 us, 4905 GB/s.  fp32: 8192 x 4096 forward 50.6 us, 5305
+// GB/s; 16384 x 4096 backward 126 us, 6402 GB/s.  16381 x 4099 fp16 (padded
+// rows) backward 125 us, 3226 GB/s.  2000 x 40000 bf16, which takes the last
+// path, 206 us forward and 436 us backward (1553 and 1102 GB/s).  The 16-bit
+// passes are bound by the latency of a row's chain (copy, statistics over the
+// CTA, output) at the two or three rows an SM's registers hold, not by DRAM:
+// ncu has DRAM at 57 to 60 % and the issue slots at 48 to 65 %.  Tried and
+// slower: more rows per SM with the parameters read again for every row from
+// L1 (74 us forward), a warp of its own to fill the ring (57 us; warps are
+// allocated in fours), 24 or 32 elements per thread for rows of 4099 (206 us
+// backward).
 //
 // A row may start at any element: its slot holds the whole 16-byte words that
 // cover it, and threads shift their vectors into place.  Which thread sums

@@ -9,10 +9,12 @@
 // Operands may run along k or across it, so no product needs a transpose.
 //
 // Measured (GB300, cuBLAS bf16 1924 TFLOP/s in a burst): 16384 x 4096 x 11008
-// bf16 with residual 815 us, 1813 TFLOP/s; 4096 x 4096 x 1024 with gelu and
-// saved pre-activation 32.6 us, 1053 TFLOP/s (3.4 waves of tiles whose
-// epilogue is as long as their products); its three gradients in fp16 71.5 us,
-// 962 TFLOP/s; one row through 11008 x 4096 18.1 us, 4990 GB/s.
+// bf16 with residual 818 us in a burst, 1807 TFLOP/s, and 944 us in a steady
+// loop, which power limits; 4096 x 4096 x 1024 with gelu and saved
+// pre-activation 32.8 us, 1048 TFLOP/s (3.4 waves of tiles whose epilogue is as
+// long as their products); its three gradients in fp16 71.5 us, 961 TFLOP/s;
+// through 11008 x 4096, one row 18.2 us, 4960 GB/s, 16 rows 20.3, 64 rows 28.2
+// and 128 rows 47.8 us.
 #include <cuda.h>
 #include <math.h>
 
