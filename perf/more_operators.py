@@ -29,38 +29,38 @@ TOP = 448.0      # the largest 8-bit value (e4m3)
 def listed():
     return [
         # Looking one token up in a generation loop: the call's latency.
-        dict(name="embedding, one token", op="emb_fwd", rows=1, vocab=32000, cols=4096, pad=0, dtype="bf16", index="i64",
+        dict(name="embedding one token", op="emb_fwd", rows=1, vocab=32000, cols=4096, pad=0, dtype="bf16", index="i64",
              scale=1.0),
         # The tokens of a training batch, scaled by the square root of the width.
-        dict(name="embedding, 16k tokens", op="emb_fwd", rows=16384, vocab=131072, cols=4096, pad=0, dtype="bf16",
+        dict(name="embedding 16k tokens", op="emb_fwd", rows=16384, vocab=131072, cols=4096, pad=0, dtype="bf16",
              index="i64", scale=64.0),
         # The gradient of that table's smaller sister: frequent tokens stand in thousands of places.
-        dict(name="embedding grad, 16k tokens", op="emb_bwd", rows=16384, vocab=32000, cols=4096, pad=0, dtype="bf16",
+        dict(name="embedding grad 16k tokens", op="emb_bwd", rows=16384, vocab=32000, cols=4096, pad=0, dtype="bf16",
              index="i64", scale=1.0, tied=False),
         # A table of odd sizes that the head shares: the gradient is added to the head's.
-        dict(name="embedding grad, tied, odd", op="emb_bwd", rows=5003, vocab=50021, cols=1003, pad=5, dtype="f32",
+        dict(name="embedding grad tied odd", op="emb_bwd", rows=5003, vocab=50021, cols=1003, pad=5, dtype="f32",
              index="i32", scale=2.0, tied=True),
         # Scoring a few positions: the head's weight is read once.
-        dict(name="head loss, few rows", op="head_fwd", rows=16, vocab=32000, k=1024, pad=0, dtype="bf16", index="i64"),
+        dict(name="head loss few rows", op="head_fwd", rows=16, vocab=32000, k=1024, pad=0, dtype="bf16", index="i64"),
         # The loss of a validation batch.
-        dict(name="head loss, 8k rows", op="head_fwd", rows=8192, vocab=32000, k=4096, pad=0, dtype="bf16", index="i64"),
+        dict(name="head loss 8k rows", op="head_fwd", rows=8192, vocab=32000, k=4096, pad=0, dtype="bf16", index="i64"),
         # Both gradients of a ragged batch on a vocabulary and a width of odd sizes.
-        dict(name="head grad, odd sizes", op="head_bwd", rows=1021, vocab=50021, k=1003, pad=3, dtype="bf16",
+        dict(name="head grad odd sizes", op="head_bwd", rows=1021, vocab=50021, k=1003, pad=3, dtype="bf16",
              index="i32"),
         # A training micro-batch of the action expert's width in fp16: loss and gradients in one call.
-        dict(name="head loss+grad, expert f16", op="head_loss_grad", rows=2500, vocab=32000, k=1024, pad=0, dtype="f16",
+        dict(name="head loss+grad expert f16", op="head_loss_grad", rows=2500, vocab=32000, k=1024, pad=0, dtype="f16",
              index="i64"),
         # A training micro-batch of the 7B list's width on a large vocabulary.
-        dict(name="head loss+grad, 4k rows", op="head_loss_grad", rows=4096, vocab=131072, k=4096, pad=0, dtype="bf16",
+        dict(name="head loss+grad 4k rows", op="head_loss_grad", rows=4096, vocab=131072, k=4096, pad=0, dtype="bf16",
              index="i64"),
         # A few small tensors: the step's latency.
-        dict(name="adamw 8 bits, small list", op="adamw", count=12, low=16, high=16384, layout=1, whole=0, grad="f32",
+        dict(name="adamw 8 bits small list", op="adamw", count=12, low=16, high=16384, layout=1, whole=0, grad="f32",
              masters=False, step=10, norm=5.0),
         # A list of ragged tensors, a quarter of which keep their moments in 32 bits.
-        dict(name="adamw 8 bits, ragged list", op="adamw", count=600, low=3, high=600000, layout=2, whole=150, grad="f32",
+        dict(name="adamw 8 bits ragged list", op="adamw", count=600, low=3, high=600000, layout=2, whole=150, grad="f32",
              masters=False, step=1000, norm=0.5),
         # The 302 M parameters of the action expert: bf16 gradients, bf16 copies of the fp32 weights.
-        dict(name="adamw 8 bits, 302M", op="adamw", count=72, low=4194304, high=4195840, layout=3, whole=4, grad="bf16",
+        dict(name="adamw 8 bits 302M", op="adamw", count=72, low=4194304, high=4195840, layout=3, whole=4, grad="bf16",
              masters=True, step=2000, norm=20.0),
     ]
 
