@@ -1,7 +1,7 @@
 /*
  * soma_ops.h -- C ABI of the training operators for GB300 (sm_103a) whose
- * gradients the optimizer step of soma_opt.h takes: layer norm, linear layer
- * and distillation loss, each forward and backward.
+ * gradients the optimizer step of soma_opt.h takes: layer norm, linear layer,
+ * distillation loss and embedding, each forward and backward.
  *
  * Matrices are row-major with unit stride along a row; `*_stride` is the
  * distance between rows in elements (at least the row's length; ignored when
@@ -169,6 +169,34 @@ soma_status_t soma_distill_loss_grad(int32_t device, const void *logits, int64_t
                                      void *dlogits, int64_t dlogits_stride, int64_t rows, int64_t vocab,
                                      int64_t top, int32_t dtype, int32_t teacher_dtype, int32_t index_type,
                                      void *stream);
+
+/* ---- embedding ---------------------------------------------------------------
+ *   y_r         = scale * weight_{i_r}
+ *   dweight_v   = scale * sum_{r: i_r = v} dy_r      (+ dweight_v, with accumulate)
+ * Row r's token i_r is index[r / length][r % length], int32 or int64: a matrix
+ * of batch x length tokens whose rows are index_stride apart, so that a slice
+ * of a batch of texts needs no copy.  rows = batch * length, at most
+ * 2^31 - 1.  A token outside [0, vocab), such as -1, stands for no entry: its
+ * y is 0 and its dy is not read.  weight[vocab][cols], y and dy [rows][cols]
+ * and dweight[vocab][cols] are in dtype; 1 <= vocab, cols <= 2^30; scale is
+ * finite.
+ *
+ * Sums are fp32, of a token's rows in rising order (64 sorted positions at a
+ * time), times scale, rounded once.  Without accumulate all of dweight is
+ * written, rows without a token with 0; with it only the rows of tokens that
+ * occur are read and written (a table shared with the last linear layer takes
+ * that one's gradient first). */
+soma_status_t soma_embedding_forward(int32_t device, const void *weight, int64_t weight_stride, const void *index,
+                                     int64_t index_stride, int64_t batch, int64_t length, void *y, int64_t y_stride,
+                                     int64_t vocab, int64_t cols, int32_t dtype, int32_t index_type, double scale,
+                                     void *stream);
+soma_status_t soma_embedding_backward_workspace(int32_t device, int64_t rows, int64_t vocab, int64_t cols,
+                                                int64_t *bytes);
+soma_status_t soma_embedding_backward(int32_t device, const void *dy, int64_t dy_stride, const void *index,
+                                      int64_t index_stride, int64_t batch, int64_t length, void *dweight,
+                                      int64_t dweight_stride, int32_t accumulate, void *workspace,
+                                      int64_t workspace_bytes, int64_t vocab, int64_t cols, int32_t dtype,
+                                      int32_t index_type, double scale, void *stream);
 
 #ifdef __cplusplus
 }

@@ -42,6 +42,10 @@ SIGNATURES = {
                                    _I32, _I32, _I32, _P]),
     "soma_distill_loss_grad": (_S, [_I32, _P, _I64, _P, _I64, _P, _I64, _P, _D, _P, _P, _P, _I64, _I64, _I64, _I64,
                                     _I32, _I32, _I32, _P]),
+    "soma_embedding_forward": (_S, [_I32, _P, _I64, _P, _I64, _I64, _I64, _P, _I64, _I64, _I64, _I32, _I32, _D, _P]),
+    "soma_embedding_backward_workspace": (_S, [_I32, _I64, _I64, _I64, _I64P]),
+    "soma_embedding_backward": (_S, [_I32, _P, _I64, _P, _I64, _I64, _I64, _P, _I64, _I32, _P, _I64, _I64, _I64, _I32,
+                                     _I32, _D, _P]),
 }
 
 _lib = None

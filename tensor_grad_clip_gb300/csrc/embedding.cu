@@ -1,0 +1,664 @@
+// Embedding lookup and its gradient (formulas in soma_ops.h).
+//
+// Forward: a warp copies a piece of a row, scaled, in 16-byte vectors of the
+// output; a table's row that starts elsewhere in its 16-byte word is shifted
+// into place.  HBM bound: rows read and written once.
+//
+// Backward: the tokens are sorted with their rows (stable, so that a token's
+// rows rise), then every chunk of the sorted order adds its rows in fp32 and
+// writes the tokens that lie wholly inside it; a token that passes over a
+// chunk's border leaves partial sums, which a last kernel joins in order.  So
+// no token is too frequent for one CTA, no atomic touches a gradient, and the
+// same call gives the same bits.  Rows of the table without a token are
+// zeroed by other CTAs of the same launch, from a bitmap that the sort leaves.
+#include <math.h>
+
+#include <algorithm>
+#include <utility>
+
+#include "ops_device.cuh"
+#include "ops_kernels.h"
+#include "soma_ops.h"
+#include "tcgen05.cuh"
+
+namespace soma {
+namespace {
+
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Token of row r, or -1 where it is outside the vocabulary.
+__device__ __forceinline__ int token_at(const TokenArgs& t, int64_t r, int vocab) {
+    const int64_t at = t.length == t.stride ? r : r / t.length * t.stride + r % t.length;
+    const int64_t v = t.type == SOMA_INDEX_I64 ? __ldg(static_cast<const long long*>(t.index) + at)
+                                               : (int64_t)__ldg(static_cast<const int*>(t.index) + at);
+    return v >= 0 && v < vocab ? (int)v : -1;
+}
+
+// ---- forward -------------------------------------------------------------------
+
+constexpr int kFwdThreads = 128;
+constexpr int kFwdDeep = 4;                   // vectors in flight per lane
+constexpr int kFwdPiece = 32 * kFwdDeep;      // vectors of a row that one warp copies
+
+template <typename T>
+__global__ void __launch_bounds__(kFwdThreads) lookup_kernel(const __grid_constant__ EmbeddingArgs a, int pieces) {
+    constexpr int kVec = 16 / sizeof(T);
+    const int lane = threadIdx.x & 31;
+    const int64_t item = (int64_t)blockIdx.x * (kFwdThreads / 32) + (threadIdx.x >> 5);
+    const int64_t r = item / pieces;
+    if (r >= a.rows) return;
+    const int piece = (int)(item - r * pieces);
+    const int v = token_at(a.tokens, r, a.vocab);
+    T* dst = static_cast<T*>(a.out) + r * a.out_stride;
+    // elements before the first whole word of the output's row, and its whole words
+    const int head = min(a.cols, (int)((16 - ((uintptr_t)dst & 15)) & 15) / (int)sizeof(T));
+    const int words = (a.cols - head) / kVec;
+    const T* table = static_cast<const T*>(a.table);
+    const T* src = table + (int64_t)max(v, 0) * a.table_stride;
+    if (piece == 0) {
+        // the ends of the row, one element a lane
+        const int ends = a.cols - words * kVec;
+        if (lane < ends) {
+            const int c = lane < head ? lane : words * kVec + lane;
+            dst[c] = from_f32<T>(v < 0 ? 0.f : to_f32(src[c]) * a.scale);
+        }
+    }
+    const int i0 = piece * kFwdPiece + lane;
+    if (i0 - lane >= words) return;
+    uint4* out = reinterpret_cast<uint4*>(dst + head);
+    if (v < 0) {
+        for (int q = 0; q < kFwdDeep; ++q)
+            if (i0 + 32 * q < words) out[i0 + 32 * q] = make_uint4(0, 0, 0, 0);
+        return;
+    }
+    const int phase = (int)((uintptr_t)(src + head) & 15);
+    const uint4* in = reinterpret_cast<const uint4*>((uintptr_t)(src + head) - phase);
+    // words that lie inside the table
+    const uintptr_t end = (uintptr_t)(table + (int64_t)(a.vocab - 1) * a.table_stride + a.cols);
+    uint4 u[kFwdDeep], w[kFwdDeep];
+#pragma unroll
+    for (int q = 0; q < kFwdDeep; ++q) {
+        const int i = i0 + 32 * q;
+        if (i >= words) break;
+        const bool inside = (uintptr_t)(in + i) >= (uintptr_t)table && (uintptr_t)(in + i + (phase ? 2 : 1)) <= end;
+        if (inside) {
+            u[q] = __ldg(in + i);
+            if (phase) w[q] = __ldg(in + i + 1);
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < kFwdDeep; ++q) {
+        const int i = i0 + 32 * q;
+        if (i >= words) break;
+        const bool inside = (uintptr_t)(in + i) >= (uintptr_t)table && (uintptr_t)(in + i + (phase ? 2 : 1)) <= end;
+        float x[kVec];
+        if (inside) {
+            widen16(phase ? shifted<T>(u[q], w[q], phase) : u[q], x, T{});
+        } else {
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) x[e] = to_f32(src[head + i * kVec + e]);
+        }
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) x[e] *= a.scale;
+        __stcs(out + i, narrow16(x, T{}));
+    }
+}
+
+// ---- sorting the tokens ----------------------------------------------------------
+//
+// Least significant digit first, stable: a warp ranks its items 32 at a time,
+// counting equal digits below each lane.  Tokens outside the vocabulary sort
+// last, as `vocab`.
+
+constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
+constexpr int kMaxDigits = 512;
+constexpr int kSortCtas = 8;                    // of the one-cluster sort, at most
+constexpr int kSortShare = 11776;                // items of one of its CTAs, at most: 16 bytes each beside 36 KB of counts
+constexpr int kSortTile = 8192;                 // items of a CTA of the many-launch sort
+
+struct SortArgs {
+    TokenArgs tokens;
+    int64_t rows;
+    int32_t vocab;
+    int32_t digit_bits, passes;
+    uint32_t* keys;       // [rows] sorted tokens
+    uint32_t* order;      // [rows] their rows
+    uint32_t* keys2;      // the many-launch sort's second buffers
+    uint32_t* order2;
+    uint32_t* counts;     // [digits][CTAs] of the many-launch sort
+    uint32_t* hit;        // bitmap of the tokens that occur, or nullptr
+    int32_t hit_words;
+    int32_t share;        // items of a CTA
+};
+
+// Histograms of the warps' items; then `hist` holds for each warp and digit
+// how many items of earlier warps have the digit, and total[] how many have it.
+template <typename Key>
+__device__ __forceinline__ void count_digits(uint32_t (*hist)[kMaxDigits], uint32_t* total, int n, int digits, Key key) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int per = (n + 32 * kSortWarps - 1) / (32 * kSortWarps) * 32;  // items of a warp
+    for (int d = threadIdx.x; d < digits * kSortWarps; d += kSortThreads) hist[d / digits][d % digits] = 0;
+    __syncthreads();
+    for (int i = warp * per + lane; i < min(n, (warp + 1) * per); i += 32) atomicAdd(&hist[warp][key(i)], 1u);
+    __syncthreads();
+    for (int d = threadIdx.x; d < digits; d += kSortThreads) {
+        uint32_t sum = 0;
+        for (int w = 0; w < kSortWarps; ++w) {
+            const uint32_t c = hist[w][d];
+            hist[w][d] = sum;
+            sum += c;
+        }
+        total[d] = sum;
+    }
+    __syncthreads();
+}
+
+// Hands item i, of digit key(i), to put(i, place): start[d] is the place of
+// the CTA's first item of digit d.
+template <typename Key, typename Put>
+__device__ __forceinline__ void scatter_digits(uint32_t (*hist)[kMaxDigits], const uint32_t* start, int n, Key key, Put put) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int per = (n + 32 * kSortWarps - 1) / (32 * kSortWarps) * 32;
+    const int end = min(n, (warp + 1) * per);
+    for (int i0 = warp * per; i0 < end; i0 += 32) {
+        const int i = i0 + lane;
+        const bool on = i < end;
+        const uint32_t d = on ? key(i) : 0xffffffffu;
+        const uint32_t peers = __match_any_sync(0xffffffffu, d);
+        uint32_t place = 0;
+        if (on) place = start[d] + hist[warp][d] + __popc(peers & ((1u << lane) - 1));
+        __syncwarp();
+        if (on && lane == 31 - __clz(peers)) hist[warp][d] += __popc(peers);
+        __syncwarp();
+        if (on) put(i, place);
+    }
+}
+
+// Exclusive sums over n <= kMaxDigits values, in place.
+__device__ __forceinline__ void scan_digits(uint32_t* x, int n, uint32_t* scratch) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = threadIdx.x;
+    static_assert(kMaxDigits == kSortThreads, "one digit per thread");
+    const uint32_t own = d < n ? x[d] : 0;
+    uint32_t sum = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t t = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += t;
+    }
+    if (lane == 31) scratch[warp] = sum;
+    __syncthreads();
+    uint32_t before = 0;
+    for (int w = 0; w < warp; ++w) before += scratch[w];
+    if (d < n) x[d] = before + sum - own;
+    __syncthreads();
+}
+
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// The whole sort in one launch: one cluster whose CTAs hold `share` items each
+// in shared memory and hand each other the items of a pass through it.
+__global__ void __launch_bounds__(kSortThreads) cluster_sort_kernel(const __grid_constant__ SortArgs a) {
+    extern __shared__ uint32_t sort_smem[];
+    __shared__ uint32_t hist[kSortWarps][kMaxDigits];
+    __shared__ uint32_t total[kMaxDigits], start[kMaxDigits], scratch[kSortWarps];
+    launch_dependents();
+    const int rank = blockIdx.x, ctas = gridDim.x, share = a.share;
+    const int begin = rank * share, n = max(0, min(share, (int)a.rows - begin));
+    uint32_t* keys[2] = {sort_smem, sort_smem + 2 * share};
+    uint32_t* order[2] = {sort_smem + share, sort_smem + 3 * share};
+    for (int i = threadIdx.x; i < n; i += kSortThreads) {
+        const int v = token_at(a.tokens, begin + i, a.vocab);
+        keys[0][i] = v < 0 ? a.vocab : v;
+        order[0][i] = begin + i;
+    }
+    if (a.hit)
+        for (int i = rank * kSortThreads + threadIdx.x; i < a.hit_words; i += ctas * kSortThreads) a.hit[i] = 0;
+    __syncthreads();
+    const int digits = 1 << a.digit_bits;
+    for (int p = 0; p < a.passes; ++p) {
+        const int from = p & 1, shift = p * a.digit_bits;
+        auto key = [&](int i) { return keys[from][i] >> shift & (digits - 1); };
+        count_digits(hist, total, n, digits, key);
+        cluster_sync_all();  // every CTA's totals are there (and, once, the cleared bitmap)
+        for (int d = threadIdx.x; d < digits; d += kSortThreads) {
+            uint32_t all = 0, before = 0;
+            for (int c = 0; c < ctas; ++c) {
+                if (c == rank) before = all;
+                all += ld_cluster_u32(cluster_map(smem_addr(total + d), c));
+            }
+            start[d] = all;
+            hist[0][d] += before;
+            for (int w = 1; w < kSortWarps; ++w) hist[w][d] += before;
+        }
+        __syncthreads();
+        scan_digits(start, digits, scratch);
+        const bool last = p == a.passes - 1;
+        scatter_digits(hist, start, n, key, [&](int i, uint32_t place) {
+            const uint32_t k = keys[from][i], r = order[from][i];
+            if (last) {
+                a.keys[place] = k;
+                a.order[place] = r;
+                if (a.hit && k < (uint32_t)a.vocab) atomicOr(a.hit + (k >> 5), 1u << (k & 31));
+            } else {
+                const uint32_t c = place / share, at = place - c * share;
+                st_cluster_u32(cluster_map(smem_addr(keys[from ^ 1] + at), c), k);
+                st_cluster_u32(cluster_map(smem_addr(order[from ^ 1] + at), c), r);
+            }
+        });
+        cluster_sync_all();  // the items have arrived; nobody reads this pass's totals any more
+    }
+}
+
+// The same in many launches, a pass in three: digits counted, places found,
+// items moved.
+__global__ void __launch_bounds__(kSortThreads) count_kernel(const __grid_constant__ SortArgs a, int pass) {
+    __shared__ uint32_t hist[kSortWarps][kMaxDigits];
+    __shared__ uint32_t total[kMaxDigits];
+    const int64_t begin = (int64_t)blockIdx.x * kSortTile;
+    const int n = (int)min((int64_t)kSortTile, a.rows - begin);
+    const int digits = 1 << a.digit_bits, shift = pass * a.digit_bits;
+    const uint32_t* keys = pass & 1 ? a.keys2 : a.keys;
+    if (pass == 0) {
+        for (int i = threadIdx.x; i < n; i += kSortThreads) {
+            const int v = token_at(a.tokens, begin + i, a.vocab);
+            a.keys[begin + i] = v < 0 ? a.vocab : v;
+            a.order[begin + i] = (uint32_t)(begin + i);
+            if (a.hit && v >= 0) atomicOr(a.hit + (v >> 5), 1u << (v & 31));
+        }
+        __syncthreads();
+    }
+    count_digits(hist, total, n, digits, [&](int i) { return keys[begin + i] >> shift & (digits - 1); });
+    for (int d = threadIdx.x; d < digits; d += kSortThreads) a.counts[(int64_t)d * gridDim.x + blockIdx.x] = total[d];
+}
+
+// Exclusive sums over all counts, in place, by one CTA.
+__global__ void __launch_bounds__(kSortThreads) place_kernel(uint32_t* counts, int64_t n) {
+    __shared__ uint32_t sums[kSortThreads], scratch[kSortWarps];
+    uint32_t carry = 0;
+    constexpr int kEach = 8;
+    for (int64_t at = 0; at < n; at += kSortThreads * kEach) {
+        uint32_t x[kEach], sum = 0;
+        const int64_t i0 = at + threadIdx.x * kEach;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            x[k] = i0 + k < n ? counts[i0 + k] : 0;
+            sum += x[k];
+        }
+        sums[threadIdx.x] = sum;
+        __syncthreads();
+        scan_digits(sums, kSortThreads, scratch);
+        uint32_t before = carry + sums[threadIdx.x];
+        if (threadIdx.x == kSortThreads - 1) scratch[0] = sums[threadIdx.x] + sum;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            if (i0 + k < n) counts[i0 + k] = before;
+            before += x[k];
+        }
+        __syncthreads();
+        carry += scratch[0];
+        __syncthreads();
+    }
+}
+
+__global__ void __launch_bounds__(kSortThreads) move_kernel(const __grid_constant__ SortArgs a, int pass) {
+    __shared__ uint32_t hist[kSortWarps][kMaxDigits];
+    __shared__ uint32_t start[kMaxDigits];
+    const int64_t begin = (int64_t)blockIdx.x * kSortTile;
+    const int n = (int)min((int64_t)kSortTile, a.rows - begin);
+    const int digits = 1 << a.digit_bits, shift = pass * a.digit_bits;
+    const uint32_t *keys = pass & 1 ? a.keys2 : a.keys, *order = pass & 1 ? a.order2 : a.order;
+    uint32_t *to_keys = pass & 1 ? a.keys : a.keys2, *to_order = pass & 1 ? a.order : a.order2;
+    auto key = [&](int i) { return keys[begin + i] >> shift & (digits - 1); };
+    count_digits(hist, start, n, digits, key);
+    for (int d = threadIdx.x; d < digits; d += kSortThreads) start[d] = a.counts[(int64_t)d * gridDim.x + blockIdx.x];
+    __syncthreads();
+    scatter_digits(hist, start, n, key, [&](int i, uint32_t place) {
+        to_keys[place] = keys[begin + i];
+        to_order[place] = order[begin + i];
+    });
+}
+
+// ---- sums of the sorted rows -------------------------------------------------------
+
+constexpr int kSumThreads = 128;
+constexpr int kChunk = 64;       // sorted positions of a CTA
+constexpr int kSumDeep = 8;      // rows in flight per thread
+constexpr int kZeroBytes = 64 * 1024;  // of a CTA that zeroes rows, about
+
+struct SumArgs {
+    const uint32_t* keys;
+    const uint32_t* order;
+    const uint32_t* hit;
+    float* partials;      // [chunks][2][cols]: of a chunk's first token, if it began earlier, and its last, if it goes on
+    const void* dy;
+    int64_t dy_stride;
+    void* out;
+    int64_t out_stride;
+    int64_t rows;
+    int32_t vocab, cols;
+    int32_t chunks, col_blocks;   // sum_kernel: chunks x col_blocks CTAs, the others zero rows
+    int32_t zero_words;           // words of the bitmap per zeroing CTA
+    float scale;
+    bool accumulate;
+};
+
+// A thread's columns: a vector of kVec (kWhole: rows of dy and out start on
+// 16-byte boundaries and hold whole vectors), else kVec columns kSumThreads apart.
+template <typename T, bool kWhole>
+struct Columns {
+    static constexpr int kVec = 16 / sizeof(T);
+    int c0, cols;
+    __device__ __forceinline__ Columns(int block, int n) : cols(n) {
+        c0 = kWhole ? (block * kSumThreads + (int)threadIdx.x) * kVec : block * kSumThreads * kVec + (int)threadIdx.x;
+    }
+    __device__ __forceinline__ int col(int e) const { return kWhole ? c0 + e : c0 + e * kSumThreads; }
+    struct Raw {
+        uint4 w;
+        T x[kWhole ? 1 : kVec];
+    };
+    __device__ __forceinline__ void load(const T* row, Raw& r) const {
+        if (kWhole) {
+            if (c0 < cols) r.w = __ldcs(reinterpret_cast<const uint4*>(row + c0));
+        } else {
+#pragma unroll
+            for (int e = 0; e < kVec; ++e)
+                if (col(e) < cols) r.x[kWhole ? 0 : e] = row[col(e)];
+        }
+    }
+    __device__ __forceinline__ void add(const Raw& r, float (&sum)[kVec]) const {
+        if (kWhole) {
+            float x[kVec];
+            widen16(r.w, x, T{});
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) sum[e] += x[e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) sum[e] += to_f32(r.x[kWhole ? 0 : e]);
+        }
+    }
+    // out (+)= scale * sum
+    __device__ __forceinline__ void store(T* row, float (&sum)[kVec], float scale, bool accumulate) const {
+        if (kWhole) {
+            if (c0 >= cols) return;
+            float x[kVec] = {};
+            if (accumulate) widen16(*reinterpret_cast<const uint4*>(row + c0), x, T{});
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) x[e] = fmaf(sum[e], scale, x[e]);
+            *reinterpret_cast<uint4*>(row + c0) = narrow16(x, T{});
+        } else {
+#pragma unroll
+            for (int e = 0; e < kVec; ++e)
+                if (col(e) < cols)
+                    row[col(e)] = from_f32<T>(fmaf(sum[e], scale, accumulate ? to_f32(row[col(e)]) : 0.f));
+        }
+    }
+    __device__ __forceinline__ void store_partial(float* row, const float (&sum)[kVec]) const {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e)
+            if (col(e) < cols) row[col(e)] = sum[e];
+    }
+};
+
+// Zeroes the rows without a token of the bitmap's words [w0, w1).
+template <typename T>
+__device__ __forceinline__ void zero_rows(const SumArgs& a, int w0, int w1) {
+    constexpr int kVec = 16 / sizeof(T);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int w = w0; w < w1; ++w) {
+        const uint32_t hit = __ldcg(a.hit + w);
+        for (int b = warp; b < 32; b += kSumThreads / 32) {
+            const int64_t v = (int64_t)w * 32 + b;
+            if (v >= a.vocab || (hit >> b & 1)) continue;
+            T* row = static_cast<T*>(a.out) + v * a.out_stride;
+            const int head = min(a.cols, (int)((16 - ((uintptr_t)row & 15)) & 15) / (int)sizeof(T));
+            const int words = (a.cols - head) / kVec;
+            if (lane < a.cols - words * kVec) row[lane < head ? lane : words * kVec + lane] = from_f32<T>(0.f);
+            uint4* body = reinterpret_cast<uint4*>(row + head);
+            for (int i = lane; i < words; i += 32) __stcs(body + i, make_uint4(0, 0, 0, 0));
+        }
+    }
+}
+
+template <typename T, bool kWhole>
+__global__ void __launch_bounds__(kSumThreads) sum_kernel(const __grid_constant__ SumArgs a) {
+    __shared__ uint32_t keys[kChunk + 2], order[kChunk];
+    launch_dependents();
+    wait_for_previous();
+    const int sums = a.chunks * a.col_blocks;
+    if ((int)blockIdx.x >= sums) {
+        const int w0 = ((int)blockIdx.x - sums) * a.zero_words;
+        zero_rows<T>(a, w0, min(w0 + a.zero_words, (a.vocab + 31) / 32));
+        return;
+    }
+    using C = Columns<T, kWhole>;
+    const int chunk = (int)blockIdx.x / a.col_blocks;
+    const C columns((int)blockIdx.x % a.col_blocks, a.cols);
+    const int64_t begin = (int64_t)chunk * kChunk;
+    const int n = (int)min((int64_t)kChunk, a.rows - begin);
+    constexpr uint32_t kNone = 0xffffffffu;
+    for (int i = threadIdx.x; i < n + 2; i += kSumThreads) {  // one neighbour on each side
+        const int64_t at = begin + i - 1;
+        keys[i] = at >= 0 && at < a.rows ? __ldcg(a.keys + at) : kNone;
+        if (i < n) order[i] = __ldcg(a.order + begin + i);
+    }
+    __syncthreads();
+    const T* dy = static_cast<const T*>(a.dy);
+    float sum[C::kVec] = {};
+    bool began_here = keys[0] != keys[1];
+    for (int i0 = 0; i0 < n && keys[1 + i0] < (uint32_t)a.vocab; i0 += kSumDeep) {
+        typename C::Raw raw[kSumDeep];
+#pragma unroll
+        for (int q = 0; q < kSumDeep; ++q)
+            if (i0 + q < n) columns.load(dy + (int64_t)order[i0 + q] * a.dy_stride, raw[q]);
+#pragma unroll
+        for (int q = 0; q < kSumDeep; ++q) {
+            const int i = i0 + q;
+            if (i >= n) break;
+            const uint32_t key = keys[1 + i];
+            if (key >= (uint32_t)a.vocab) break;
+            columns.add(raw[q], sum);
+            const bool ends = key != keys[2 + i];
+            if (!ends && i + 1 < n) continue;
+            if (ends && began_here)
+                columns.store(static_cast<T*>(a.out) + (int64_t)key * a.out_stride, sum, a.scale, a.accumulate);
+            else
+                columns.store_partial(a.partials + ((int64_t)chunk * 2 + (began_here ? 1 : 0)) * a.cols, sum);
+            began_here = true;
+#pragma unroll
+            for (int e = 0; e < C::kVec; ++e) sum[e] = 0.f;
+        }
+    }
+}
+
+// A token that goes on after chunk c but began in it: its partial sums from
+// chunk c on, in order.
+template <typename T, bool kWhole>
+__global__ void __launch_bounds__(kSumThreads) join_kernel(const __grid_constant__ SumArgs a) {
+    launch_dependents();
+    wait_for_previous();
+    using C = Columns<T, kWhole>;
+    const int chunk = (int)blockIdx.x / a.col_blocks;
+    const int64_t begin = (int64_t)chunk * kChunk, last = begin + kChunk - 1;  // (there is a chunk after this one)
+    const uint32_t key = __ldcg(a.keys + last);
+    if (key >= (uint32_t)a.vocab || __ldcg(a.keys + last + 1) != key) return;
+    if (begin > 0 && __ldcg(a.keys + begin - 1) == key) return;  // began earlier
+    const C columns((int)blockIdx.x % a.col_blocks, a.cols);
+    float sum[C::kVec];
+    auto at = [&](int c, int which, int e) {
+        return columns.col(e) < a.cols ? __ldcg(a.partials + ((int64_t)c * 2 + which) * a.cols + columns.col(e)) : 0.f;
+    };
+#pragma unroll
+    for (int e = 0; e < C::kVec; ++e) sum[e] = at(chunk, 1, e);
+    // chunks whose first key is the token and that hold nothing else, then the one where it ends
+    int end = chunk + 1;
+    while (end + 1 < a.chunks && __ldcg(a.keys + (int64_t)(end + 1) * kChunk) == key) ++end;
+    for (int c = chunk + 1; c <= end; ++c) {
+#pragma unroll
+        for (int e = 0; e < C::kVec; ++e) sum[e] += at(c, 0, e);
+    }
+    columns.store(static_cast<T*>(a.out) + (int64_t)key * a.out_stride, sum, a.scale, a.accumulate);
+}
+
+// ---- host side -------------------------------------------------------------------
+
+int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
+
+// Digits that the tokens and `vocab` itself need, in passes of at most 9 bits.
+void plan_digits(SortArgs& s) {
+    int bits = 1;
+    while (((int64_t)1 << bits) <= s.vocab) ++bits;
+    s.passes = (bits + 8) / 9;
+    s.digit_bits = (bits + s.passes - 1) / s.passes;
+}
+
+bool one_cluster(int64_t rows) { return rows <= (int64_t)kSortCtas * kSortShare; }
+
+// The workspace: sorted tokens and rows, bitmap, partial sums, and what the
+// many-launch sort needs.
+struct Layout {
+    int64_t keys, order, hit, partials, keys2, order2, counts, bytes;
+    int64_t chunks;
+    Layout(int64_t rows, int64_t vocab, int64_t cols) {
+        chunks = (rows + kChunk - 1) / kChunk;
+        int64_t at = 0;
+        auto take = [&](int64_t n) { const int64_t here = at; at += align256(n); return here; };
+        keys = take(rows * 4);
+        order = take(rows * 4);
+        hit = take((vocab + 31) / 32 * 4);
+        partials = take(chunks > 1 ? chunks * 2 * cols * 4 : 0);
+        const bool many = !one_cluster(rows);
+        keys2 = take(many ? rows * 4 : 0);
+        order2 = take(many ? rows * 4 : 0);
+        counts = take(many ? (rows + kSortTile - 1) / kSortTile * kMaxDigits * 4 : 0);
+        bytes = at;
+    }
+};
+
+int launch_after(const void* kernel, int64_t grid, int threads, void** args, void* stream) {
+    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = (cudaStream_t)stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return (int)cudaLaunchKernelExC(&cfg, kernel, args);
+}
+
+int launch_sort(SortArgs& s, void* stream) {
+    cudaStream_t st = (cudaStream_t)stream;
+    plan_digits(s);
+    if (one_cluster(s.rows)) {
+        int ctas = 1;
+        while (ctas < kSortCtas && (int64_t)ctas * 1024 < s.rows) ctas *= 2;
+        s.share = (int32_t)((s.rows + ctas - 1) / ctas);
+        const int smem = s.share * 16;
+        if (const int e = allow_smem((const void*)cluster_sort_kernel, smem)) return e;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(ctas);
+        cfg.blockDim = dim3(kSortThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = ctas;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        void* args[] = {&s};
+        return (int)cudaLaunchKernelExC(&cfg, (const void*)cluster_sort_kernel, args);
+    }
+    if (s.hit)
+        if (const int e = cudaMemsetAsync(s.hit, 0, (size_t)s.hit_words * 4, st)) return e;
+    const int tiles = (int)((s.rows + kSortTile - 1) / kSortTile);
+    if (s.passes & 1) {  // the last pass ends in the first buffers
+        std::swap(s.keys, s.keys2);
+        std::swap(s.order, s.order2);
+    }
+    for (int p = 0; p < s.passes; ++p) {
+        count_kernel<<<tiles, kSortThreads, 0, st>>>(s, p);
+        place_kernel<<<1, kSortThreads, 0, st>>>(s.counts, (int64_t)tiles << s.digit_bits);
+        move_kernel<<<tiles, kSortThreads, 0, st>>>(s, p);
+    }
+    return (int)cudaGetLastError();
+}
+
+}  // namespace
+
+int launch_embedding_fwd(const EmbeddingArgs& a, void* stream) {
+    return with_type(a.dtype, [&](auto t) {
+        using T = decltype(t);
+        const int vectors = (a.cols + 16 / (int)sizeof(T) - 1) / (16 / (int)sizeof(T));
+        int pieces = std::max(1, (vectors + kFwdPiece - 1) / kFwdPiece);
+        const int64_t grid = (a.rows * pieces + kFwdThreads / 32 - 1) / (kFwdThreads / 32);
+        if (grid > 0x7fffffff) return (int)cudaErrorInvalidConfiguration;
+        lookup_kernel<T><<<(unsigned)grid, kFwdThreads, 0, (cudaStream_t)stream>>>(a, pieces);
+        return (int)cudaGetLastError();
+    });
+}
+
+int64_t embedding_bwd_workspace(int64_t rows, int64_t vocab, int64_t cols) { return Layout(rows, vocab, cols).bytes; }
+
+int launch_embedding_bwd(const EmbeddingArgs& a, const void* dy, int64_t dy_stride, bool accumulate, void* workspace,
+                         void* stream) {
+    const Layout at(a.rows, a.vocab, a.cols);
+    char* ws = static_cast<char*>(workspace);
+    SortArgs s{};
+    s.tokens = a.tokens;
+    s.rows = a.rows;
+    s.vocab = a.vocab;
+    s.keys = reinterpret_cast<uint32_t*>(ws + at.keys);
+    s.order = reinterpret_cast<uint32_t*>(ws + at.order);
+    s.keys2 = reinterpret_cast<uint32_t*>(ws + at.keys2);
+    s.order2 = reinterpret_cast<uint32_t*>(ws + at.order2);
+    s.counts = reinterpret_cast<uint32_t*>(ws + at.counts);
+    s.hit = accumulate ? nullptr : reinterpret_cast<uint32_t*>(ws + at.hit);
+    s.hit_words = (a.vocab + 31) / 32;
+    SumArgs u{};
+    u.keys = s.keys;
+    u.order = s.order;
+    if (const int e = launch_sort(s, stream)) return e;
+    return with_type(a.dtype, [&](auto t) {
+        using T = decltype(t);
+        constexpr int kVec = 16 / sizeof(T);
+        u.hit = s.hit;
+        u.partials = reinterpret_cast<float*>(ws + at.partials);
+        u.dy = dy;
+        u.dy_stride = dy_stride;
+        u.out = a.out;
+        u.out_stride = a.out_stride;
+        u.rows = a.rows;
+        u.vocab = a.vocab;
+        u.cols = a.cols;
+        u.chunks = (int32_t)at.chunks;
+        u.col_blocks = (a.cols + kSumThreads * kVec - 1) / (kSumThreads * kVec);
+        u.scale = a.scale;
+        u.accumulate = accumulate;
+        const int64_t row_bytes = (int64_t)a.cols * sizeof(T);
+        u.zero_words = (int32_t)std::max<int64_t>(1, kZeroBytes / (32 * row_bytes));
+        const int64_t sums = (int64_t)u.chunks * u.col_blocks;
+        if (sums > 0x3fffffff) return (int)cudaErrorInvalidConfiguration;
+        const int64_t zeros = accumulate ? 0 : (s.hit_words + u.zero_words - 1) / u.zero_words;
+        const bool whole = a.cols % kVec == 0 && (uintptr_t)dy % 16 == 0 && (uintptr_t)a.out % 16 == 0 &&
+                           (a.rows == 1 || dy_stride % kVec == 0) && (a.vocab == 1 || a.out_stride % kVec == 0);
+        void* args[] = {&u};
+        int e = launch_after(whole ? (const void*)sum_kernel<T, true> : (const void*)sum_kernel<T, false>, sums + zeros,
+                             kSumThreads, args, stream);
+        if (e != cudaSuccess || u.chunks < 2) return e;
+        return launch_after(whole ? (const void*)join_kernel<T, true> : (const void*)join_kernel<T, false>,
+                            (int64_t)(u.chunks - 1) * u.col_blocks, kSumThreads, args, stream);
+    });
+}
+
+}  // namespace soma

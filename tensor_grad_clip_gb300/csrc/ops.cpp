@@ -16,62 +16,14 @@
 #include <tuple>
 #include <utility>
 
+#include "ops_host.h"
 #include "ops_kernels.h"
-#include "soma_kernels.h"
 
 namespace {
 
+using namespace soma;
+
 thread_local std::string g_error;
-
-soma_status_t fail(soma_status_t st, const char* fmt, ...) {
-    char buf[400];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    try {
-        g_error = std::string(soma_status_string(st)) + ": " + buf;
-    } catch (...) {  // no memory for the text: the status alone
-        g_error.clear();
-    }
-    return st;
-}
-
-soma_status_t cuda_status(int e, const char* what) {
-    if (e == cudaSuccess) return SOMA_OK;
-    cudaGetLastError();
-    return fail(SOMA_ERR_CUDA, "%s: %s (%d)", what, cudaGetErrorString((cudaError_t)e), e);
-}
-
-// Makes `dev` current for the scope and restores the caller's device.
-struct DeviceGuard {
-    int prev = -1, dev;
-    cudaError_t status;
-    explicit DeviceGuard(int d) : dev(d) {
-        status = cudaGetDevice(&prev);
-        if (status == cudaSuccess && prev != dev) status = cudaSetDevice(dev);
-    }
-    ~DeviceGuard() {
-        if (prev >= 0 && prev != dev) cudaSetDevice(prev);
-    }
-};
-
-// SM count of a device, looked up once.
-int sm_count(int device) {
-    static std::array<std::atomic<int>, 64> known{};
-    if (device < 0) return 0;
-    if (device < 64 && known[device].load(std::memory_order_relaxed) > 0) return known[device].load();
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    if (device < 64) known[device].store(n);
-    return n;
-}
-
-constexpr int64_t kMaxInt = 0x7fffffff;
-constexpr int64_t kMaxExtent = 1 << 30;  // of a dimension that kernels index with an int, sums of a few included
 
 std::mutex g_facts_mu;
 // (device, kernel, block or -1, shared memory) -> resident CTAs, or 1 where the shared memory is allowed
@@ -81,38 +33,6 @@ std::map<std::tuple<int, const void*, int, int>, int> g_facts;
 // at: layer norm, linear, distillation.
 using Counts = std::array<unsigned, 3>;
 std::map<int, Counts> g_gave_up;
-
-bool is_dtype(int32_t d) { return d == SOMA_DTYPE_F32 || d == SOMA_DTYPE_BF16 || d == SOMA_DTYPE_F16; }
-int size_of(int32_t d) { return d == SOMA_DTYPE_F32 ? 4 : 2; }
-int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
-
-// Checks a matrix argument.  A matrix without elements may be NULL.
-soma_status_t check_matrix(const char* name, const void* p, int64_t stride, int64_t rows, int64_t cols, int esize,
-                           bool optional = false) {
-    if (rows == 0 || cols == 0) return SOMA_OK;
-    if (!p) return optional ? SOMA_OK : fail(SOMA_ERR_INVALID_ARG, "%s is NULL", name);
-    if (rows > 1 && stride < cols)
-        return fail(SOMA_ERR_INVALID_ARG, "%s: stride %lld is below the row length %lld", name, (long long)stride,
-                    (long long)cols);
-    if (rows > 1 && stride > INT64_MAX / esize / rows)
-        return fail(SOMA_ERR_LIMIT, "%s: stride %lld x %lld rows does not fit 64 bits", name, (long long)stride,
-                    (long long)rows);
-    if ((uintptr_t)p % esize) return fail(SOMA_ERR_ALIGNMENT, "%s is not aligned to its element size", name);
-    return SOMA_OK;
-}
-
-soma_status_t check_vector(const char* name, const void* p, int64_t n, int esize, bool optional) {
-    return check_matrix(name, p, n, 1, n, esize, optional);
-}
-
-soma_status_t check_workspace(const void* workspace, int64_t have, int64_t need) {
-    if (need == 0) return SOMA_OK;
-    if (!workspace) return fail(SOMA_ERR_INVALID_ARG, "workspace is NULL, %lld bytes are needed", (long long)need);
-    if (have < need)
-        return fail(SOMA_ERR_LIMIT, "workspace has %lld bytes, %lld are needed", (long long)have, (long long)need);
-    if ((uintptr_t)workspace % 256) return fail(SOMA_ERR_ALIGNMENT, "workspace is not 256-byte aligned");
-    return SOMA_OK;
-}
 
 // A 16-bit operand of a matrix product: where it is, or the part of the
 // workspace that a copy with aligned rows takes.
@@ -135,19 +55,6 @@ struct Operand {
         return e;
     }
 };
-
-#define SOMA_TRY(x)                              \
-    do {                                         \
-        const soma_status_t st_ = (x);           \
-        if (st_ != SOMA_OK) return st_;          \
-    } while (0)
-
-// Start of a launching entry point, after its argument checks.
-#define SOMA_ON_DEVICE(device)                                                             \
-    DeviceGuard guard(device);                                                             \
-    if (guard.status != cudaSuccess) return cuda_status((int)guard.status, "cudaSetDevice"); \
-    const int sms = sm_count(device);                                                      \
-    if (sms <= 0) return fail(SOMA_ERR_CUDA, "no SM count for device %d", (int)(device))
 
 soma_status_t check_norm(int64_t rows, int64_t cols, int32_t dtype, int32_t param_dtype) {
     if (rows < 0) return fail(SOMA_ERR_INVALID_ARG, "rows < 0");
@@ -221,6 +128,39 @@ soma::DistillArgs distill_args(const void* logits, int64_t logits_stride, const 
 }  // namespace
 
 namespace soma {
+
+soma_status_t fail(soma_status_t st, const char* fmt, ...) {
+    char buf[400];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    try {
+        g_error = std::string(soma_status_string(st)) + ": " + buf;
+    } catch (...) {  // no memory for the text: the status alone
+        g_error.clear();
+    }
+    return st;
+}
+
+soma_status_t cuda_status(int e, const char* what) {
+    if (e == cudaSuccess) return SOMA_OK;
+    cudaGetLastError();
+    return fail(SOMA_ERR_CUDA, "%s: %s (%d)", what, cudaGetErrorString((cudaError_t)e), e);
+}
+
+int sm_count(int device) {
+    static std::array<std::atomic<int>, 64> known{};
+    if (device < 0) return 0;
+    if (device < 64 && known[device].load(std::memory_order_relaxed) > 0) return known[device].load();
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    if (device < 64) known[device].store(n);
+    return n;
+}
 
 int allow_smem(const void* kernel, int bytes) {
     int device = 0;

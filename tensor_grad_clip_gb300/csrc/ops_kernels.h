@@ -1,6 +1,5 @@
-// Argument blocks and launchers of the training operators (layer norm,
-// linear layer, distillation loss), shared by the host checks (ops.cpp) and
-// the kernels.  Every launcher returns the cudaError_t of its launches as int.
+// Argument blocks and launchers of the training operators, shared by the host
+// checks (ops.cpp, lm_ops.cpp) and the kernels.  Every launcher returns the cudaError_t of its launches as int.
 #pragma once
 
 #include <cstdint>
@@ -123,6 +122,32 @@ struct DistillArgs {
 enum DistillPass : int32_t { kDistillForward, kDistillBackward, kDistillLossGrad };
 
 int launch_distill(const DistillArgs& a, DistillPass pass, int sm_count, void* stream);
+
+// Tokens, in rows of `length` that are `stride` apart: row r's is at
+// (r / length) * stride + r % length.
+struct TokenArgs {
+    const void* index;
+    int64_t stride, length;
+    int32_t type;  // SOMA_INDEX_*
+};
+
+struct EmbeddingArgs {
+    TokenArgs tokens;
+    const void* table;      // forward
+    int64_t table_stride;
+    void* out;              // forward: [rows][cols]; backward: [vocab][cols]
+    int64_t out_stride;
+    int64_t rows;
+    int32_t vocab, cols;
+    int32_t dtype;
+    float scale;
+};
+
+int launch_embedding_fwd(const EmbeddingArgs& a, void* stream);
+int64_t embedding_bwd_workspace(int64_t rows, int64_t vocab, int64_t cols);
+// rows >= 1
+int launch_embedding_bwd(const EmbeddingArgs& a, const void* dy, int64_t dy_stride, bool accumulate, void* workspace,
+                         void* stream);
 
 // How often a bounded wait inside a kernel of the current device has run out:
 // a count that only grows (modulo 2^32).  The copy waits for the legacy default

@@ -34,7 +34,8 @@ from . import SomaError, _ops_abi
 from ._abi import SOMA_DTYPE_BF16, SOMA_DTYPE_F16, SOMA_DTYPE_F32
 
 __all__ = ["layer_norm_forward", "layer_norm_backward", "linear_forward", "linear_backward", "distill_forward",
-           "distill_backward", "distill_loss_grad", "layer_norm", "linear", "distill_loss", "check", "ACTIVATIONS"]
+           "distill_backward", "distill_loss_grad", "embedding_forward", "embedding_backward", "layer_norm", "linear",
+           "distill_loss", "embedding", "check", "ACTIVATIONS"]
 
 ACTIVATIONS = {"none": _ops_abi.SOMA_ACT_NONE, "relu": _ops_abi.SOMA_ACT_RELU, "gelu": _ops_abi.SOMA_ACT_GELU,
                "gelu_tanh": _ops_abi.SOMA_ACT_GELU_TANH, "silu": _ops_abi.SOMA_ACT_SILU}
@@ -413,6 +414,72 @@ def distill_loss_grad(logits, teacher_logits, teacher_index, *, temperature: flo
     return loss, gradient
 
 
+# ---- embedding ----------------------------------------------------------------
+
+def _tokens(t, name, other):
+    """Token numbers of any shape as the C calls take them: (address, stride, batch, length, type)."""
+    code = _code(t, name, _INDEX)
+    if t.device != other.device:
+        raise ValueError(f"{name}: on {t.device}, expected {other.device}")
+    if t.dim() == 0:
+        t = t.unsqueeze(0)
+    m = _matrix(t, name)
+    return m.data_ptr(), m.stride(0), m.shape[0], m.shape[1], code
+
+
+@functools.lru_cache(maxsize=1024)
+def _embedding_bytes(dev, rows, vocab, cols):
+    need = ctypes.c_int64()
+    _check(_ops_abi.soma_embedding_backward_workspace(dev, rows, vocab, cols, ctypes.byref(need)))
+    return need.value
+
+
+@_on_stream
+def embedding_forward(index, weight, *, scale: float = 1.0):
+    """y = scale * weight[index], [..., cols] in the weight's dtype.
+
+    index [...]: int32 or int64; a token outside the vocabulary, such as -1,
+    gets zeros.  weight [vocab, cols]: fp32, bf16 or fp16."""
+    _ops_abi.load()
+    if weight.dim() != 2:
+        raise ValueError(f"weight: {weight.dim()} dimensions, expected 2")
+    w = _matrix(weight, "weight")
+    vocab, cols = w.shape
+    address, stride, batch, length, code = _tokens(index, "index", weight)
+    y = torch.empty((*index.shape, cols), dtype=weight.dtype, device=weight.device)
+    dev = weight.device.index
+    _check(_ops_abi.soma_embedding_forward(dev, w.data_ptr(), w.stride(0), address, stride, batch, length, y.data_ptr(),
+                                           cols, vocab, cols, _code(weight, "weight"), code, scale, _raw_stream(dev)))
+    return y
+
+
+@_on_stream
+def embedding_backward(dy, index, vocab: int, *, scale: float = 1.0, out=None):
+    """dweight [vocab, cols] of embedding_forward, in dy's dtype; summed in
+    fp32.  With `out` (such as the gradient of a last linear layer that shares
+    the table) the gradient is added to it, and it is returned."""
+    _ops_abi.load()
+    d = _matrix(dy, "dy")
+    cols = d.shape[1]
+    _like(dy, "dy", dy, (*index.shape, cols))
+    address, stride, batch, length, code = _tokens(index, "index", dy)
+    dt = _code(dy, "dy")
+    dweight = out
+    if out is None:
+        dweight = torch.empty((vocab, cols), dtype=dy.dtype, device=dy.device)
+    else:
+        _like(out, "out", dy, (vocab, cols), dy.dtype)
+    w = _matrix(dweight, "out")
+    dev = dy.device.index
+    need = _embedding_bytes(dev, batch * length, vocab, cols)
+    work = _workspace(need, dy.device)
+    _check(_ops_abi.soma_embedding_backward(dev, d.data_ptr(), d.stride(0), address, stride, batch, length, w.data_ptr(),
+                                            w.stride(0), int(out is not None), _ptr(work), need, vocab, cols, dt, code,
+                                            scale, _raw_stream(dev)))
+    _written(out)
+    return dweight
+
+
 # ---- autograd -----------------------------------------------------------------
 
 def _even(g):
@@ -487,6 +554,20 @@ class _Distill(torch.autograd.Function):
                                 temperature=ctx.temperature, row_weight=row_weight), None, None, None, None
 
 
+class _Embedding(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, index, weight, scale):
+        ctx.save_for_backward(index)
+        ctx.vocab, ctx.scale = weight.shape[0], scale
+        return embedding_forward(index, weight, scale=scale)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        index, = ctx.saved_tensors
+        return None, embedding_backward(_even(dy), index, ctx.vocab, scale=ctx.scale), None
+
+
 def layer_norm(x, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None, eps: float = 1e-5):
     """Differentiable layer norm over the last dimension (see layer_norm_forward)."""
     return _LayerNorm.apply(x, weight, bias, eps)
@@ -505,3 +586,8 @@ def distill_loss(logits, teacher_logits, teacher_index, *, temperature: float = 
     """Differentiable distillation loss per row (see distill_forward); the
     teacher and the row weights are constants."""
     return _Distill.apply(logits, teacher_logits, teacher_index, temperature, row_weight)
+
+
+def embedding(index, weight, *, scale: float = 1.0):
+    """Differentiable scale * weight[index] (see embedding_forward)."""
+    return _Embedding.apply(index, weight, scale)
