@@ -9,8 +9,9 @@
 // writes the tokens that lie wholly inside it; a token that passes over a
 // chunk's border leaves partial sums, which a last kernel joins in order.  So
 // no token is too frequent for one CTA, no atomic touches a gradient, and the
-// same call gives the same bits.  Rows of the table without a token are
-// zeroed by other CTAs of the same launch, from a bitmap that the sort leaves.
+// same call gives the same bits.  While one cluster sorts, the launch's other
+// CTAs zero the table, the rows with tokens too: that costs less than knowing
+// which they are before the sort is done.
 #include <math.h>
 
 #include <algorithm>
@@ -127,9 +128,9 @@ struct SortArgs {
     uint32_t* keys2;      // the many-launch sort's second buffers
     uint32_t* order2;
     uint32_t* counts;     // [digits][CTAs] of the many-launch sort
-    uint32_t* hit;        // bitmap of the tokens that occur, or nullptr
-    int32_t hit_words;
     int32_t share;        // items of a CTA
+    char* zero;           // the table of gradients to zero: zero_rows rows (0: none) of zero_cols bytes, zero_stride apart
+    int64_t zero_stride, zero_rows, zero_cols;
 };
 
 // Histograms of the warps' items; then `hist` holds for each warp and digit
@@ -194,6 +195,11 @@ __device__ __forceinline__ void scan_digits(uint32_t* x, int n, uint32_t* scratc
     __syncthreads();
 }
 
+__device__ __forceinline__ int cluster_size() {
+    uint32_t n;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+    return (int)n;
+}
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
     uint32_t v;
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
@@ -203,14 +209,44 @@ __device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// The whole sort in one launch: one cluster whose CTAs hold `share` items each
-// in shared memory and hand each other the items of a pass through it.
+// Zeroes `bytes` bytes (a multiple of 2) from p on, with the threads [at, at + 1, ...) of `step`.
+__device__ __forceinline__ void zero_bytes(char* p, int64_t bytes, int64_t at, int64_t step) {
+    const int64_t head = min(bytes, (int64_t)((16 - ((uintptr_t)p & 15)) & 15)), words = (bytes - head) / 16;
+    for (int64_t i = at; i < (bytes - words * 16) / 2; i += step)
+        *reinterpret_cast<uint16_t*>(p + (2 * i < head ? 2 * i : words * 16 + 2 * i)) = 0;
+    uint4* body = reinterpret_cast<uint4*>(p + head);
+#pragma unroll 4
+    for (int64_t i = at; i < words; i += step) __stcs(body + i, make_uint4(0, 0, 0, 0));
+}
+
+constexpr int64_t kPage = 32768;  // bytes
+constexpr int kZeroCtas = 4;  // per SM: 90 us for the table of 32000 x 4096 bf16 and 16384 tokens; 95 with 2, 92 with 8
+
+// CTA `at` of `ctas` zeroes its part of the table.
+__device__ __forceinline__ void zero_table(const SortArgs& a, int at, int ctas) {
+    if (a.zero_stride == a.zero_cols) {  // one long row, a page of it at a time
+        const int64_t bytes = a.zero_rows * a.zero_cols;
+        for (int64_t b = (int64_t)at * kPage; b < bytes; b += (int64_t)ctas * kPage)
+            zero_bytes(a.zero + b, min(kPage, bytes - b), threadIdx.x, kSortThreads);
+        return;
+    }
+    for (int64_t r = (int64_t)at * kSortWarps + (threadIdx.x >> 5); r < a.zero_rows; r += (int64_t)ctas * kSortWarps)
+        zero_bytes(a.zero + r * a.zero_stride, a.zero_cols, threadIdx.x & 31, 32);
+}
+
+// The whole sort in one launch: the first cluster's CTAs hold `share` items
+// each in shared memory and hand each other the items of a pass through it.
+// The other clusters zero the table.
 __global__ void __launch_bounds__(kSortThreads) cluster_sort_kernel(const __grid_constant__ SortArgs a) {
     extern __shared__ uint32_t sort_smem[];
     __shared__ uint32_t hist[kSortWarps][kMaxDigits];
     __shared__ uint32_t total[kMaxDigits], start[kMaxDigits], scratch[kSortWarps];
     launch_dependents();
-    const int rank = blockIdx.x, ctas = gridDim.x, share = a.share;
+    const int rank = cluster_rank(), ctas = cluster_size(), share = a.share;
+    if ((int)blockIdx.x >= ctas) {
+        zero_table(a, blockIdx.x - ctas, gridDim.x - ctas);
+        return;
+    }
     const int begin = rank * share, n = max(0, min(share, (int)a.rows - begin));
     uint32_t* keys[2] = {sort_smem, sort_smem + 2 * share};
     uint32_t* order[2] = {sort_smem + share, sort_smem + 3 * share};
@@ -219,34 +255,36 @@ __global__ void __launch_bounds__(kSortThreads) cluster_sort_kernel(const __grid
         keys[0][i] = v < 0 ? a.vocab : v;
         order[0][i] = begin + i;
     }
-    if (a.hit)
-        for (int i = rank * kSortThreads + threadIdx.x; i < a.hit_words; i += ctas * kSortThreads) a.hit[i] = 0;
     __syncthreads();
     const int digits = 1 << a.digit_bits;
     for (int p = 0; p < a.passes; ++p) {
         const int from = p & 1, shift = p * a.digit_bits;
         auto key = [&](int i) { return keys[from][i] >> shift & (digits - 1); };
         count_digits(hist, total, n, digits, key);
-        cluster_sync_all();  // every CTA's totals are there (and, once, the cleared bitmap)
-        for (int d = threadIdx.x; d < digits; d += kSortThreads) {
-            uint32_t all = 0, before = 0;
-            for (int c = 0; c < ctas; ++c) {
-                if (c == rank) before = all;
-                all += ld_cluster_u32(cluster_map(smem_addr(total + d), c));
+        cluster_sync_all();  // every CTA's totals are there
+        uint32_t all = 0, before = 0;
+        const int d = threadIdx.x;
+        if (d < digits) {
+            uint32_t x[kSortCtas];
+#pragma unroll
+            for (int c = 0; c < kSortCtas; ++c) x[c] = c < ctas ? ld_cluster_u32(cluster_map(smem_addr(total + d), c)) : 0;
+#pragma unroll
+            for (int c = 0; c < kSortCtas; ++c) {
+                if (c < rank) before += x[c];
+                all += x[c];
             }
             start[d] = all;
-            hist[0][d] += before;
-            for (int w = 1; w < kSortWarps; ++w) hist[w][d] += before;
         }
         __syncthreads();
         scan_digits(start, digits, scratch);
+        if (d < digits) start[d] += before;
+        __syncthreads();
         const bool last = p == a.passes - 1;
         scatter_digits(hist, start, n, key, [&](int i, uint32_t place) {
             const uint32_t k = keys[from][i], r = order[from][i];
             if (last) {
                 a.keys[place] = k;
                 a.order[place] = r;
-                if (a.hit && k < (uint32_t)a.vocab) atomicOr(a.hit + (k >> 5), 1u << (k & 31));
             } else {
                 const uint32_t c = place / share, at = place - c * share;
                 st_cluster_u32(cluster_map(smem_addr(keys[from ^ 1] + at), c), k);
@@ -255,6 +293,11 @@ __global__ void __launch_bounds__(kSortThreads) cluster_sort_kernel(const __grid
         });
         cluster_sync_all();  // the items have arrived; nobody reads this pass's totals any more
     }
+}
+
+// Zeroes the table, for the sort in many launches.
+__global__ void __launch_bounds__(kSortThreads) zero_kernel(const __grid_constant__ SortArgs a) {
+    zero_table(a, blockIdx.x, gridDim.x);
 }
 
 // The same in many launches, a pass in three: digits counted, places found,
@@ -271,7 +314,6 @@ __global__ void __launch_bounds__(kSortThreads) count_kernel(const __grid_consta
             const int v = token_at(a.tokens, begin + i, a.vocab);
             a.keys[begin + i] = v < 0 ? a.vocab : v;
             a.order[begin + i] = (uint32_t)(begin + i);
-            if (a.hit && v >= 0) atomicOr(a.hit + (v >> 5), 1u << (v & 31));
         }
         __syncthreads();
     }
@@ -329,14 +371,12 @@ __global__ void __launch_bounds__(kSortThreads) move_kernel(const __grid_constan
 // ---- sums of the sorted rows -------------------------------------------------------
 
 constexpr int kSumThreads = 128;
-constexpr int kChunk = 64;       // sorted positions of a CTA
-constexpr int kSumDeep = 8;      // rows in flight per thread
-constexpr int kZeroBytes = 64 * 1024;  // of a CTA that zeroes rows, about
+constexpr int kMostChunk = 64, kLeastChunk = 16;  // sorted positions of a CTA
+constexpr int kSumDeep = 8;                       // rows in flight per thread
 
 struct SumArgs {
     const uint32_t* keys;
     const uint32_t* order;
-    const uint32_t* hit;
     float* partials;      // [chunks][2][cols]: of a chunk's first token, if it began earlier, and its last, if it goes on
     const void* dy;
     int64_t dy_stride;
@@ -344,10 +384,8 @@ struct SumArgs {
     int64_t out_stride;
     int64_t rows;
     int32_t vocab, cols;
-    int32_t chunks, col_blocks;   // sum_kernel: chunks x col_blocks CTAs, the others zero rows
-    int32_t zero_words;           // words of the bitmap per zeroing CTA
+    int32_t chunk, chunks, col_blocks;  // chunks x col_blocks CTAs
     float scale;
-    bool accumulate;
 };
 
 // A thread's columns: a vector of kVec (kWhole: rows of dy and out start on
@@ -384,20 +422,20 @@ struct Columns {
             for (int e = 0; e < kVec; ++e) sum[e] += to_f32(r.x[kWhole ? 0 : e]);
         }
     }
-    // out (+)= scale * sum
-    __device__ __forceinline__ void store(T* row, float (&sum)[kVec], float scale, bool accumulate) const {
+    // out = scale * sum + before (a Raw of out, where kAdd)
+    template <bool kAdd>
+    __device__ __forceinline__ void store(T* row, const float (&sum)[kVec], float scale, const Raw& before) const {
         if (kWhole) {
             if (c0 >= cols) return;
             float x[kVec] = {};
-            if (accumulate) widen16(*reinterpret_cast<const uint4*>(row + c0), x, T{});
+            if (kAdd) widen16(before.w, x, T{});
 #pragma unroll
             for (int e = 0; e < kVec; ++e) x[e] = fmaf(sum[e], scale, x[e]);
             *reinterpret_cast<uint4*>(row + c0) = narrow16(x, T{});
         } else {
 #pragma unroll
             for (int e = 0; e < kVec; ++e)
-                if (col(e) < cols)
-                    row[col(e)] = from_f32<T>(fmaf(sum[e], scale, accumulate ? to_f32(row[col(e)]) : 0.f));
+                if (col(e) < cols) row[col(e)] = from_f32<T>(fmaf(sum[e], scale, kAdd ? to_f32(before.x[kWhole ? 0 : e]) : 0.f));
         }
     }
     __device__ __forceinline__ void store_partial(float* row, const float (&sum)[kVec]) const {
@@ -407,42 +445,16 @@ struct Columns {
     }
 };
 
-// Zeroes the rows without a token of the bitmap's words [w0, w1).
-template <typename T>
-__device__ __forceinline__ void zero_rows(const SumArgs& a, int w0, int w1) {
-    constexpr int kVec = 16 / sizeof(T);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int w = w0; w < w1; ++w) {
-        const uint32_t hit = __ldcg(a.hit + w);
-        for (int b = warp; b < 32; b += kSumThreads / 32) {
-            const int64_t v = (int64_t)w * 32 + b;
-            if (v >= a.vocab || (hit >> b & 1)) continue;
-            T* row = static_cast<T*>(a.out) + v * a.out_stride;
-            const int head = min(a.cols, (int)((16 - ((uintptr_t)row & 15)) & 15) / (int)sizeof(T));
-            const int words = (a.cols - head) / kVec;
-            if (lane < a.cols - words * kVec) row[lane < head ? lane : words * kVec + lane] = from_f32<T>(0.f);
-            uint4* body = reinterpret_cast<uint4*>(row + head);
-            for (int i = lane; i < words; i += 32) __stcs(body + i, make_uint4(0, 0, 0, 0));
-        }
-    }
-}
-
-template <typename T, bool kWhole>
+template <typename T, bool kWhole, bool kAdd>
 __global__ void __launch_bounds__(kSumThreads) sum_kernel(const __grid_constant__ SumArgs a) {
-    __shared__ uint32_t keys[kChunk + 2], order[kChunk];
+    __shared__ uint32_t keys[kMostChunk + 2], order[kMostChunk];
     launch_dependents();
     wait_for_previous();
-    const int sums = a.chunks * a.col_blocks;
-    if ((int)blockIdx.x >= sums) {
-        const int w0 = ((int)blockIdx.x - sums) * a.zero_words;
-        zero_rows<T>(a, w0, min(w0 + a.zero_words, (a.vocab + 31) / 32));
-        return;
-    }
     using C = Columns<T, kWhole>;
     const int chunk = (int)blockIdx.x / a.col_blocks;
     const C columns((int)blockIdx.x % a.col_blocks, a.cols);
-    const int64_t begin = (int64_t)chunk * kChunk;
-    const int n = (int)min((int64_t)kChunk, a.rows - begin);
+    const int64_t begin = (int64_t)chunk * a.chunk;
+    const int n = (int)min((int64_t)a.chunk, a.rows - begin);
     constexpr uint32_t kNone = 0xffffffffu;
     for (int i = threadIdx.x; i < n + 2; i += kSumThreads) {  // one neighbour on each side
         const int64_t at = begin + i - 1;
@@ -451,13 +463,19 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const __grid_constant_
     }
     __syncthreads();
     const T* dy = static_cast<const T*>(a.dy);
+    auto out = [&](uint32_t key) { return static_cast<T*>(a.out) + (int64_t)key * a.out_stride; };
     float sum[C::kVec] = {};
     bool began_here = keys[0] != keys[1];
     for (int i0 = 0; i0 < n && keys[1 + i0] < (uint32_t)a.vocab; i0 += kSumDeep) {
-        typename C::Raw raw[kSumDeep];
+        typename C::Raw raw[kSumDeep], before[kAdd ? kSumDeep : 1];
 #pragma unroll
-        for (int q = 0; q < kSumDeep; ++q)
-            if (i0 + q < n) columns.load(dy + (int64_t)order[i0 + q] * a.dy_stride, raw[q]);
+        for (int q = 0; q < kSumDeep; ++q) {
+            const int i = i0 + q;
+            if (i >= n) break;
+            columns.load(dy + (int64_t)order[i] * a.dy_stride, raw[q]);
+            // what a token's sum is added to, where it ends (read now: one at a time they cost a latency each)
+            if (kAdd && keys[1 + i] < (uint32_t)a.vocab && keys[1 + i] != keys[2 + i]) columns.load(out(keys[1 + i]), before[kAdd ? q : 0]);
+        }
 #pragma unroll
         for (int q = 0; q < kSumDeep; ++q) {
             const int i = i0 + q;
@@ -467,10 +485,8 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const __grid_constant_
             columns.add(raw[q], sum);
             const bool ends = key != keys[2 + i];
             if (!ends && i + 1 < n) continue;
-            if (ends && began_here)
-                columns.store(static_cast<T*>(a.out) + (int64_t)key * a.out_stride, sum, a.scale, a.accumulate);
-            else
-                columns.store_partial(a.partials + ((int64_t)chunk * 2 + (began_here ? 1 : 0)) * a.cols, sum);
+            if (ends && began_here) columns.template store<kAdd>(out(key), sum, a.scale, before[kAdd ? q : 0]);
+            else columns.store_partial(a.partials + ((int64_t)chunk * 2 + (began_here ? 1 : 0)) * a.cols, sum);
             began_here = true;
 #pragma unroll
             for (int e = 0; e < C::kVec; ++e) sum[e] = 0.f;
@@ -478,33 +494,41 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const __grid_constant_
     }
 }
 
-// A token that goes on after chunk c but began in it: its partial sums from
-// chunk c on, in order.
-template <typename T, bool kWhole>
+// A token that began in a chunk and goes on after it: its partial sums from
+// that chunk on, in order.
+template <typename T, bool kWhole, bool kAdd>
 __global__ void __launch_bounds__(kSumThreads) join_kernel(const __grid_constant__ SumArgs a) {
     launch_dependents();
     wait_for_previous();
     using C = Columns<T, kWhole>;
-    const int chunk = (int)blockIdx.x / a.col_blocks;
-    const int64_t begin = (int64_t)chunk * kChunk, last = begin + kChunk - 1;  // (there is a chunk after this one)
-    const uint32_t key = __ldcg(a.keys + last);
-    if (key >= (uint32_t)a.vocab || __ldcg(a.keys + last + 1) != key) return;
-    if (begin > 0 && __ldcg(a.keys + begin - 1) == key) return;  // began earlier
+    const int chunk = (int)blockIdx.x / a.col_blocks, lane = threadIdx.x & 31;
+    const int64_t begin = (int64_t)chunk * a.chunk, last = begin + a.chunk - 1;  // (there is a chunk after this one)
+    const uint32_t key = __ldcg(a.keys + last), next = __ldcg(a.keys + last + 1);
+    const uint32_t previous = begin > 0 ? __ldcg(a.keys + begin - 1) : ~key;
+    if (key >= (uint32_t)a.vocab || next != key || previous == key) return;
     const C columns((int)blockIdx.x % a.col_blocks, a.cols);
+    typename C::Raw before;
+    T* out = static_cast<T*>(a.out) + (int64_t)key * a.out_stride;
+    if (kAdd) columns.load(out, before);
     float sum[C::kVec];
     auto at = [&](int c, int which, int e) {
         return columns.col(e) < a.cols ? __ldcg(a.partials + ((int64_t)c * 2 + which) * a.cols + columns.col(e)) : 0.f;
     };
 #pragma unroll
     for (int e = 0; e < C::kVec; ++e) sum[e] = at(chunk, 1, e);
-    // chunks whose first key is the token and that hold nothing else, then the one where it ends
-    int end = chunk + 1;
-    while (end + 1 < a.chunks && __ldcg(a.keys + (int64_t)(end + 1) * kChunk) == key) ++end;
-    for (int c = chunk + 1; c <= end; ++c) {
+    // the chunks after this one whose first key is the token, 32 of them looked at together
+    for (int c0 = chunk + 1; c0 < a.chunks; c0 += 32) {
+        const bool mine = c0 + lane < a.chunks && __ldcg(a.keys + (int64_t)(c0 + lane) * a.chunk) == key;
+        const uint32_t same = __ballot_sync(0xffffffffu, mine);
+        const int count = same == 0xffffffffu ? 32 : __ffs(~same) - 1;
+#pragma unroll 4
+        for (int c = c0; c < c0 + count; ++c) {
 #pragma unroll
-        for (int e = 0; e < C::kVec; ++e) sum[e] += at(c, 0, e);
+            for (int e = 0; e < C::kVec; ++e) sum[e] += at(c, 0, e);
+        }
+        if (count < 32) break;
     }
-    columns.store(static_cast<T*>(a.out) + (int64_t)key * a.out_stride, sum, a.scale, a.accumulate);
+    columns.template store<kAdd>(out, sum, a.scale, before);
 }
 
 // ---- host side -------------------------------------------------------------------
@@ -521,18 +545,22 @@ void plan_digits(SortArgs& s) {
 
 bool one_cluster(int64_t rows) { return rows <= (int64_t)kSortCtas * kSortShare; }
 
-// The workspace: sorted tokens and rows, bitmap, partial sums, and what the
+// The workspace: sorted tokens and rows, partial sums, and what the
 // many-launch sort needs.
 struct Layout {
-    int64_t keys, order, hit, partials, keys2, order2, counts, bytes;
+    int64_t keys, order, partials, keys2, order2, counts, bytes;
+    int32_t chunk;
     int64_t chunks;
-    Layout(int64_t rows, int64_t vocab, int64_t cols) {
-        chunks = (rows + kChunk - 1) / kChunk;
+    Layout(int64_t rows, int64_t cols) {
+        // Long chunks leave fewer partial sums; the CTAs of 1024 columns should still be six per SM.
+        const int64_t blocks = (cols + 1023) / 1024;
+        chunk = kMostChunk;
+        while (chunk > kLeastChunk && (rows + chunk - 1) / chunk * blocks < 6 * 152) chunk /= 2;
+        chunks = (rows + chunk - 1) / chunk;
         int64_t at = 0;
         auto take = [&](int64_t n) { const int64_t here = at; at += align256(n); return here; };
         keys = take(rows * 4);
         order = take(rows * 4);
-        hit = take((vocab + 31) / 32 * 4);
         partials = take(chunks > 1 ? chunks * 2 * cols * 4 : 0);
         const bool many = !one_cluster(rows);
         keys2 = take(many ? rows * 4 : 0);
@@ -556,9 +584,12 @@ int launch_after(const void* kernel, int64_t grid, int threads, void** args, voi
     return (int)cudaLaunchKernelExC(&cfg, kernel, args);
 }
 
-int launch_sort(SortArgs& s, void* stream) {
+int launch_sort(SortArgs& s, int sm_count, void* stream) {
     cudaStream_t st = (cudaStream_t)stream;
     plan_digits(s);
+    const int64_t zero = s.zero_rows * s.zero_cols;
+    // CTAs that zero: a page each at least, at most kZeroCtas per SM
+    const int zeros = (int)std::min<int64_t>(kZeroCtas * sm_count, (zero + kPage - 1) / kPage);
     if (one_cluster(s.rows)) {
         int ctas = 1;
         while (ctas < kSortCtas && (int64_t)ctas * 1024 < s.rows) ctas *= 2;
@@ -566,7 +597,7 @@ int launch_sort(SortArgs& s, void* stream) {
         const int smem = s.share * 16;
         if (const int e = allow_smem((const void*)cluster_sort_kernel, smem)) return e;
         cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(ctas);
+        cfg.gridDim = dim3(ctas + (zeros + ctas - 1) / ctas * ctas);
         cfg.blockDim = dim3(kSortThreads);
         cfg.dynamicSmemBytes = smem;
         cfg.stream = st;
@@ -579,8 +610,7 @@ int launch_sort(SortArgs& s, void* stream) {
         void* args[] = {&s};
         return (int)cudaLaunchKernelExC(&cfg, (const void*)cluster_sort_kernel, args);
     }
-    if (s.hit)
-        if (const int e = cudaMemsetAsync(s.hit, 0, (size_t)s.hit_words * 4, st)) return e;
+    if (zeros) zero_kernel<<<zeros, kSortThreads, 0, st>>>(s);
     const int tiles = (int)((s.rows + kSortTile - 1) / kSortTile);
     if (s.passes & 1) {  // the last pass ends in the first buffers
         std::swap(s.keys, s.keys2);
@@ -608,11 +638,11 @@ int launch_embedding_fwd(const EmbeddingArgs& a, void* stream) {
     });
 }
 
-int64_t embedding_bwd_workspace(int64_t rows, int64_t vocab, int64_t cols) { return Layout(rows, vocab, cols).bytes; }
+int64_t embedding_bwd_workspace(int64_t rows, int64_t cols) { return Layout(rows, cols).bytes; }
 
 int launch_embedding_bwd(const EmbeddingArgs& a, const void* dy, int64_t dy_stride, bool accumulate, void* workspace,
-                         void* stream) {
-    const Layout at(a.rows, a.vocab, a.cols);
+                         int sm_count, void* stream) {
+    const Layout at(a.rows, a.cols);
     char* ws = static_cast<char*>(workspace);
     SortArgs s{};
     s.tokens = a.tokens;
@@ -623,16 +653,18 @@ int launch_embedding_bwd(const EmbeddingArgs& a, const void* dy, int64_t dy_stri
     s.keys2 = reinterpret_cast<uint32_t*>(ws + at.keys2);
     s.order2 = reinterpret_cast<uint32_t*>(ws + at.order2);
     s.counts = reinterpret_cast<uint32_t*>(ws + at.counts);
-    s.hit = accumulate ? nullptr : reinterpret_cast<uint32_t*>(ws + at.hit);
-    s.hit_words = (a.vocab + 31) / 32;
+    const int esize = a.dtype == kF32 ? 4 : 2;
+    s.zero = static_cast<char*>(a.out);
+    s.zero_rows = accumulate ? 0 : a.vocab;
+    s.zero_cols = (int64_t)a.cols * esize;
+    s.zero_stride = a.vocab == 1 ? s.zero_cols : a.out_stride * esize;
     SumArgs u{};
     u.keys = s.keys;
     u.order = s.order;
-    if (const int e = launch_sort(s, stream)) return e;
+    if (const int e = launch_sort(s, sm_count, stream)) return e;
     return with_type(a.dtype, [&](auto t) {
         using T = decltype(t);
         constexpr int kVec = 16 / sizeof(T);
-        u.hit = s.hit;
         u.partials = reinterpret_cast<float*>(ws + at.partials);
         u.dy = dy;
         u.dy_stride = dy_stride;
@@ -641,23 +673,24 @@ int launch_embedding_bwd(const EmbeddingArgs& a, const void* dy, int64_t dy_stri
         u.rows = a.rows;
         u.vocab = a.vocab;
         u.cols = a.cols;
+        u.chunk = at.chunk;
         u.chunks = (int32_t)at.chunks;
         u.col_blocks = (a.cols + kSumThreads * kVec - 1) / (kSumThreads * kVec);
         u.scale = a.scale;
-        u.accumulate = accumulate;
-        const int64_t row_bytes = (int64_t)a.cols * sizeof(T);
-        u.zero_words = (int32_t)std::max<int64_t>(1, kZeroBytes / (32 * row_bytes));
-        const int64_t sums = (int64_t)u.chunks * u.col_blocks;
-        if (sums > 0x3fffffff) return (int)cudaErrorInvalidConfiguration;
-        const int64_t zeros = accumulate ? 0 : (s.hit_words + u.zero_words - 1) / u.zero_words;
         const bool whole = a.cols % kVec == 0 && (uintptr_t)dy % 16 == 0 && (uintptr_t)a.out % 16 == 0 &&
                            (a.rows == 1 || dy_stride % kVec == 0) && (a.vocab == 1 || a.out_stride % kVec == 0);
+        const void *sum, *join;
+        if (accumulate) {
+            sum = whole ? (const void*)sum_kernel<T, true, true> : (const void*)sum_kernel<T, false, true>;
+            join = whole ? (const void*)join_kernel<T, true, true> : (const void*)join_kernel<T, false, true>;
+        } else {
+            sum = whole ? (const void*)sum_kernel<T, true, false> : (const void*)sum_kernel<T, false, false>;
+            join = whole ? (const void*)join_kernel<T, true, false> : (const void*)join_kernel<T, false, false>;
+        }
         void* args[] = {&u};
-        int e = launch_after(whole ? (const void*)sum_kernel<T, true> : (const void*)sum_kernel<T, false>, sums + zeros,
-                             kSumThreads, args, stream);
+        const int e = launch_after(sum, (int64_t)u.chunks * u.col_blocks, kSumThreads, args, stream);
         if (e != cudaSuccess || u.chunks < 2) return e;
-        return launch_after(whole ? (const void*)join_kernel<T, true> : (const void*)join_kernel<T, false>,
-                            (int64_t)(u.chunks - 1) * u.col_blocks, kSumThreads, args, stream);
+        return launch_after(join, (int64_t)(u.chunks - 1) * u.col_blocks, kSumThreads, args, stream);
     });
 }
 

@@ -61,7 +61,7 @@ soma_status_t soma_embedding_backward_workspace(int32_t device, int64_t rows, in
     if (rows < 0 || rows > kMaxInt) return fail(SOMA_ERR_INVALID_ARG, "rows must be in [0, 2^31)");
     if (vocab < 1 || vocab > kMaxExtent) return fail(SOMA_ERR_INVALID_ARG, "vocab must be in [1, 2^30]");
     if (cols < 1 || cols > kMaxExtent) return fail(SOMA_ERR_INVALID_ARG, "cols must be in [1, 2^30]");
-    *bytes = rows == 0 ? 0 : embedding_bwd_workspace(rows, vocab, cols);
+    *bytes = rows == 0 ? 0 : embedding_bwd_workspace(rows, cols);
     return SOMA_OK;
 }
 
@@ -78,9 +78,8 @@ soma_status_t soma_embedding_backward(int32_t device, const void* dy, int64_t dy
     SOMA_TRY(check_matrix("dy", dy, dy_stride, rows, cols, e));
     SOMA_TRY(check_matrix("dweight", dweight, dweight_stride, vocab, cols, e));
     if (rows == 0 && accumulate) return SOMA_OK;
-    if (rows > 0) SOMA_TRY(check_workspace(workspace, workspace_bytes, embedding_bwd_workspace(rows, vocab, cols)));
+    if (rows > 0) SOMA_TRY(check_workspace(workspace, workspace_bytes, embedding_bwd_workspace(rows, cols)));
     SOMA_ON_DEVICE(device);
-    (void)sms;
     if (rows == 0) {
         const size_t pitch = (size_t)(vocab > 1 ? dweight_stride : cols) * e;
         return cuda_status(cudaMemset2DAsync(dweight, pitch, 0, (size_t)cols * e, (size_t)vocab, (cudaStream_t)stream),
@@ -88,7 +87,7 @@ soma_status_t soma_embedding_backward(int32_t device, const void* dy, int64_t dy
     }
     return cuda_status(launch_embedding_bwd({t, nullptr, 0, dweight, dweight_stride, rows, (int32_t)vocab,
                                              (int32_t)cols, dtype, (float)scale},
-                                            dy, dy_stride, accumulate != 0, workspace, stream),
+                                            dy, dy_stride, accumulate != 0, workspace, sms, stream),
                        "embedding backward");
 }
 

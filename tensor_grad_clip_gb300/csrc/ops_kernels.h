@@ -144,10 +144,10 @@ struct EmbeddingArgs {
 };
 
 int launch_embedding_fwd(const EmbeddingArgs& a, void* stream);
-int64_t embedding_bwd_workspace(int64_t rows, int64_t vocab, int64_t cols);
+int64_t embedding_bwd_workspace(int64_t rows, int64_t cols);
 // rows >= 1
 int launch_embedding_bwd(const EmbeddingArgs& a, const void* dy, int64_t dy_stride, bool accumulate, void* workspace,
-                         void* stream);
+                         int sm_count, void* stream);
 
 // How often a bounded wait inside a kernel of the current device has run out:
 // a count that only grows (modulo 2^32).  The copy waits for the legacy default
