@@ -203,6 +203,47 @@ soma_status_t soma_opt_step(soma_opt_t opt, const soma_tensor_t *list, int64_t n
 soma_status_t soma_opt_step_graph(soma_opt_t opt, const soma_tensor_t *list, int64_t n,
                                   double grad_divisor, double max_norm, void *stream);
 
+/* ---- moments in 8 bits --------------------------------------------------------
+ * The calls of this header that take a list, for lists some or all of whose
+ * entries hold their moments in 8 bits: 16 bytes of traffic an element with
+ * 16-bit gradients instead of 28, and 2 bytes of state instead of 8.  scales
+ * has one pair for each entry of the list.  Both NULL: the entry's moments are
+ * fp32, as ever.  Both set: exp_avg and exp_avg_sq point to numel bytes (any
+ * alignment; 8-byte aligned ones run fastest, beside a param, grad and
+ * param_lowp on 16-byte boundaries), and the scales to ceil(numel /
+ * SOMA_STATE_BLOCK) floats each: block b, the elements [b, b + 1) *
+ * SOMA_STATE_BLOCK of the tensor, has
+ *   m = scale_m[b] * e4m3(exp_avg[i]),   sqrt(v) = scale_v[b] * e4m3(exp_avg_sq[i])
+ * (e4m3: 8-bit floating point with 4 bits of exponent and 3 of fraction, the
+ * largest value 448).  All zeros is the state before step 1.  The step
+ * computes m, v and p in fp32 as for fp32 moments, then for each block
+ *   scale = largest |x| / 448 (0 where that is below 2^-100),  x = m or sqrt(v),
+ *   code  = |x| * 448 / largest |x|, rounded up or down to a neighbouring e4m3
+ *           value by chance, so that its mean is the number itself; a second
+ *           moment that is not 0 gets at least e4m3's smallest value, so that
+ *           m / sqrt(v) stays bounded.
+ * Chance is a hash of the element's index in its tensor and of its group's
+ * step count: the same call with the same state gives the same bits, and a
+ * resumed run continues as the first would have.  A moment that is not finite
+ * makes its block's moments NaN or infinite.
+ * These lists never run as the single-launch step: a step is the square-sum
+ * kernel and one update kernel for each kind of entry in the list.
+ * soma_opt_get_segments' update table has the entries with fp32 moments. */
+#define SOMA_STATE_BLOCK 256
+typedef struct {
+    float *exp_avg;     /* scales of exp_avg's blocks, or NULL */
+    float *exp_avg_sq;
+} soma_scales_t;
+soma_status_t soma_opt_step8(soma_opt_t opt, const soma_tensor_t *list, const soma_scales_t *scales, int64_t n,
+                             double grad_divisor, double max_norm, void *stream);
+soma_status_t soma_opt_step_graph8(soma_opt_t opt, const soma_tensor_t *list, const soma_scales_t *scales, int64_t n,
+                                   double grad_divisor, double max_norm, void *stream);
+soma_status_t soma_opt_sumsq8(soma_opt_t opt, const soma_tensor_t *list, const soma_scales_t *scales, int64_t n,
+                              double grad_divisor, double *sumsq_out, void *stream);
+soma_status_t soma_opt_step_from_sumsq8(soma_opt_t opt, const soma_tensor_t *list, const soma_scales_t *scales,
+                                        int64_t n, double grad_divisor, double max_norm, const double *rank_sumsq,
+                                        int32_t nranks, void *stream);
+
 /* Device table entry of one group (64 bytes); soma_opt_device_groups returns
  * SOMA_MAX_GROUPS of them, indexed by group id. */
 typedef struct {

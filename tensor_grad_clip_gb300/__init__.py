@@ -19,9 +19,10 @@ from typing import Optional, Sequence
 
 from . import _abi
 from ._abi import (SOMA_DTYPE_BF16, SOMA_DTYPE_F16, SOMA_DTYPE_F32, SOMA_MAX_GROUPS,  # noqa: F401
-                   soma_plan_t, soma_tensor_t)
+                   SOMA_STATE_BLOCK, soma_plan_t, soma_scales_t, soma_tensor_t)
 
-__all__ = ["SomaOpt", "TensorList", "SomaError", "load", "soma_tensor_t", "soma_plan_t"]
+__all__ = ["SomaOpt", "TensorList", "SomaError", "load", "soma_tensor_t", "soma_plan_t", "zeros_8bit", "to_8bit",
+           "from_8bit"]
 
 
 def load():
@@ -69,6 +70,34 @@ def _check_f64_out(t, n):
         raise ValueError("expected a contiguous float64 CUDA tensor")
 
 
+# ---- moments in 8 bits ------------------------------------------------------
+
+def zeros_8bit(like):
+    """(codes, scales) of a moment that is 0 everywhere: e4m3 values of the
+    tensor's shape, and an fp32 scale for each SOMA_STATE_BLOCK elements."""
+    import torch
+    codes = torch.zeros(like.shape, dtype=torch.uint8, device=like.device).view(torch.float8_e4m3fn)
+    return codes, torch.zeros(-(-like.numel() // SOMA_STATE_BLOCK), dtype=torch.float32, device=like.device)
+
+
+def to_8bit(moment):
+    """(codes, scales) of an fp32 moment, rounded to nearest: exp_avg, or the
+    square root of exp_avg_sq (which is what the step holds in 8 bits)."""
+    import torch
+    flat = moment.detach().float().reshape(-1)
+    blocks = torch.nn.functional.pad(flat, (0, -flat.numel() % SOMA_STATE_BLOCK)).view(-1, SOMA_STATE_BLOCK)
+    scales = blocks.abs().amax(1) * (1.0 / 448.0)
+    values = blocks / torch.where(scales > 0, scales, 1.0)[:, None]
+    codes = values.clamp(-448.0, 448.0).to(torch.float8_e4m3fn)
+    return codes.view(-1)[:flat.numel()].reshape(moment.shape), scales
+
+
+def from_8bit(codes, scales):
+    """The fp32 values that codes and scales stand for (of exp_avg_sq: their square root)."""
+    flat = codes.detach().float().reshape(-1)
+    return (flat * scales.repeat_interleave(SOMA_STATE_BLOCK)[:flat.numel()]).reshape(codes.shape)
+
+
 class TensorList:
     """The soma_tensor_t array for lists of torch tensors, built once and
     reused every step (the tensors must stay alive and keep their storage).
@@ -78,11 +107,17 @@ class TensorList:
     groups: group id per tensor.  trainable / owned: bools per tensor
     (default all True).  Frozen entries may pass None buffers.
     params_lowp: optional bfloat16/float16 model weights per tensor (or None
-    entries), rewritten each step from the updated fp32 master `params`."""
+    entries), rewritten each step from the updated fp32 master `params`.
+    exp_avg_scales / exp_avg_sq_scales: optional; where they have a tensor and
+    not None, that entry's moments are held in 8 bits: exp_avgs and exp_avg_sqs
+    are float8_e4m3fn, the scales float32 with one value for each
+    SOMA_STATE_BLOCK elements (zeros_8bit makes both; exp_avg_sqs holds the
+    square root, see soma_opt_step8 in soma_opt.h)."""
 
     def __init__(self, params: Sequence, grads: Sequence, exp_avgs: Sequence, exp_avg_sqs: Sequence,
                  groups: Sequence[int], trainable: Optional[Sequence[bool]] = None,
-                 owned: Optional[Sequence[bool]] = None, params_lowp: Optional[Sequence] = None):
+                 owned: Optional[Sequence[bool]] = None, params_lowp: Optional[Sequence] = None,
+                 exp_avg_scales: Optional[Sequence] = None, exp_avg_sq_scales: Optional[Sequence] = None):
         import torch
         n = len(params)
         if not (len(grads) == len(exp_avgs) == len(exp_avg_sqs) == len(groups) == n):
@@ -92,7 +127,16 @@ class TensorList:
         params_lowp = [None] * n if params_lowp is None else list(params_lowp)
         if len(params_lowp) != n:
             raise ValueError("params_lowp must have one entry per tensor")
+        if (exp_avg_scales is None) != (exp_avg_sq_scales is None):
+            raise ValueError("exp_avg_scales and exp_avg_sq_scales go together")
+        eight = exp_avg_scales is not None
+        m_scales = list(exp_avg_scales) if eight else [None] * n
+        v_scales = list(exp_avg_sq_scales) if eight else [None] * n
+        if len(m_scales) != n or len(v_scales) != n:
+            raise ValueError("exp_avg_scales and exp_avg_sq_scales must have one entry per tensor")
         self.lowp = params_lowp  # keep alive
+        self.scale_tensors = (m_scales, v_scales)
+        self.scales = (soma_scales_t * max(n, 1))() if eight else None
         self.n = n
         self.array = (soma_tensor_t * max(n, 1))()
         self.tensors = list(zip(params, grads, exp_avgs, exp_avg_sqs))  # keep alive
@@ -114,10 +158,20 @@ class TensorList:
                 for other in (g, m, v):
                     if other is None or other.numel() != numel:
                         raise ValueError(f"tensor {k}: param, grad, exp_avg, exp_avg_sq must have equal numel")
+            ms, vs = m_scales[k], v_scales[k]
+            if (ms is None) != (vs is None):
+                raise ValueError(f"tensor {k}: exp_avg_scales and exp_avg_sq_scales go together")
+            state = torch.float32 if ms is None else torch.float8_e4m3fn
             e.param = ptr(p, torch.float32)
             e.grad = ptr(g)
-            e.exp_avg = ptr(m, torch.float32)
-            e.exp_avg_sq = ptr(v, torch.float32)
+            e.exp_avg = ptr(m, state)
+            e.exp_avg_sq = ptr(v, state)
+            if ms is not None and tr:
+                blocks = -(-numel // SOMA_STATE_BLOCK)
+                if ms.numel() != blocks or vs.numel() != blocks:
+                    raise ValueError(f"tensor {k}: {blocks} scales expected, one per {SOMA_STATE_BLOCK} elements")
+                self.scales[k].exp_avg = ptr(ms, torch.float32)
+                self.scales[k].exp_avg_sq = ptr(vs, torch.float32)
             lp = params_lowp[k]
             if lp is not None and tr and lp.numel() != numel:
                 raise ValueError(f"tensor {k}: params_lowp must have the param's numel")
@@ -131,6 +185,13 @@ class TensorList:
 
     def pointer(self):
         return ctypes.cast(self.array, ctypes.POINTER(soma_tensor_t))
+
+    def _call(self, name: str):
+        """The C function that takes this list, and its list arguments."""
+        if self.scales is None:
+            return getattr(_abi, name), (self.pointer(), self.n)
+        return getattr(_abi, name + "8"), (self.pointer(), ctypes.cast(self.scales, ctypes.POINTER(soma_scales_t)),
+                                           self.n)
 
 
 class SomaOpt:
@@ -223,30 +284,30 @@ class SomaOpt:
         self._check(_abi.soma_opt_set_group_step(self._h, group, t))
 
     def step(self, tensors: TensorList, grad_divisor: float, max_norm: float, stream=None):
-        self._check(_abi.soma_opt_step(self._h, tensors.pointer(), tensors.n, grad_divisor, max_norm,
-                                       _stream_handle(stream)))
+        step, entries = tensors._call("soma_opt_step")
+        self._check(step(self._h, *entries, grad_divisor, max_norm, _stream_handle(stream)))
 
     def sumsq(self, tensors: TensorList, grad_divisor: float, out, stream=None):
         """This rank's sum of (g/d)^2 over owned entries into `out` (a float64
         CUDA tensor with at least one element; written at out[0])."""
         _check_f64_out(out, 1)
-        self._check(_abi.soma_opt_sumsq(self._h, tensors.pointer(), tensors.n, grad_divisor, out.data_ptr(),
-                                        _stream_handle(stream)))
+        sumsq, entries = tensors._call("soma_opt_sumsq")
+        self._check(sumsq(self._h, *entries, grad_divisor, out.data_ptr(), _stream_handle(stream)))
 
     def step_from_sumsq(self, tensors: TensorList, grad_divisor: float, max_norm: float, rank_sumsq,
                         stream=None):
         """The update with the global norm from all ranks' sums (a float64
         CUDA tensor, rank r at index r)."""
         _check_f64_out(rank_sumsq, 1)
-        self._check(_abi.soma_opt_step_from_sumsq(self._h, tensors.pointer(), tensors.n, grad_divisor, max_norm,
-                                                  rank_sumsq.data_ptr(), rank_sumsq.numel(),
-                                                  _stream_handle(stream)))
+        step, entries = tensors._call("soma_opt_step_from_sumsq")
+        self._check(step(self._h, *entries, grad_divisor, max_norm, rank_sumsq.data_ptr(), rank_sumsq.numel(),
+                         _stream_handle(stream)))
 
     def step_graph(self, tensors: TensorList, grad_divisor: float, max_norm: float, stream=None):
         """The graph-capturable step (soma_opt_step_graph): may be called
         inside torch.cuda.graph capture once it has run outside capture."""
-        self._check(_abi.soma_opt_step_graph(self._h, tensors.pointer(), tensors.n, grad_divisor, max_norm,
-                                             _stream_handle(stream)))
+        step, entries = tensors._call("soma_opt_step_graph")
+        self._check(step(self._h, *entries, grad_divisor, max_norm, _stream_handle(stream)))
 
     def push_groups(self, stream=None):
         self._check(_abi.soma_opt_push_groups(self._h, _stream_handle(stream)))

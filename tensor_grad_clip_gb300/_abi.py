@@ -27,6 +27,7 @@ SOMA_MAX_GROUPS = 64
 SOMA_ABI_VERSION = 5
 SOMA_MAX_RANKS = 65536
 SOMA_PLAN_CACHE = 4
+SOMA_STATE_BLOCK = 256
 
 soma_status_t = ctypes.c_int32
 soma_opt_t = ctypes.c_void_p
@@ -49,6 +50,13 @@ class soma_tensor_t(ctypes.Structure):
 
 
 assert ctypes.sizeof(soma_tensor_t) == 56
+
+
+class soma_scales_t(ctypes.Structure):
+    _fields_ = [("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p)]
+
+
+assert ctypes.sizeof(soma_scales_t) == 16
 
 
 class soma_plan_t(ctypes.Structure):
@@ -122,6 +130,15 @@ SIGNATURES = {
                                                  ctypes.c_void_p, _I32, ctypes.c_void_p]),
     "soma_opt_step_graph": (soma_status_t, [soma_opt_t, ctypes.POINTER(soma_tensor_t), _I64, _D, _D,
                                             ctypes.c_void_p]),
+    "soma_opt_step8": (soma_status_t, [soma_opt_t, ctypes.POINTER(soma_tensor_t), ctypes.POINTER(soma_scales_t), _I64,
+                                       _D, _D, ctypes.c_void_p]),
+    "soma_opt_step_graph8": (soma_status_t, [soma_opt_t, ctypes.POINTER(soma_tensor_t), ctypes.POINTER(soma_scales_t),
+                                             _I64, _D, _D, ctypes.c_void_p]),
+    "soma_opt_sumsq8": (soma_status_t, [soma_opt_t, ctypes.POINTER(soma_tensor_t), ctypes.POINTER(soma_scales_t), _I64,
+                                        _D, ctypes.c_void_p, ctypes.c_void_p]),
+    "soma_opt_step_from_sumsq8": (soma_status_t, [soma_opt_t, ctypes.POINTER(soma_tensor_t),
+                                                  ctypes.POINTER(soma_scales_t), _I64, _D, _D, ctypes.c_void_p, _I32,
+                                                  ctypes.c_void_p]),
     "soma_opt_push_groups": (soma_status_t, [soma_opt_t, ctypes.c_void_p]),
     "soma_opt_pull_groups": (soma_status_t, [soma_opt_t, ctypes.c_void_p]),
     "soma_opt_device_groups": (soma_status_t, [soma_opt_t, ctypes.POINTER(ctypes.c_void_p)]),

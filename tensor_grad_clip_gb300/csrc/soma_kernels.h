@@ -186,6 +186,44 @@ struct UpdateArgs {
     const float* gscale;          // group divisors: c / d of each group, written by the norm side
 };
 
+// Tensors whose moments are held in 8 bits: blocks of kStateBlock elements,
+// counted from the tensor's start, share a scale, so segments are cut at
+// block borders only.
+constexpr int kStateBlock = 256;
+
+struct Seg8 {               // 80 bytes
+    float* p;               // already offset to the segment's first element
+    const void* g;
+    uint8_t* m;             // e4m3 codes
+    uint8_t* v;             // (of sqrt(v))
+    void* plow;
+    float* ms;              // scale of the segment's first block
+    float* vs;
+    int64_t first;          // index in its tensor of the segment's first element
+    int32_t len;
+    uint16_t group;
+    uint8_t gdtype, lowdt;
+    int32_t aligned;        // p, g and plow start on 16-byte boundaries, m and v on 8-byte ones
+    int32_t pad;
+};
+static_assert(sizeof(Seg8) == 80, "Seg8 layout");
+
+struct Table8 {
+    const Seg8* segs;
+    const int32_t* chunk_begin;
+    int32_t nchunks;
+};
+
+struct Update8Args {
+    Table8 t;
+    const Result* res;
+    GroupHp groups[kMaxGroups];   // regular step
+    uint32_t step[kMaxGroups];    // and the step counts it reaches
+    const GroupHp* dhp;           // graph-capturable step: both in device memory
+    const DevGroup* dgroups;
+    const float* gscale;
+};
+
 // Host-side cutting rule shared by every table builder.  A segment that
 // starts at element `off` of an n-element tensor with vector head h (-1 =
 // no vector body) and may take up to `room` elements ends at the returned
@@ -215,6 +253,7 @@ inline void segment_body(int64_t off, int64_t len, int h, Seg& s) {
 
 constexpr int kNormBlock = 512;
 constexpr int kUpdateBlock = 256;
+constexpr int kUpdate8Block = 256;
 
 // Launch wrappers (kernels.cu).  Return the cudaError_t of the launch as int.
 // graph = true selects the variants that take group constants from device
@@ -229,6 +268,8 @@ int launch_norm(const NormArgs& a, int grid, void* stream, bool graph = false, b
                 bool overlap = false);
 int launch_update(const UpdateArgs& a, int grid, void* stream, bool graph = false, bool overlap = false,
                   bool group_div = false);
+int launch_update8(const Update8Args& a, void* stream, bool graph = false, bool overlap = false,
+                   bool group_div = false);
 int launch_finish(const FinishArgs& a, void* stream);
 
 // Single-launch step (small lists): one cluster of `ctas` CTAs does the

@@ -50,6 +50,13 @@ constexpr int64_t kNormCtasPerSm = 3;  // the square-sum kernel's resident CTAs 
 constexpr int64_t kMinAutoChunk = 1024;   // smallest chunk the automatic sizing picks
 constexpr int64_t kUpdateCtasPerSm = 2;   // the update kernel's resident CTAs per SM (its launch bounds)
 constexpr int64_t kAutoChunksPerSm = 4;   // small lists: aim for this many chunks per SM
+// Elements of an 8-bit update's CTA: one block of 256 for each of its warps in
+// lists that one wave of its resident CTAs holds so, sixteen where that leaves
+// eight waves, else four.  302 M elements 974 us with 32 Ki, 977 with 16 Ki,
+// 1000 with 64 Ki; 31 M in 600 tensors 146 us with 8 Ki, 156 with 4 Ki, 149
+// with 16 Ki.
+constexpr int64_t kSmallUpdate8Chunk = 2048, kUpdate8Chunk = 8192, kLargeUpdate8Chunk = 32768;
+constexpr int64_t kUpdate8CtasPerSm = 4;
 constexpr int64_t kSinglePerCta = 4096;   // default single-launch limit: one 8-element vector per thread of each cluster CTA
 constexpr size_t kTimingRing = 1024;
 constexpr int kMaxPlans = SOMA_PLAN_CACHE;
@@ -80,9 +87,11 @@ struct PreparedList {
     bool valid = false;
     uint64_t used = 0;              // stamp of the last step that ran it
     std::vector<soma_tensor_t> key;
+    std::vector<soma_scales_t> scales;  // as passed with it, or empty
     char* d_tables = nullptr;
     size_t cap = 0;                 // bytes
     soma::Table norm_tab{}, upd_tab{};
+    soma::Table8 upd8_tab{};
     std::vector<uint8_t> group_present;
     int norm_grid = 1, upd_grid = 0;
     bool single = false;            // small enough for the single-launch step
@@ -132,10 +141,14 @@ struct soma_opt {
     uint64_t stamp = 0;
     int64_t plan_builds = 0, plan_reuses = 0;
     soma::Table norm_tab{}, upd_tab{};
+    soma::Table8 upd8_tab{};
     std::vector<uint8_t> group_present;
     int norm_grid = 1, upd_grid = 0;
     bool single = false;
     soma_plan_t plan{};
+
+    // the running call's scales, entry by entry of its list, or nullptr
+    const soma_scales_t* scales = nullptr;
 
     // kernel timing
     bool timing = false;
@@ -208,8 +221,13 @@ soma_status_t validate_entry(soma_opt* o, const soma_tensor_t& t, int64_t k) {
     if (t.numel == 0) return SOMA_OK;
     if (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq)
         return o->fail(SOMA_ERR_INVALID_ARG, "list[%lld]: null buffer in a trainable entry", (long long)k);
-    if ((uintptr_t)t.param % 4 || (uintptr_t)t.exp_avg % 4 || (uintptr_t)t.exp_avg_sq % 4 ||
-        (uintptr_t)t.grad % grad_size(t.grad_dtype) || (uintptr_t)t.param_lowp % 2)
+    const soma_scales_t q = o->scales ? o->scales[k] : soma_scales_t{};
+    if (!q.exp_avg != !q.exp_avg_sq)
+        return o->fail(SOMA_ERR_INVALID_ARG, "scales[%lld]: one of the two is NULL", (long long)k);
+    const uintptr_t state = q.exp_avg ? 1 : 4;  // bytes of a moment
+    if ((uintptr_t)t.param % 4 || (uintptr_t)t.exp_avg % state || (uintptr_t)t.exp_avg_sq % state ||
+        (uintptr_t)t.grad % grad_size(t.grad_dtype) || (uintptr_t)t.param_lowp % 2 || (uintptr_t)q.exp_avg % 4 ||
+        (uintptr_t)q.exp_avg_sq % 4)
         return o->fail(SOMA_ERR_ALIGNMENT, "list[%lld]: a buffer is not aligned to its element size",
                        (long long)k);
     return SOMA_OK;
@@ -290,6 +308,53 @@ struct TableBuilder {
             consumed += len;
             ++cur_segs;
             off = cut;
+        }
+    }
+    int32_t nchunks() const { return (int32_t)begin.size() - 1; }
+};
+
+// The same for entries with moments in 8 bits, cut at the borders of the
+// blocks that share a scale.
+struct TableBuilder8 {
+    int64_t chunk = kUpdate8Chunk;
+    std::vector<soma::Seg8> segs;
+    std::vector<int32_t> begin{0};
+    int64_t cur_elems = 0;  // in whole blocks: a warp takes a block, however short
+    int cur_segs = 0;
+
+    void close() {
+        if (cur_segs == 0) return;
+        begin.push_back((int32_t)segs.size());
+        cur_elems = 0;
+        cur_segs = 0;
+    }
+    void add(const soma_tensor_t& t, const soma_scales_t& q) {
+        const int64_t block = soma::kStateBlock;
+        const int gsz = grad_size(t.grad_dtype);
+        const bool aligned = (uintptr_t)t.param % 16 == 0 && (uintptr_t)t.grad % 16 == 0 &&
+                             (uintptr_t)t.param_lowp % 16 == 0 && (uintptr_t)t.exp_avg % 8 == 0 &&
+                             (uintptr_t)t.exp_avg_sq % 8 == 0;
+        for (int64_t off = 0; off < t.numel;) {
+            if (cur_segs == soma::kMaxSegsPerChunk || cur_elems >= chunk) close();
+            const int64_t len = std::min(t.numel - off, chunk - cur_elems);
+            soma::Seg8 s{};
+            s.p = t.param + off;
+            s.g = static_cast<const char*>(t.grad) + off * gsz;
+            s.m = reinterpret_cast<uint8_t*>(t.exp_avg) + off;
+            s.v = reinterpret_cast<uint8_t*>(t.exp_avg_sq) + off;
+            s.plow = t.param_lowp ? static_cast<char*>(t.param_lowp) + off * 2 : nullptr;
+            s.ms = q.exp_avg + off / block;
+            s.vs = q.exp_avg_sq + off / block;
+            s.first = off;
+            s.len = (int32_t)len;
+            s.group = (uint16_t)t.group;
+            s.gdtype = t.grad_dtype;
+            s.lowdt = t.param_lowp ? t.lowp_dtype : 0;
+            s.aligned = aligned;
+            segs.push_back(s);
+            cur_elems += (len + block - 1) / block * block;
+            ++cur_segs;
+            off += len;
         }
     }
     int32_t nchunks() const { return (int32_t)begin.size() - 1; }
@@ -381,6 +446,7 @@ void activate(soma_opt* o, int i) {
     o->active = i;
     o->norm_tab = pl.norm_tab;
     o->upd_tab = pl.upd_tab;
+    o->upd8_tab = pl.upd8_tab;
     o->group_present = pl.group_present;
     o->norm_grid = pl.norm_grid;
     o->upd_grid = pl.upd_grid;
@@ -388,11 +454,14 @@ void activate(soma_opt* o, int i) {
     o->plan = pl.info;
 }
 
-// Index of the prepared list equal to `list`, or -1 (the active one first).
+// Index of the prepared list equal to `list` (and its scales), or -1 (the active one first).
 int find_plan(const soma_opt* o, const soma_tensor_t* list, int64_t n) {
     auto equal = [&](const PreparedList& pl) {
         return pl.valid && (int64_t)pl.key.size() == n &&
-               (n == 0 || std::memcmp(pl.key.data(), list, (size_t)n * sizeof(soma_tensor_t)) == 0);
+               (n == 0 || (std::memcmp(pl.key.data(), list, (size_t)n * sizeof(soma_tensor_t)) == 0 &&
+                           pl.scales.empty() == !o->scales &&
+                           (!o->scales || std::memcmp(pl.scales.data(), o->scales,
+                                                      (size_t)n * sizeof(soma_scales_t)) == 0)));
     };
     if (o->active >= 0 && equal(o->plans[o->active])) return o->active;
     for (int i = 0; i < kMaxPlans; ++i)
@@ -403,11 +472,18 @@ int find_plan(const soma_opt* o, const soma_tensor_t* list, int64_t n) {
 // Builds the tables of a list not yet prepared into a free slot, else into
 // the least recently used one, and activates it.
 soma_status_t rebuild(soma_opt* o, const soma_tensor_t* list, int64_t n, void* stream) {
+    // trainable_total and f32_total: of the entries whose moments are fp32
     int64_t trainable_total = 0, owned_total = 0, owned_tensors = 0, f32_total = 0;
+    int64_t total8 = 0;
+    auto in_8_bits = [&](int64_t k) { return o->scales && o->scales[k].exp_avg && list[k].numel > 0; };
     for (int64_t k = 0; k < n; ++k) {
         if (!list[k].trainable) continue;
-        trainable_total += list[k].numel;
-        if (list[k].grad_dtype == SOMA_DTYPE_F32) f32_total += list[k].numel;
+        if (in_8_bits(k)) {
+            total8 += list[k].numel;
+        } else {
+            trainable_total += list[k].numel;
+            if (list[k].grad_dtype == SOMA_DTYPE_F32) f32_total += list[k].numel;
+        }
         if (list[k].owned && list[k].numel > 0) {
             owned_total += list[k].numel;
             owned_tensors += 1;
@@ -416,7 +492,7 @@ soma_status_t rebuild(soma_opt* o, const soma_tensor_t* list, int64_t n, void* s
     // A list for the single-launch step is cut into about one chunk per
     // cluster CTA, so each CTA's share is one pass of its threads.
     const int64_t limit = o->single_limit >= 0 ? o->single_limit : (int64_t)o->single_ctas * kSinglePerCta;
-    const bool single = o->single_ctas > 0 && trainable_total <= limit;
+    const bool single = o->single_ctas > 0 && trainable_total <= limit && total8 == 0;
     auto per_cta = [&](int64_t total) {  // ceil(total / CTAs), rounded up to a multiple of 64, at least 64
         const int64_t k = std::max(o->single_ctas, 1);
         return std::max<int64_t>(64, ((total + k - 1) / k + 63) / 64 * 64);
@@ -437,6 +513,10 @@ soma_status_t rebuild(soma_opt* o, const soma_tensor_t* list, int64_t n, void* s
         nrm.tail_total = owned_total;
         nrm.tail_slots = (int64_t)o->sm_count * kNormCtasPerSm;
     }
+    TableBuilder8 upd8;
+    const int64_t wave8 = kUpdate8CtasPerSm * std::max(o->sm_count, 1);
+    if (total8 <= kSmallUpdate8Chunk * wave8) upd8.chunk = kSmallUpdate8Chunk;
+    else if (total8 >= kLargeUpdate8Chunk * 8 * wave8) upd8.chunk = kLargeUpdate8Chunk;
     std::vector<uint8_t> present(o->groups.size(), 0);
     int64_t trainable = 0, owned = 0;
     for (int64_t k = 0; k < n; ++k) {
@@ -447,7 +527,8 @@ soma_status_t rebuild(soma_opt* o, const soma_tensor_t* list, int64_t n, void* s
         const uintptr_t a5[5] = {(uintptr_t)t.grad, (uintptr_t)t.param, (uintptr_t)t.exp_avg,
                                  (uintptr_t)t.exp_avg_sq, (uintptr_t)t.param_lowp};
         const int e5[5] = {grad_size(t.grad_dtype), 4, 4, 4, 2};
-        upd.add(t, vector_head(a5, e5, t.param_lowp ? 5 : 4), true);
+        if (in_8_bits(k)) upd8.add(t, o->scales[k]);
+        else upd.add(t, vector_head(a5, e5, t.param_lowp ? 5 : 4), true);
         trainable += t.numel;
         if (t.owned) {
             nrm.add(t, vector_head(a5, e5, 1), false);
@@ -455,14 +536,17 @@ soma_status_t rebuild(soma_opt* o, const soma_tensor_t* list, int64_t n, void* s
         }
     }
     upd.close();
+    upd8.close();
     nrm.close();
 
-    // layout: [update segs][norm segs][update chunk_begin][norm chunk_begin]
+    // layout: [update segs][norm segs][update chunk_begin][norm chunk_begin][8-bit update segs][its chunk_begin]
     const size_t o_us = 0;
     const size_t o_ns = align_up(o_us + upd.segs.size() * sizeof(soma::Seg), 256);
     const size_t o_ub = align_up(o_ns + nrm.segs.size() * sizeof(soma::Seg), 256);
     const size_t o_nb = align_up(o_ub + upd.begin.size() * sizeof(int32_t), 256);
-    const size_t bytes = align_up(o_nb + nrm.begin.size() * sizeof(int32_t), 256);
+    const size_t o_8s = align_up(o_nb + nrm.begin.size() * sizeof(int32_t), 256);
+    const size_t o_8b = align_up(o_8s + upd8.segs.size() * sizeof(soma::Seg8), 256);
+    const size_t bytes = align_up(o_8b + (total8 > 0 ? upd8.begin.size() : 0) * sizeof(int32_t), 256);
     const size_t nparts = std::max<size_t>(1, (size_t)nrm.nchunks());
 
     int slot = 0;
@@ -503,6 +587,10 @@ soma_status_t rebuild(soma_opt* o, const soma_tensor_t* list, int64_t n, void* s
     std::memcpy(h + o_ns, nrm.segs.data(), nrm.segs.size() * sizeof(soma::Seg));
     std::memcpy(h + o_ub, upd.begin.data(), upd.begin.size() * sizeof(int32_t));
     std::memcpy(h + o_nb, nrm.begin.data(), nrm.begin.size() * sizeof(int32_t));
+    if (total8 > 0) {
+        std::memcpy(h + o_8s, upd8.segs.data(), upd8.segs.size() * sizeof(soma::Seg8));
+        std::memcpy(h + o_8b, upd8.begin.data(), upd8.begin.size() * sizeof(int32_t));
+    }
     if ((e = cudaMemcpyAsync(pl.d_tables, h, bytes, cudaMemcpyHostToDevice, (cudaStream_t)stream)) != cudaSuccess)
         return o->cuda_fail(e, "cudaMemcpyAsync(tables)");
 
@@ -511,6 +599,8 @@ soma_status_t rebuild(soma_opt* o, const soma_tensor_t* list, int64_t n, void* s
                              reinterpret_cast<const int32_t*>(d + o_ub), upd.nchunks()};
     pl.norm_tab = soma::Table{reinterpret_cast<const soma::Seg*>(d + o_ns),
                               reinterpret_cast<const int32_t*>(d + o_nb), nrm.nchunks()};
+    pl.upd8_tab = soma::Table8{reinterpret_cast<const soma::Seg8*>(d + o_8s),
+                               reinterpret_cast<const int32_t*>(d + o_8b), upd8.nchunks()};
     const int64_t ucap = o->update_ctas_per_sm > 0 ? (int64_t)o->sm_count * o->update_ctas_per_sm : INT32_MAX;
     const int64_t ncap = o->norm_ctas_per_sm > 0 ? (int64_t)o->sm_count * o->norm_ctas_per_sm : INT32_MAX;
     pl.upd_grid = (int)std::min<int64_t>(upd.nchunks(), ucap);
@@ -518,6 +608,8 @@ soma_status_t rebuild(soma_opt* o, const soma_tensor_t* list, int64_t n, void* s
     pl.group_present = present;
     pl.single = single;
     pl.key.assign(list, list + n);
+    pl.scales.clear();
+    if (o->scales) pl.scales.assign(o->scales, o->scales + n);
 
     soma_plan_t& p = pl.info;
     p = soma_plan_t{};
@@ -531,7 +623,7 @@ soma_status_t rebuild(soma_opt* o, const soma_tensor_t* list, int64_t n, void* s
     p.update_block = soma::kUpdateBlock;
     p.trainable_numel = trainable;
     p.owned_numel = owned;
-    p.launches_per_step = 1 + (pl.upd_grid > 0 ? 1 : 0);
+    p.launches_per_step = 1 + (pl.upd_grid > 0 ? 1 : 0) + (upd8.nchunks() > 0 ? 1 : 0);
     pl.valid = true;
     o->plan_builds += 1;
     activate(o, slot);
@@ -824,6 +916,24 @@ void host_group_constants(soma_opt* o, soma::UpdateArgs& ua, std::vector<int64_t
     }
 }
 
+// The update of the entries with moments in 8 bits.
+cudaError_t launch_eight(soma_opt* o, const soma::UpdateArgs& ua, const std::vector<int64_t>* next, void* stream,
+                         bool overlap) {
+    if (o->upd8_tab.nchunks == 0) return cudaSuccess;
+    soma::Update8Args a{};
+    a.t = o->upd8_tab;
+    a.res = o->d_res;
+    a.gscale = o->d_gscale;
+    if (next) {
+        std::memcpy(a.groups, ua.groups, sizeof a.groups);
+        for (size_t q = 0; q < next->size(); ++q) a.step[q] = (uint32_t)(*next)[q];
+    } else {
+        a.dhp = o->d_hp;
+        a.dgroups = o->d_groups;
+    }
+    return (cudaError_t)soma::launch_update8(a, stream, next == nullptr, overlap, any_group_divisor(o));
+}
+
 // The launches of a step: the norm side (the square-sum kernel, or for the
 // multi-rank step the finish kernel over the ranks' sums), then the update.
 soma_status_t launch_step(soma_opt* o, double grad_divisor, double max_norm, const double* rank_sums,
@@ -897,7 +1007,9 @@ soma_status_t launch_step(soma_opt* o, double grad_divisor, double max_norm, con
         (e = (cudaError_t)soma::launch_update(ua, o->upd_grid, stream, false, ev == nullptr,
                                               any_group_divisor(o))) != cudaSuccess)
         return o->cuda_fail(e, "launching the update kernel");
-    o->plan.launches_per_step = single ? 1 : 1 + (o->upd_grid > 0 ? 1 : 0);
+    if (!single && (e = launch_eight(o, ua, &next, stream, ev == nullptr)) != cudaSuccess)
+        return o->cuda_fail(e, "launching the 8-bit update kernel");
+    o->plan.launches_per_step = single ? 1 : 1 + (o->upd_grid > 0 ? 1 : 0) + (o->upd8_tab.nchunks > 0 ? 1 : 0);
     o->plan.single_launch_ctas = single ? o->single_ctas : 0;
     if (ev) {
         if ((e = cudaEventRecord((*ev)[2], (cudaStream_t)stream)) != cudaSuccess)
@@ -1055,8 +1167,10 @@ soma_status_t soma_opt_step_graph(soma_opt_t h, const soma_tensor_t* list, int64
             (e = (cudaError_t)soma::launch_update(ua, o->upd_grid, stream, true, true, any_group_divisor(o))) !=
                 cudaSuccess)
             return o->cuda_fail(e, "launching the update kernel");
+        if ((e = launch_eight(o, ua, nullptr, stream, true)) != cudaSuccess)
+            return o->cuda_fail(e, "launching the 8-bit update kernel");
     }
-    o->plan.launches_per_step = single ? 1 : 1 + (o->upd_grid > 0 ? 1 : 0);
+    o->plan.launches_per_step = single ? 1 : 1 + (o->upd_grid > 0 ? 1 : 0) + (o->upd8_tab.nchunks > 0 ? 1 : 0);
     o->plan.single_launch_ctas = single ? o->single_ctas : 0;
     o->graph_locked = true;
     if (!cap) {
@@ -1066,6 +1180,54 @@ soma_status_t soma_opt_step_graph(soma_opt_t h, const soma_tensor_t* list, int64
         o->last_stream = stream;
     }
     return SOMA_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// A call with scales: the fp32 call with the handle told of them.
+template <typename F>
+soma_status_t with_scales(soma_opt_t h, const soma_scales_t* scales, int64_t n, F&& call) {
+    soma_opt* o = live_handle(h);
+    if (!o) return SOMA_ERR_STATE;
+    if (n > 0 && !scales) return o->fail(SOMA_ERR_INVALID_ARG, "scales is NULL with n > 0");
+    o->scales = n > 0 ? scales : nullptr;
+    soma_status_t st;
+    try {
+        st = call();
+    } catch (...) {
+        st = SOMA_ERR_OOM;
+    }
+    o->scales = nullptr;
+    return st;
+}
+
+}  // namespace
+
+extern "C" {
+
+soma_status_t soma_opt_step8(soma_opt_t h, const soma_tensor_t* list, const soma_scales_t* scales, int64_t n,
+                             double grad_divisor, double max_norm, void* stream) {
+    return with_scales(h, scales, n, [&] { return soma_opt_step(h, list, n, grad_divisor, max_norm, stream); });
+}
+
+soma_status_t soma_opt_step_graph8(soma_opt_t h, const soma_tensor_t* list, const soma_scales_t* scales, int64_t n,
+                                   double grad_divisor, double max_norm, void* stream) {
+    return with_scales(h, scales, n, [&] { return soma_opt_step_graph(h, list, n, grad_divisor, max_norm, stream); });
+}
+
+soma_status_t soma_opt_sumsq8(soma_opt_t h, const soma_tensor_t* list, const soma_scales_t* scales, int64_t n,
+                              double grad_divisor, double* sumsq_out, void* stream) {
+    return with_scales(h, scales, n, [&] { return soma_opt_sumsq(h, list, n, grad_divisor, sumsq_out, stream); });
+}
+
+soma_status_t soma_opt_step_from_sumsq8(soma_opt_t h, const soma_tensor_t* list, const soma_scales_t* scales, int64_t n,
+                                        double grad_divisor, double max_norm, const double* rank_sumsq, int32_t nranks,
+                                        void* stream) {
+    return with_scales(h, scales, n, [&] {
+        return soma_opt_step_from_sumsq(h, list, n, grad_divisor, max_norm, rank_sumsq, nranks, stream);
+    });
 }
 
 soma_status_t soma_opt_push_groups(soma_opt_t h, void* stream) {
