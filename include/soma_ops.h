@@ -1,7 +1,8 @@
 /*
  * soma_ops.h -- C ABI of the training operators for GB300 (sm_103a) whose
  * gradients the optimizer step of soma_opt.h takes: layer norm, linear layer,
- * distillation loss and embedding, each forward and backward.
+ * distillation loss, embedding and the cross entropy of a linear layer, each
+ * forward and backward.
  *
  * Matrices are row-major with unit stride along a row; `*_stride` is the
  * distance between rows in elements (at least the row's length; ignored when
@@ -197,6 +198,57 @@ soma_status_t soma_embedding_backward(int32_t device, const void *dy, int64_t dy
                                       int64_t dweight_stride, int32_t accumulate, void *workspace,
                                       int64_t workspace_bytes, int64_t vocab, int64_t cols, int32_t dtype,
                                       int32_t index_type, double scale, void *stream);
+
+/* ---- cross entropy of a linear layer over a vocabulary -------------------------
+ * The last linear layer and its loss in one, without the logits in memory:
+ *   z_rv   = sum_j x_rj * weight_vj,   lse_r = log sum_v exp(z_rv)
+ *   loss_r = row_weight_r * (lse_r - z_{r, t_r})
+ * and for grad_loss_r = dL/dloss_r, with g_r = row_weight_r * grad_loss_r,
+ *   dz_rv = g_r * (exp(z_rv - lse_r) - [v = t_r])
+ *   dx = dz * weight,   dweight = dz^T * x
+ * x[rows][k], weight[vocab][k], dx and dweight are all bf16 or all fp16;
+ * t_r = target[r / length][r % length] as for the embedding, rows = batch *
+ * length; row_weight[rows] fp32 (NULL = 1).  A row counts if its weight is not
+ * 0 and its target lies in [0, vocab); any other row has loss, lse and gradient
+ * 0, whatever its x and grad_loss hold (rows of padding, a target of -100).
+ * 1 <= k, vocab <= 2^30, rows <= 2^30.
+ *
+ * Logits, exponentials and sums are fp32.  dz is rounded once to the operands'
+ * 16 bits before the two products, whose tensor-core operands are 16-bit; a
+ * power of two, found from the largest |g|, keeps it in fp16's range.  The
+ * gradients make the logits again in pieces of the vocabulary; a piece's dz,
+ * at most 512 MB (or 512 bytes a row), lies in the workspace, as does a copy of
+ * the rows of x that count, and of weight where its rows do not start on
+ * 16-byte boundaries.
+ *
+ *   forward    loss and lse (either may be NULL)
+ *   backward   dx and dweight (either may be NULL) from forward's lse
+ *   loss_grad  loss, lse (may be NULL), and dx and dweight for grad_loss = 1
+ * The workspace functions take the arguments that sizes depend on: forward is
+ * 1 for forward and loss_grad, 0 for backward; dx and dweight are 1 where they
+ * are wanted. */
+soma_status_t soma_linear_cross_entropy_workspace(int32_t device, const void *weight, int64_t weight_stride, int64_t rows,
+                                                  int64_t vocab, int64_t k, int32_t dtype, int32_t forward, int32_t dx,
+                                                  int32_t dweight, int64_t *bytes);
+soma_status_t soma_linear_cross_entropy_forward(int32_t device, const void *x, int64_t x_stride, const void *weight,
+                                                int64_t weight_stride, const void *target, int64_t target_stride,
+                                                int64_t batch, int64_t length, const float *row_weight, float *loss,
+                                                float *lse, void *workspace, int64_t workspace_bytes, int64_t vocab,
+                                                int64_t k, int32_t dtype, int32_t index_type, void *stream);
+soma_status_t soma_linear_cross_entropy_backward(int32_t device, const float *grad_loss, const void *x, int64_t x_stride,
+                                                 const void *weight, int64_t weight_stride, const void *target,
+                                                 int64_t target_stride, int64_t batch, int64_t length, const float *lse,
+                                                 const float *row_weight, void *dx, int64_t dx_stride, void *dweight,
+                                                 int64_t dweight_stride, void *workspace, int64_t workspace_bytes,
+                                                 int64_t vocab, int64_t k, int32_t dtype, int32_t index_type,
+                                                 void *stream);
+soma_status_t soma_linear_cross_entropy_loss_grad(int32_t device, const void *x, int64_t x_stride, const void *weight,
+                                                  int64_t weight_stride, const void *target, int64_t target_stride,
+                                                  int64_t batch, int64_t length, const float *row_weight, float *loss,
+                                                  float *lse, void *dx, int64_t dx_stride, void *dweight,
+                                                  int64_t dweight_stride, void *workspace, int64_t workspace_bytes,
+                                                  int64_t vocab, int64_t k, int32_t dtype, int32_t index_type,
+                                                  void *stream);
 
 #ifdef __cplusplus
 }

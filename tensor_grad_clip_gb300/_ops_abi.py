@@ -46,6 +46,13 @@ SIGNATURES = {
     "soma_embedding_backward_workspace": (_S, [_I32, _I64, _I64, _I64, _I64P]),
     "soma_embedding_backward": (_S, [_I32, _P, _I64, _P, _I64, _I64, _I64, _P, _I64, _I32, _P, _I64, _I64, _I64, _I32,
                                      _I32, _D, _P]),
+    "soma_linear_cross_entropy_workspace": (_S, [_I32, _P, _I64, _I64, _I64, _I64, _I32, _I32, _I32, _I32, _I64P]),
+    "soma_linear_cross_entropy_forward": (_S, [_I32, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _P, _P, _P, _P, _I64, _I64,
+                                               _I64, _I32, _I32, _P]),
+    "soma_linear_cross_entropy_backward": (_S, [_I32, _P, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _P, _P, _P, _I64, _P,
+                                                _I64, _P, _I64, _I64, _I64, _I32, _I32, _P]),
+    "soma_linear_cross_entropy_loss_grad": (_S, [_I32, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _P, _P, _P, _P, _I64, _P,
+                                                 _I64, _P, _I64, _I64, _I64, _I32, _I32, _P]),
 }
 
 _lib = None

@@ -21,8 +21,8 @@ LIB = os.path.join(OUT_DIR, "libsoma_opt.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["kernels.cu", "soma_opt.cpp", "noalloc.cu", "ops.cpp", "layer_norm.cu", "linear.cu", "distill.cu",
-           "lm_ops.cpp", "embedding.cu", "adamw8.cu"]
-HEADERS = ["soma_kernels.h", "ops_kernels.h", "ops_host.h", "ops_device.cuh", "mbarrier.cuh", "tcgen05.cuh"]
+           "lm_ops.cpp", "embedding.cu", "adamw8.cu", "cross_entropy.cu"]
+HEADERS = ["soma_kernels.h", "ops_kernels.h", "ops_host.h", "ops_device.cuh", "mbarrier.cuh", "tcgen05.cuh", "gemm_tile.cuh"]
 PUBLIC_HEADERS = ["soma_opt.h", "soma_ops.h"]
 
 

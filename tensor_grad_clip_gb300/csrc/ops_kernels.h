@@ -149,11 +149,36 @@ int64_t embedding_bwd_workspace(int64_t rows, int64_t cols);
 int launch_embedding_bwd(const EmbeddingArgs& a, const void* dy, int64_t dy_stride, bool accumulate, void* workspace,
                          int sm_count, void* stream);
 
+struct HeadArgs {
+    const void* x;
+    int64_t x_stride;
+    const void* weight;
+    int64_t weight_stride;
+    TokenArgs tokens;
+    const float* row_weight;  // or nullptr
+    const float* grad_loss;   // backward; else nullptr
+    const float* lse_in;      // backward
+    float* loss;              // forward, loss_grad; or nullptr
+    float* lse;               // forward, loss_grad; or nullptr
+    void* dx;                 // backward, loss_grad; or nullptr
+    int64_t dx_stride;
+    void* dweight;            // backward, loss_grad; or nullptr
+    int64_t dweight_stride;
+    int64_t rows;
+    int32_t vocab, k;
+    int32_t dtype;
+};
+
+// forward: log-sum-exp and loss; the gradients of dx and dweight that are not nullptr.  rows >= 1.
+int64_t head_workspace(const HeadArgs& a, bool forward, int sm_count);
+int launch_head(const HeadArgs& a, bool forward, void* workspace, int sm_count, void* stream);
+
 // How often a bounded wait inside a kernel of the current device has run out:
 // a count that only grows (modulo 2^32).  The copy waits for the legacy default
 // stream alone; kernels on others may still be running.
 int read_norm_gave_up(unsigned* count);
-int read_linear_gave_up(unsigned* count);
+int read_linear_gave_up(unsigned* count);  // those of the linear layer with cross entropy too
+int read_head_gave_up(unsigned* count);
 int read_distill_gave_up(unsigned* count);
 
 }  // namespace soma

@@ -34,8 +34,9 @@ from . import SomaError, _ops_abi
 from ._abi import SOMA_DTYPE_BF16, SOMA_DTYPE_F16, SOMA_DTYPE_F32
 
 __all__ = ["layer_norm_forward", "layer_norm_backward", "linear_forward", "linear_backward", "distill_forward",
-           "distill_backward", "distill_loss_grad", "embedding_forward", "embedding_backward", "layer_norm", "linear",
-           "distill_loss", "embedding", "check", "ACTIVATIONS"]
+           "distill_backward", "distill_loss_grad", "embedding_forward", "embedding_backward",
+           "linear_cross_entropy_forward", "linear_cross_entropy_backward", "linear_cross_entropy_loss_grad", "layer_norm",
+           "linear", "distill_loss", "embedding", "linear_cross_entropy", "check", "ACTIVATIONS"]
 
 ACTIVATIONS = {"none": _ops_abi.SOMA_ACT_NONE, "relu": _ops_abi.SOMA_ACT_RELU, "gelu": _ops_abi.SOMA_ACT_GELU,
                "gelu_tanh": _ops_abi.SOMA_ACT_GELU_TANH, "silu": _ops_abi.SOMA_ACT_SILU}
@@ -480,6 +481,95 @@ def embedding_backward(dy, index, vocab: int, *, scale: float = 1.0, out=None):
     return dweight
 
 
+# ---- cross entropy of a linear layer ---------------------------------------------
+
+@functools.lru_cache(maxsize=1024)
+def _head_bytes(dev, w, rows, vocab, k, dt, forward, dx, dweight):
+    need = ctypes.c_int64()
+    _check(_ops_abi.soma_linear_cross_entropy_workspace(dev, *_operand(w, k), rows, vocab, k, dt, forward, dx, dweight,
+                                                        ctypes.byref(need)))
+    return need.value
+
+
+def _head_inputs(x, weight, target, row_weight, forward, dx, dweight):
+    """What the three calls share: (device, what the C calls take first, row weights, workspace, what they take last)."""
+    x2 = _matrix(x, "x")
+    w2 = _matrix(weight, "weight")
+    rows, k = x2.shape
+    vocab = w2.shape[0]
+    _like(weight, "weight", x, (vocab, k), x.dtype)
+    if target.shape != x.shape[:-1]:
+        raise ValueError(f"target: shape {tuple(target.shape)}, expected {tuple(x.shape[:-1])}")
+    address, stride, batch, length, code = _tokens(target, "target", x)
+    w = None
+    if row_weight is not None:
+        _like(row_weight, "row_weight", x, x.shape[:-1], torch.float32)
+        if not row_weight.is_contiguous():
+            raise ValueError("row_weight: must be contiguous")
+        w = row_weight.data_ptr()
+    dt = _code(x, "x")
+    dev = x.device.index
+    need = _head_bytes(dev, _unaligned(w2), rows, vocab, k, dt, int(forward), int(dx), int(dweight))
+    first = (x2.data_ptr(), x2.stride(0), w2.data_ptr(), w2.stride(0), address, stride, batch, length)
+    return dev, first, w, _workspace(need, x.device), need, (vocab, k, dt, code)
+
+
+def _head_gradients(x, weight, dx, dweight):
+    """New gradients, and (address, stride) of both."""
+    k = x.shape[-1]
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if dx else None
+    dw = torch.empty(weight.shape, dtype=x.dtype, device=x.device) if dweight else None
+    return dx, dw, (_ptr(dx), k, _ptr(dw), k)
+
+
+@_on_stream
+def linear_cross_entropy_forward(x, weight, target, *, row_weight=None):
+    """(loss, lse), fp32 and one per row: the cross entropy of softmax(x
+    weight^T) at the target tokens, without the logits in memory.
+
+    x [..., k] and weight [vocab, k]: bf16 or fp16.  target [...]: int32 or
+    int64; a target outside the vocabulary, such as -100, or a row_weight (fp32,
+    [...]) of 0 marks a row that does not count: loss, lse and gradient are 0."""
+    _ops_abi.load()
+    dev, first, w, work, need, last = _head_inputs(x, weight, target, row_weight, True, False, False)
+    loss = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    lse = torch.empty_like(loss)
+    _check(_ops_abi.soma_linear_cross_entropy_forward(dev, *first, w, loss.data_ptr(), lse.data_ptr(), _ptr(work), need,
+                                                      *last, _raw_stream(dev)))
+    return loss, lse
+
+
+@_on_stream
+def linear_cross_entropy_backward(grad_loss, x, weight, target, lse, *, row_weight=None, input_grad: bool = True,
+                                  weight_grad: bool = True):
+    """(dx, dweight) for grad_loss = dL/dloss, in x's dtype; lse is the
+    forward pass's.  Those not asked for are None."""
+    _ops_abi.load()
+    dev, first, w, work, need, last = _head_inputs(x, weight, target, row_weight, False, input_grad, weight_grad)
+    for t, name in ((grad_loss, "grad_loss"), (lse, "lse")):
+        _like(t, name, x, x.shape[:-1], torch.float32)
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: must be contiguous")
+    dx, dw, out = _head_gradients(x, weight, input_grad, weight_grad)
+    _check(_ops_abi.soma_linear_cross_entropy_backward(dev, grad_loss.data_ptr(), *first, lse.data_ptr(), w, *out,
+                                                       _ptr(work), need, *last, _raw_stream(dev)))
+    return dx, dw
+
+
+@_on_stream
+def linear_cross_entropy_loss_grad(x, weight, target, *, row_weight=None, input_grad: bool = True,
+                                   weight_grad: bool = True):
+    """(loss, dx, dweight): the forward pass and the gradients of the losses'
+    sum (put 1 / (number of rows), a loss scale and the like into row_weight)."""
+    _ops_abi.load()
+    dev, first, w, work, need, last = _head_inputs(x, weight, target, row_weight, True, input_grad, weight_grad)
+    loss = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    dx, dw, out = _head_gradients(x, weight, input_grad, weight_grad)
+    _check(_ops_abi.soma_linear_cross_entropy_loss_grad(dev, *first, w, loss.data_ptr(), None, *out, _ptr(work), need,
+                                                        *last, _raw_stream(dev)))
+    return loss, dx, dw
+
+
 # ---- autograd -----------------------------------------------------------------
 
 def _even(g):
@@ -568,6 +658,23 @@ class _Embedding(torch.autograd.Function):
         return None, embedding_backward(_even(dy), index, ctx.vocab, scale=ctx.scale), None
 
 
+class _LinearCrossEntropy(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, target, row_weight):
+        loss, lse = linear_cross_entropy_forward(x, weight, target, row_weight=row_weight)
+        ctx.save_for_backward(x, weight, target, lse, row_weight)
+        return loss
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_loss):
+        x, weight, target, lse, row_weight = ctx.saved_tensors
+        wants = ctx.needs_input_grad
+        dx, dw = linear_cross_entropy_backward(grad_loss.contiguous(), x, weight, target, lse, row_weight=row_weight,
+                                               input_grad=wants[0], weight_grad=wants[1])
+        return dx, dw, None, None
+
+
 def layer_norm(x, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None, eps: float = 1e-5):
     """Differentiable layer norm over the last dimension (see layer_norm_forward)."""
     return _LayerNorm.apply(x, weight, bias, eps)
@@ -591,3 +698,9 @@ def distill_loss(logits, teacher_logits, teacher_index, *, temperature: float = 
 def embedding(index, weight, *, scale: float = 1.0):
     """Differentiable scale * weight[index] (see embedding_forward)."""
     return _Embedding.apply(index, weight, scale)
+
+
+def linear_cross_entropy(x, weight, target, *, row_weight: Optional[torch.Tensor] = None):
+    """Differentiable cross entropy per row of softmax(x weight^T) (see
+    linear_cross_entropy_forward); the row weights are constants."""
+    return _LinearCrossEntropy.apply(x, weight, target, row_weight)
