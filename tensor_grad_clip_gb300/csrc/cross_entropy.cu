@@ -6,11 +6,14 @@
 //   gather   those rows of x, one after the other on 16-byte boundaries: rows
 //            that do not count cost nothing in the products, and what they
 //            hold (NaN, say) reaches no gradient
-//   stats    z = x W^T; a tile's maximum and sum of exponentials per row
+//   stats    z = x W^T; maximum and sum of exponentials of every 32 logits
 //   join     log-sum-exp and loss
 // and for the gradients, for one piece of the vocabulary after the other,
 //   dz       z again; dz = g (exp(z - lse) - [its token]), rounded to the
-//            operands' 16 bits into a buffer of the piece's size
+//            operands' 16 bits into a buffer of the piece's size; where one
+//            piece is the whole vocabulary and the loss is wanted too, `stats`
+//            leaves exp(z - the 32 logits' maximum) there, and a pass over the
+//            buffer makes dz of it, instead of a fourth product
 //   dweight  dz^T x, the piece's rows, complete
 //   dx       dz W added to fp32 sums, which a last kernel rounds
 // The number of rows that count is only known on the device: the products read
@@ -161,8 +164,9 @@ __global__ void __launch_bounds__(256) gather_kernel(const T* x, int64_t stride,
 struct LogitArgs {
     CUtensorMap a, b, out;
     HeadRows h;
-    int64_t pitch;          // of `parts`: rows
-    float2* parts;          // [slices of BN / 4 columns][pitch] maximum and sum of exponentials
+    float2* parts;          // [rows][slices of 32 columns] maximum and sum of exponentials
+    int64_t slices;
+    bool keep;              // stats: store the exponentials too
     int32_t n, k;           // columns (of the piece), their first in the vocabulary, sum length
     int32_t first;
     int32_t tiles_n, strip;
@@ -192,31 +196,26 @@ __device__ __forceinline__ void load_logits(uint32_t acc, int col, int n, float 
     }
 }
 
+// What the kept exponentials, at most 1, are multiplied by: fp16 has no
+// small enough numbers for what a vocabulary's tail weighs.
+template <typename T>
+constexpr float kKeepScale = kIsBf16<T> ? 1.f : 16384.f;
+
 template <int CG, int BN, typename T>
 __global__ void __launch_bounds__(kTileThreads, 1) stats_kernel(const __grid_constant__ LogitArgs p) {
     tile_products<CG, BN, T>(
         &p.a, &p.b, true, true,
-        [&] { return plan_rows<CG>(p.h.counted->padded, p.k, p.tiles_n, p.strip, false, 1); },
-        [&](uint32_t acc, int row0, int col0, int cols, int, const TilePlan&, char*) {
-            if (col0 >= p.n) return;
+        [&] { return plan_rows<CG>(p.h.counted->padded, p.k, p.tiles_n, p.strip, true, 1); },
+        [&](uint32_t acc, int row0, int col0, int cols, int, const TilePlan&, char* staging) {
             const int row = row0 + (threadIdx.x & 31);
-            const int at = __ldg(p.h.token + row) - col0;  // the token's column here
-            float m = kLowest, s = 0.f;
-            for (int c = 0; c < cols; c += 32) {
+            const int at = p.h.token[row] - col0;  // the token's column here
+            Stager<T> stager{staging + (threadIdx.x >> 5) * kStagerBytes, row0, 0, p.n};
+            for (int c = 0; c < cols && col0 + c < p.n; c += 32) {
                 float z[32];
                 load_logits(acc + c, col0 + c, p.n, z);
-                float top = m;
+                float m = kLowest;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) top = fmaxf(top, z[i]);
-                s *= exp2_fast((m - top) * kLog2e);
-                m = top;
-                float even = 0.f, odd = 0.f;
-#pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    even += exp2_fast((z[i] - m) * kLog2e);
-                    odd += exp2_fast((z[i + 1] - m) * kLog2e);
-                }
-                s += even + odd;
+                for (int i = 0; i < 32; ++i) m = fmaxf(m, z[i]);
                 const int d = at - c;
                 if (__any_sync(0xffffffffu, d >= 0 && d < 32) && d >= 0 && d < 32) {
                     float t = z[0];
@@ -224,39 +223,80 @@ __global__ void __launch_bounds__(kTileThreads, 1) stats_kernel(const __grid_con
                     for (int i = 1; i < 32; ++i) t = d == i ? z[i] : t;
                     p.h.z_token[row] = t;
                 }
+                float even = 0.f, odd = 0.f;
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    z[i] = exp2_fast((z[i] - m) * kLog2e);
+                    z[i + 1] = exp2_fast((z[i + 1] - m) * kLog2e);
+                    even += z[i];
+                    odd += z[i + 1];
+                }
+                p.parts[row * p.slices + (col0 + c) / 32] = make_float2(m, even + odd);
+                if (p.keep) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) z[i] *= kKeepScale<T>;
+                    stager.store(z, col0 + c, &p.out, true, nullptr, 0);
+                }
             }
-            p.parts[(int64_t)(col0 / (BN / 4)) * p.pitch + row] = make_float2(m, s);
         });
 }
 
 __device__ __forceinline__ float2 join_stats(float2 a, float2 b) {
     const float m = fmaxf(a.x, b.x);
-    return make_float2(m, a.y * exp2f((a.x - m) * kLog2e) + b.y * exp2f((b.x - m) * kLog2e));
+    return make_float2(m, a.y * exp2_fast((a.x - m) * kLog2e) + b.y * exp2_fast((b.x - m) * kLog2e));
 }
 
-// Log-sum-exp and loss of 32 counted rows per CTA: a lane a row, warps take
-// slices in turn.
-constexpr int kJoinWarps = 32;
-__global__ void __launch_bounds__(32 * kJoinWarps) stats_join_kernel(const float2* parts, int64_t pitch, int slices,
-                                                                     HeadRows h, float* loss, float* lse) {
-    __shared__ float2 sums[kJoinWarps][32];
+// Log-sum-exp and loss of a counted row per CTA.
+constexpr int kJoinWarps = 4;
+__global__ void __launch_bounds__(32 * kJoinWarps) stats_join_kernel(const float2* parts, int64_t slices, HeadRows h,
+                                                                     float* loss, float* lse) {
+    __shared__ float2 sums[kJoinWarps];
     follow_stream();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = blockIdx.x * 32 + lane;
-    if ((int)blockIdx.x * 32 >= h.counted->rows) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = blockIdx.x;
+    if (i >= h.counted->rows) return;
     float2 own = make_float2(kLowest, 0.f);
 #pragma unroll 8
-    for (int q = warp; q < slices; q += kJoinWarps) own = join_stats(own, __ldcg(parts + q * pitch + i));
-    sums[warp][lane] = own;
+    for (int64_t q = threadIdx.x; q < slices; q += 32 * kJoinWarps) own = join_stats(own, __ldcg(parts + i * slices + q));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        own = join_stats(own, make_float2(__shfl_xor_sync(0xffffffffu, own.x, o), __shfl_xor_sync(0xffffffffu, own.y, o)));
+    if (lane == 0) sums[warp] = own;
     __syncthreads();
-    if (warp) return;
-    for (int w = 1; w < kJoinWarps; ++w) own = join_stats(own, sums[w][lane]);
-    if (i >= h.counted->rows) return;
+    if (threadIdx.x) return;
+    for (int w = 1; w < kJoinWarps; ++w) own = join_stats(own, sums[w]);
     const float log_s = logf(own.y), total = own.x + log_s;
     const int r = h.row[i];
     h.lse[i] = total;
     if (lse) lse[r] = total;
     // (m - z) + log s: near 0 it keeps its digits where lse - z would not
     if (loss) loss[r] = h.weight[i] * ((own.x - h.z_token[i]) + log_s);
+}
+
+// dz of the kept exponentials, in place: a thread 8 of them.  What rounding
+// them once more costs is at most another half step of 16 bits; the token's
+// own element, a difference from 1, is made of its logit.
+template <typename T>
+__global__ void __launch_bounds__(256) keep_kernel(T* dz, int64_t stride, const float2* parts, int64_t slices, HeadRows h,
+                                                   int32_t n) {
+    follow_stream();
+    const int row = blockIdx.y;
+    if (row >= h.counted->padded) return;
+    const int c = ((int)blockIdx.x * 256 + (int)threadIdx.x) * 8;
+    if (c >= n) return;
+    const float lse = h.lse[row], g = h.g[row] * h.counted->scale;
+    const float f = g * (1.f / kKeepScale<T>) * exp2_fast((__ldg(&parts[row * slices + c / 32].x) - lse) * kLog2e);
+    uint4* at = reinterpret_cast<uint4*>(dz + row * stride + c);
+    float x[8];
+    widen16(*at, x, T{});
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] *= f;
+    const int d = h.token[row] - c;
+    if (d >= 0 && d < 8) {
+        const float own = g * (exp2_fast((h.z_token[row] - lse) * kLog2e) - 1.f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = d == i ? own : x[i];
+    }
+    *at = narrow16(x, T{});
 }
 
 // dz of a piece, scaled.
@@ -399,7 +439,8 @@ __global__ void __launch_bounds__(256) dx_round_kernel(const float* sums, int64_
 
 int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 
-// The buffer for a piece's dz: half a gigabyte, or what one column of tiles needs.
+// The buffer for a piece's dz: half a gigabyte or as much as the weight has,
+// or what one column of tiles needs.
 constexpr int64_t kPieceBytes = 512ll << 20;
 
 struct HeadLayout {
@@ -416,14 +457,25 @@ struct HeadLayout {
         const int64_t pairs = std::max(1, sms / 2);
         const int64_t t256 = (rows + 255) / 256 * ((vocab + 255) / 256), t128 = (rows + 127) / 128 * ((vocab + 127) / 128);
         big = rows > 128 && (t256 + pairs - 1) / pairs < (t128 + sms - 1) / sms;
-        const int64_t most = std::max<int64_t>(256, kPieceBytes / (2 * pitch) / 256 * 256);
+        const int64_t buffer = std::max(kPieceBytes, vocab * k * 2);
+        const int64_t most = std::max<int64_t>(256, buffer / (2 * pitch) / 256 * 256);
         pieces = (vocab + most - 1) / most;
         piece = ((vocab + pieces - 1) / pieces + 255) / 256 * 256;
         pieces = (vocab + piece - 1) / piece;
-        const int64_t tiles = (rows + 127) / 128 * ((k + 127) / 128);
+        // dx has few tiles and long sums: parts of the sums make the last wave
+        // full, or the only one.  (A part more costs its share of writing and
+        // reading the sums, about as much as four of its pipeline stages.)
+        const int64_t edge = big ? 256 : 128, workers = big ? pairs : sms, kts = std::min(piece, vocab) / kBK + 1;
+        const int64_t tiles = (rows + edge - 1) / edge * ((k + edge - 1) / edge);
         splits = 1;
-        if (pieces == 1 && !big)
-            while (splits < 16 && tiles * splits * 2 <= sms && (vocab + kBK - 1) / kBK >= 16 * splits) splits *= 2;
+        double least = 0;
+        for (int s = 1; s <= 16 && kts >= 16 * s && tiles <= 4 * workers; ++s) {
+            const double time = (double)((tiles * s + workers - 1) / workers) * ((double)kts / s + 4) + 0.05 * kts * (s > 1);
+            if (s == 1 || time < least) {
+                least = time;
+                splits = s;
+            }
+        }
         x_stride = (k + 7) / 8 * 8;
         w_stride = x_stride;
         sums_stride = (k + 255) / 256 * 256;
@@ -439,18 +491,17 @@ struct HeadLayout {
         z_token = take(pitch * 4);
         x = take(pitch * x_stride * 2);
         w = take(copy_weight ? vocab * w_stride * 2 : 0);
-        parts = take(forward ? (vocab + slice() - 1) / slice() * pitch * 8 : 0);
+        parts = take(forward ? pitch * slices(vocab) * 8 : 0);
         dz = take(dx || dweight ? pitch * piece * 2 : 0);
         sums = take(dx ? splits * pitch * sums_stride * 4 : 0);
         bytes = at;
     }
-    int64_t slice() const { return big ? 64 : 32; }  // columns of a part
+    static int64_t slices(int64_t vocab) { return (vocab + 31) / 32; }
 };
 
-int launch_after(const void* kernel, int64_t grid, int threads, void** args, void* stream) {
-    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+int launch_after(const void* kernel, dim3 grid, int threads, void** args, void* stream) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.stream = (cudaStream_t)stream;
     cudaLaunchAttribute attr[1];
@@ -488,7 +539,7 @@ struct Head {
     // z = x W^T over columns [first, first + n) of the vocabulary.
     int logits(LogitArgs& p, int64_t first, int64_t n, const void* kernel) const {
         p.h = h;
-        p.pitch = at.pitch;
+        p.slices = HeadLayout::slices(a.vocab);
         p.n = (int32_t)n;
         p.k = a.k;
         p.first = (int32_t)first;
@@ -501,24 +552,35 @@ struct Head {
         // (half tiles make at most twice as many units)
         return tiles(kernel, rows_of_tiles(a.rows) * p.tiles_n * 2, args);
     }
-    int forward() const {
+    int forward(bool keep) const {
         LogitArgs p{};
         p.parts = reinterpret_cast<float2*>(ws + at.parts);
-        if (const int e = logits(p, 0, a.vocab, (const void*)stats_kernel<CG, BN, T>)) return e;
+        p.keep = keep;
+        int e = keep ? make_map(&p.out, a.dtype, ws + at.dz, at.piece, at.pitch, a.vocab, 32, 32) : cudaSuccess;
+        if (!e) e = logits(p, 0, a.vocab, (const void*)stats_kernel<CG, BN, T>);
+        if (e) return e;
         const float2* parts = p.parts;
-        int64_t pitch = at.pitch;
-        int slices = (int)((a.vocab + BN / 4 - 1) / (BN / 4));
+        int64_t slices = p.slices, stride = at.piece;
         HeadRows rows = h;
         float *loss = a.loss, *lse = a.lse;
-        void* args[] = {&parts, &pitch, &slices, &rows, &loss, &lse};
-        return launch_after((const void*)stats_join_kernel, (a.rows + 31) / 32, 32 * kJoinWarps, args, stream);
+        void* args[] = {&parts, &slices, &rows, &loss, &lse};
+        e = launch_after((const void*)stats_join_kernel, dim3((unsigned)a.rows), 32 * kJoinWarps, args, stream);
+        if (e || !keep) return e;
+        T* dz = reinterpret_cast<T*>(ws + at.dz);
+        int32_t n = a.vocab;
+        void* keep_args[] = {&dz, &stride, &parts, &slices, &rows, &n};
+        return launch_after((const void*)keep_kernel<T>, dim3((a.vocab + 2047) / 2048, (unsigned)std::max<int64_t>(64, (a.rows + 63) / 64 * 64)),
+                            256, keep_args, stream);
     }
-    int gradients() const {
+    int gradients(bool kept) const {
         for (int64_t first = 0; first < a.vocab; first += at.piece) {
             const int64_t n = std::min<int64_t>(at.piece, a.vocab - first);
-            LogitArgs p{};
-            int e = make_map(&p.out, a.dtype, ws + at.dz, at.piece, at.pitch, n, 32, 32);
-            if (!e) e = logits(p, first, n, (const void*)dz_kernel<CG, BN, T>);
+            int e = cudaSuccess;
+            if (!kept) {
+                LogitArgs p{};
+                e = make_map(&p.out, a.dtype, ws + at.dz, at.piece, at.pitch, n, 32, 32);
+                if (!e) e = logits(p, first, n, (const void*)dz_kernel<CG, BN, T>);
+            }
             if (!e && a.dweight) e = dweight(first, n);
             if (!e && a.dx) e = dx(first, n);
             if (e) return e;
@@ -531,7 +593,9 @@ struct Head {
         HeadRows hr = h;
         T* out = static_cast<T*>(a.dx);
         void* args[] = {&sums, &pitch, &sums_stride, &splits, &hr, &out, &stride, &rows, &cols, &pieces};
-        return launch_after((const void*)dx_round_kernel<T>, (rows * pieces + 7) / 8, 256, args, stream);
+        const int64_t grid = (rows * pieces + 7) / 8;
+        if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+        return launch_after((const void*)dx_round_kernel<T>, dim3((unsigned)grid), 256, args, stream);
     }
     int dweight(int64_t first, int64_t n) const {
         GradArgs p{};
@@ -561,7 +625,8 @@ struct Head {
         p.add = first > 0;
         p.n = a.k;
         p.k = (int32_t)n;
-        p.splits = at.splits;
+        // (a last piece that has less than a stage for each part is added to the first part's sums)
+        p.splits = (n + kBK - 1) / kBK >= at.splits ? at.splits : 1;
         p.tiles_n = (a.k + BN - 1) / BN;
         p.strip = strip_of(p.tiles_n, BN, n);
         const char* b = static_cast<const char*>(w) + first * w_stride * 2;
@@ -600,7 +665,7 @@ int launch_head(const HeadArgs& a, bool forward, void* workspace, int sm_count, 
     {
         HeadArgs copy_of = a;
         void* args[] = {&copy_of, &h};
-        if ((e = launch_after((const void*)select_kernel, 1, kSelectThreads, args, stream))) return e;
+        if ((e = launch_after((const void*)select_kernel, dim3(1), kSelectThreads, args, stream))) return e;
     }
     auto run = [&](auto t) -> int {
         using T = decltype(t);
@@ -611,11 +676,15 @@ int launch_head(const HeadArgs& a, bool forward, void* workspace, int sm_count, 
         int pieces = (a.k + 255) / 256;
         void* args[] = {&x, &stride, &rows, &cols, &out, &out_stride, &h, &pieces};
         const int64_t padded = std::max<int64_t>(64, (a.rows + 63) / 64 * 64);
-        int e = launch_after((const void*)gather_kernel<T>, (padded * pieces + 7) / 8, 256, args, stream);
-        if (e) return e;
+        const int64_t grid = (padded * pieces + 7) / 8;
+        if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+        if (const int e = launch_after((const void*)gather_kernel<T>, dim3((unsigned)grid), 256, args, stream)) return e;
         auto products = [&](const auto& head) {
-            int e = forward ? head.forward() : cudaSuccess;
-            if (!e && (a.dx || a.dweight)) e = head.gradients();
+            const bool gradients = a.dx || a.dweight;
+            // (a row of the pass over the kept exponentials is a row of its grid)
+            const bool keep = forward && gradients && at.pieces == 1 && a.rows <= 65472;
+            int e = forward ? head.forward(keep) : cudaSuccess;
+            if (!e && gradients) e = head.gradients(keep);
             return e;
         };
         if (at.big) return products(Head<2, 256, T>{a, at, h, ws, w, w_stride, sm_count, stream});

@@ -43,8 +43,9 @@ class Case:
         self.g = torch.randn(rows, device="cuda")
         self.rows, self.vocab, self.k, self.dtype = rows, vocab, k, dtype
 
-    def reference(self, grad_loss=None, lse=None):
-        """Loss, lse, dx, dweight and their bounds in fp64; lse: as given to the backward pass."""
+    def reference(self, grad_loss=None, lse=None, kept=False):
+        """Loss, lse, dx, dweight and their bounds in fp64; lse: as given to the backward pass; kept: exponentials are
+        rounded to 16 bits before dz is, which is another half step of p, or of fp16's smallest 2^-24 / 2^14 of the largest."""
         x, w = self.x.double(), self.w.double()
         counts = (self.t >= 0) & (self.t < self.vocab)
         weight = torch.ones(self.rows, device="cuda", dtype=torch.float64) if self.weight is None else self.weight.double()
@@ -68,6 +69,8 @@ class Case:
         e_dz = g.abs()[:, None] * p * torch.expm1(near) + 2 * U32 * (g.abs()[:, None] * p + dz.abs())
         # rounded once to 16 bits; what is scaled below the type's smallest steps (fp16: 2^-25 of 2^14 / the largest |g|)
         step = g.abs().max() * 2.0 ** -38 if self.dtype == torch.float16 else 2.0 ** -126
+        if kept:
+            e_dz = e_dz + g.abs()[:, None] * (HALF_ULP[self.dtype] * p + (2.0 ** -39 if self.dtype == torch.float16 else 2.0 ** -126))
         e_dz = e_dz + HALF_ULP[self.dtype] * (dz.abs() + e_dz) + step
         mag = dz.abs() + e_dz
         dx, dw = dz @ w, dz.t() @ x
@@ -84,7 +87,7 @@ class Case:
 
     def check(self, ops, what=""):
         kw = dict(row_weight=self.weight)
-        ref = self.reference()
+        ref = self.reference(kept=True)
         loss, lse = ops.linear_cross_entropy_forward(self.x, self.w, self.t, **kw)
         assert loss.dtype == lse.dtype == torch.float32
         assert_close(loss, *ref["loss"], f"{what}: loss")
@@ -122,6 +125,35 @@ def test_many_tiles(ops, dtype, rows, vocab, k):
 def test_pieces_of_the_vocabulary_and_parts_of_the_sum(ops, dtype, rows, vocab):
     torch.manual_seed(1)
     Case(rows, vocab, 64, dtype).check(ops)
+
+
+def test_a_last_piece_of_one_column(ops):
+    """65536 rows take 4096 columns at a time: 16 pieces, the last with one."""
+    torch.manual_seed(11)
+    rows, vocab, k = 65536, 15 * 4096 + 1, 64
+    c = Case(rows, vocab, k, torch.bfloat16)
+    c.t[:50] = vocab - 1
+    loss, lse = ops.linear_cross_entropy_forward(c.x, c.w, c.t, row_weight=c.weight)
+    dx, dw = ops.linear_cross_entropy_backward(c.g, c.x, c.w, c.t, lse, row_weight=c.weight)
+    at = torch.arange(0, rows, 173, device="cuda")
+    at[:40] = torch.arange(40, device="cuda")
+    part = Case(1, 1, 1, torch.bfloat16)
+    part.x, part.w, part.t, part.weight = c.x[at], c.w, c.t[at], c.weight[at]
+    part.rows, part.vocab, part.k = len(at), vocab, k
+    assert_close(loss[at], *part.reference()["loss"], "loss")
+    assert_close(dx[at], *part.reference(c.g[at], lse[at])["dx"], "dx")
+    # the last column's gradient, of all rows
+    counts = (c.t >= 0) & (c.t < vocab) & (c.weight != 0)
+    g = torch.where(counts, c.weight * c.g, 0.0).double()
+    z = c.x.double() @ c.w[-1].double()
+    dz = g * (torch.exp(z - torch.where(counts, lse, 0.0).double()) - (c.t == vocab - 1).double())
+    want = dz @ c.x.double()
+    near = 2.0 ** -20 + (k + 8) * 2 * U32 * (c.x.double().abs() @ c.w[-1].double().abs())
+    e = g.abs() * 2 * near + 2.0 ** -8 * dz.abs()
+    tol = e @ c.x.double().abs() + (rows + 65) * 2 * U32 * (dz.abs() @ c.x.double().abs())
+    assert_close(dw[-1], want, tol + rounding(want.abs() + tol, torch.bfloat16), "the last column")
+    _, dx2, _ = ops.linear_cross_entropy_loss_grad(c.x, c.w, c.t, row_weight=c.weight, weight_grad=False)
+    assert_close(dx2[at], *part.reference()["dx"], "dx of the loss")
 
 
 @pytest.mark.parametrize("xpad,wpad,offset", [(0, 0, 1), (3, 0, 0), (8, 8, 0), (0, 5, 0), (1, 1, 3), (8, 0, 4)])
@@ -205,10 +237,13 @@ def test_shapes_and_slices(ops):
     assert torch.equal(loss.view(-1), flat)
     loss3, dx, dw = ops.linear_cross_entropy_loss_grad(x, w, t, row_weight=torch.ones(6, 20, device="cuda"))
     assert torch.equal(loss3, loss) and dx.shape == x.shape and dw.shape == w.shape
-    only, none = ops.linear_cross_entropy_backward(torch.ones(6, 20, device="cuda"), x, w, t, lse, weight_grad=False)
-    assert none is None and torch.equal(only, dx)
-    none, only = ops.linear_cross_entropy_backward(torch.ones(6, 20, device="cuda"), x, w, t, lse, input_grad=False)
-    assert none is None and torch.equal(only, dw)
+    for call, first in ((ops.linear_cross_entropy_backward, (torch.ones(6, 20, device="cuda"), x, w, t, lse)),
+                        (ops.linear_cross_entropy_loss_grad, (x, w, t))):  # (these round dz once and twice)
+        dx, dw = call(*first)[-2:]
+        only, none = call(*first, weight_grad=False)[-2:]
+        assert none is None and torch.equal(only, dx)
+        none, only = call(*first, input_grad=False)[-2:]
+        assert none is None and torch.equal(only, dw)
     one, _ = ops.linear_cross_entropy_forward(x[2, 5], w, t[2, 5])
     assert one.shape == ()
     empty, dx, dw = ops.linear_cross_entropy_loss_grad(x[:0], w, t[:0])
