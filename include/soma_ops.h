@@ -220,7 +220,7 @@ soma_status_t soma_embedding_backward(int32_t device, const void *dy, int64_t dy
  * weight's size if that is more (512 bytes a row at least), lies in the
  * workspace, as does a copy of the rows of x that count, and of weight where
  * its rows do not start on 16-byte boundaries.  Each piece makes its logits
- * again, except that loss_grad with one piece (at most 65472 rows) keeps their
+ * again, except that loss_grad with one piece (at most 2 million rows) keeps their
  * exponentials, rounded to 16 bits, in that buffer: dz is then rounded twice.
  *
  *   forward    loss and lse (either may be NULL)

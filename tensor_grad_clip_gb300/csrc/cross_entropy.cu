@@ -35,6 +35,8 @@ struct Counted {
     int32_t rows;           // that count
     int32_t padded;         // the next multiple of 64, 64 at least: what the products run over
     float scale, unscale;   // a power of two that brings the largest |g| to about 2^14, and its inverse
+    int32_t parts;          // in which the sums of dx were made
+    uint32_t ticket;        // CTAs of the few rows' statistics that are done
 };
 
 // Row pointers are numbered by counted rows, up to Counted::padded.
@@ -49,7 +51,7 @@ struct HeadRows {
     float* z_token;         // its token's logit
 };
 
-constexpr int kSelectThreads = 1024, kSelectEach = 4;
+constexpr int kSelectEach = 4;
 
 __device__ __forceinline__ int64_t token_of(const TokenArgs& t, int64_t r) {
     const int64_t at = t.length == t.stride ? r : r / t.length * t.stride + r % t.length;
@@ -57,15 +59,18 @@ __device__ __forceinline__ int64_t token_of(const TokenArgs& t, int64_t r) {
                                     : (int64_t)__ldg(static_cast<const int*>(t.index) + at);
 }
 
-// One CTA: it has a few microseconds' work where the products have hundreds.
-__global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_constant__ HeadArgs a, HeadRows h) {
-    __shared__ int sums[32];
-    __shared__ float tops[32];
-    follow_stream();
+// Numbers the rows that count, by one CTA of kThreads; returns how many there
+// are.  kWrite: it writes what the other kernels read, and what the other
+// rows get.  here(number, row), if any, is told of each.
+template <int kThreads, bool kWrite, typename Here>
+__device__ __forceinline__ int select_rows(const HeadArgs& a, const HeadRows& h, Here&& here) {
+    constexpr int kWarps = kThreads / 32;
+    __shared__ int sums[kWarps];
+    __shared__ float tops[kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int done = 0;  // rows counted so far
     float top = 0.f;
-    for (int64_t base = 0; base < a.rows; base += kSelectThreads * kSelectEach) {
+    for (int64_t base = 0; base < a.rows; base += kThreads * kSelectEach) {
         const int64_t r0 = base + threadIdx.x * kSelectEach;
         int token[kSelectEach], mine = 0;
         float weight[kSelectEach], g[kSelectEach];
@@ -83,7 +88,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
                 g[q] *= weight[q];
                 if (isfinite(g[q])) top = fmaxf(top, fabsf(g[q]));
                 ++mine;
-            } else {
+            } else if (kWrite) {
                 h.place[r0 + q] = -1;
                 if (a.loss) a.loss[r0 + q] = 0.f;
                 if (a.lse) a.lse[r0 + q] = 0.f;
@@ -98,7 +103,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
         if (lane == 31) sums[warp] = before;
         __syncthreads();
         int total = 0, earlier = 0;
-        for (int w = 0; w < kSelectThreads / 32; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
             if (w == warp) earlier = total;
             total += sums[w];
         }
@@ -106,44 +111,52 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
 #pragma unroll
         for (int q = 0; q < kSelectEach; ++q) {
             if (token[q] < 0) continue;
-            h.row[at] = (int)(r0 + q);
-            h.place[r0 + q] = at;
-            h.token[at] = token[q];
-            h.weight[at] = weight[q];
-            h.g[at] = g[q];
-            if (a.lse_in) h.lse[at] = a.lse_in[r0 + q];
+            here(at, (int)(r0 + q));
+            if (kWrite) {
+                h.row[at] = (int)(r0 + q);
+                h.place[r0 + q] = at;
+                h.token[at] = token[q];
+                h.weight[at] = weight[q];
+                h.g[at] = g[q];
+                if (a.lse_in) h.lse[at] = a.lse_in[r0 + q];
+            }
             ++at;
         }
         done += total;
         __syncthreads();
     }
+    if constexpr (kWrite) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) tops[warp] = top;
-    __syncthreads();
-    const int padded = max(64, (done + 63) / 64 * 64);
-    for (int i = done + threadIdx.x; i < padded; i += kSelectThreads) {
-        h.row[i] = h.token[i] = -1;
-        h.weight[i] = h.g[i] = h.lse[i] = 0.f;
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (lane == 0) tops[warp] = top;
+        __syncthreads();
+        const int padded = max(64, (done + 63) / 64 * 64);
+        for (int i = done + threadIdx.x; i < padded; i += kThreads) {
+            h.row[i] = h.token[i] = -1;
+            h.weight[i] = h.g[i] = h.lse[i] = 0.f;
+        }
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < kWarps; ++w) top = fmaxf(top, tops[w]);
+            int e = 0;
+            if (top > 0.f) frexpf(top, &e);
+            e = min(max(14 - e, -100), 100);
+            *h.counted = {done, padded, ldexpf(1.f, e), ldexpf(1.f, -e), 1, 0};
+        }
     }
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < kSelectThreads / 32; ++w) top = fmaxf(top, tops[w]);
-        int e = 0;
-        if (top > 0.f) frexpf(top, &e);
-        e = min(max(14 - e, -100), 100);
-        *h.counted = {done, padded, ldexpf(1.f, e), ldexpf(1.f, -e)};
-    }
+    return done;
 }
 
-// The counted rows of x, and zeros in the padding: a warp copies 32 vectors.
-template <typename T>
-__global__ void __launch_bounds__(256) gather_kernel(const T* x, int64_t stride, int64_t rows, int32_t cols, T* out,
-                                                     int64_t out_stride, HeadRows h, int pieces) {
+// One CTA: it has a few microseconds' work where the products have hundreds.
+constexpr int kSelectThreads = 1024;
+__global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_constant__ HeadArgs a, HeadRows h) {
     follow_stream();
-    const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int to = (int)(item / pieces), i = (int)(item - (int64_t)to * pieces) * 32 + (threadIdx.x & 31);
-    if (to >= h.counted->padded || i * 8 >= cols) return;
-    const int from = h.row[to];
+    select_rows<kSelectThreads, true>(a, h, [](int, int) {});
+}
+
+// Vector i of a counted row of x (from < 0: of the padding), to its place.
+template <typename T>
+__device__ __forceinline__ void gather_vector(const T* x, int64_t stride, int64_t rows, int32_t cols, T* out,
+                                              int64_t out_stride, int from, int to, int i) {
     uint4 v = make_uint4(0, 0, 0, 0);
     if (from >= 0) {
         const RowReader<T, false> row(x, stride, rows, from, cols);
@@ -159,14 +172,48 @@ __global__ void __launch_bounds__(256) gather_kernel(const T* x, int64_t stride,
     reinterpret_cast<uint4*>(out + to * out_stride)[i] = v;
 }
 
+// Both in one launch, for rows that one pass of a CTA counts: every CTA counts
+// them and copies its share.
+constexpr int kFewThreads = 256, kFewRows = kFewThreads * kSelectEach;
+template <typename T>
+__global__ void __launch_bounds__(kFewThreads) select_few_kernel(const __grid_constant__ HeadArgs a, HeadRows h, T* out,
+                                                                 int64_t out_stride, int pieces) {
+    __shared__ int row[kFewRows];
+    follow_stream();
+    auto here = [&](int number, int r) { row[number] = r; };
+    const int count = blockIdx.x == 0 ? select_rows<kFewThreads, true>(a, h, here) : select_rows<kFewThreads, false>(a, h, here);
+    __syncthreads();
+    const int padded = max(64, (count + 63) / 64 * 64), warps = gridDim.x * (kFewThreads / 32);
+    for (int item = blockIdx.x * (kFewThreads / 32) + (threadIdx.x >> 5); item < padded * pieces; item += warps) {
+        const int to = item / pieces, i = (item - to * pieces) * 32 + (threadIdx.x & 31);
+        if (i * 8 < a.k)
+            gather_vector<T>(static_cast<const T*>(a.x), a.x_stride, a.rows, a.k, out, out_stride, to < count ? row[to] : -1,
+                             to, i);
+    }
+}
+
+// The counted rows of x, and zeros in the padding: a warp copies 32 vectors.
+template <typename T>
+__global__ void __launch_bounds__(256) gather_kernel(const T* x, int64_t stride, int64_t rows, int32_t cols, T* out,
+                                                     int64_t out_stride, HeadRows h, int pieces) {
+    follow_stream();
+    const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int to = (int)(item / pieces), i = (int)(item - (int64_t)to * pieces) * 32 + (threadIdx.x & 31);
+    if (to >= h.counted->padded || i * 8 >= cols) return;
+    gather_vector<T>(x, stride, rows, cols, out, out_stride, h.row[to], to, i);
+}
+
 // ---- logits -------------------------------------------------------------------
 
 struct LogitArgs {
     CUtensorMap a, b, out;
     HeadRows h;
-    float2* parts;          // [rows][slices of 32 columns] maximum and sum of exponentials
-    int64_t slices;
+    float2* parts;          // maximum and sum of exponentials of row r's slice q of 32 columns, at
+    int64_t pitch, step;    //   q * pitch + r * step
     bool keep;              // stats: store the exponentials too
+    int32_t columns;        // stats: of narrow tiles, or 0
+    float *loss, *lse;      // stats of few rows: what the last CTA writes (either may be nullptr)
+    bool join;
     int32_t n, k;           // columns (of the piece), their first in the vocabulary, sum length
     int32_t first;
     int32_t tiles_n, strip;
@@ -175,8 +222,9 @@ struct LogitArgs {
 // Rows of tiles, and where halves begin so that a last wave that at most half
 // of the workers have is done by all.
 template <int CG>
-__device__ __forceinline__ TilePlan plan_rows(int rows, int k, int tiles_n, int strip, bool halves, int splits) {
-    TilePlan p{rows, k, (rows + kBM * CG - 1) / (kBM * CG), tiles_n, strip, 0, splits};
+__device__ __forceinline__ TilePlan plan_rows(int rows, int k, int tiles_n, int strip, bool halves, int splits = 1,
+                                              int chunk = kOneChunk) {
+    TilePlan p{rows, k, (rows + kBM * CG - 1) / (kBM * CG), tiles_n, strip, 0, splits, chunk};
     const int tiles = p.tiles_m * tiles_n, workers = (int)gridDim.x / CG, rest = tiles % workers;
     p.whole = halves && CG == 2 && splits == 1 && 2 * rest <= workers ? tiles - rest : tiles;
     return p;
@@ -201,102 +249,190 @@ __device__ __forceinline__ void load_logits(uint32_t acc, int col, int n, float 
 template <typename T>
 constexpr float kKeepScale = kIsBf16<T> ? 1.f : 16384.f;
 
-template <int CG, int BN, typename T>
-__global__ void __launch_bounds__(kTileThreads, 1) stats_kernel(const __grid_constant__ LogitArgs p) {
-    tile_products<CG, BN, T>(
-        &p.a, &p.b, true, true,
-        [&] { return plan_rows<CG>(p.h.counted->padded, p.k, p.tiles_n, p.strip, true, 1); },
-        [&](uint32_t acc, int row0, int col0, int cols, int, const TilePlan&, char* staging) {
-            const int row = row0 + (threadIdx.x & 31);
-            const int at = p.h.token[row] - col0;  // the token's column here
-            Stager<T> stager{staging + (threadIdx.x >> 5) * kStagerBytes, row0, 0, p.n};
-            for (int c = 0; c < cols && col0 + c < p.n; c += 32) {
-                float z[32];
-                load_logits(acc + c, col0 + c, p.n, z);
-                float m = kLowest;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) m = fmaxf(m, z[i]);
-                const int d = at - c;
-                if (__any_sync(0xffffffffu, d >= 0 && d < 32) && d >= 0 && d < 32) {
-                    float t = z[0];
-#pragma unroll
-                    for (int i = 1; i < 32; ++i) t = d == i ? z[i] : t;
-                    p.h.z_token[row] = t;
-                }
-                float even = 0.f, odd = 0.f;
-#pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    z[i] = exp2_fast((z[i] - m) * kLog2e);
-                    z[i + 1] = exp2_fast((z[i + 1] - m) * kLog2e);
-                    even += z[i];
-                    odd += z[i + 1];
-                }
-                p.parts[row * p.slices + (col0 + c) / 32] = make_float2(m, even + odd);
-                if (p.keep) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) z[i] *= kKeepScale<T>;
-                    stager.store(z, col0 + c, &p.out, true, nullptr, 0);
-                }
-            }
-        });
-}
-
 __device__ __forceinline__ float2 join_stats(float2 a, float2 b) {
     const float m = fmaxf(a.x, b.x);
     return make_float2(m, a.y * exp2_fast((a.x - m) * kLog2e) + b.y * exp2_fast((b.x - m) * kLog2e));
 }
 
-// Log-sum-exp and loss of a counted row per CTA.
-constexpr int kJoinWarps = 4;
-__global__ void __launch_bounds__(32 * kJoinWarps) stats_join_kernel(const float2* parts, int64_t slices, HeadRows h,
-                                                                     float* loss, float* lse) {
-    __shared__ float2 sums[kJoinWarps];
-    follow_stream();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = blockIdx.x;
-    if (i >= h.counted->rows) return;
+// Joins parts q, q + step, ... of what `at` points to, eight reads at a time.
+__device__ __forceinline__ float2 join_parts(const float2* at, int64_t pitch, int q, int step, int count) {
     float2 own = make_float2(kLowest, 0.f);
-#pragma unroll 8
-    for (int64_t q = threadIdx.x; q < slices; q += 32 * kJoinWarps) own = join_stats(own, __ldcg(parts + i * slices + q));
+    for (; q < count; q += 8 * step) {
+        float2 v[8];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        own = join_stats(own, make_float2(__shfl_xor_sync(0xffffffffu, own.x, o), __shfl_xor_sync(0xffffffffu, own.y, o)));
-    if (lane == 0) sums[warp] = own;
-    __syncthreads();
-    if (threadIdx.x) return;
-    for (int w = 1; w < kJoinWarps; ++w) own = join_stats(own, sums[w]);
-    const float log_s = logf(own.y), total = own.x + log_s;
+        for (int k = 0; k < 8; ++k) v[k] = q + k * step < count ? __ldcg(at + (q + k * step) * pitch) : make_float2(kLowest, 0.f);
+        float m = own.x;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m = fmaxf(m, v[k].x);
+        float s = own.y * exp2_fast((own.x - m) * kLog2e);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s += v[k].y * exp2_fast((v[k].x - m) * kLog2e);
+        own = make_float2(m, s);
+    }
+    return own;
+}
+
+// A counted row's loss and log-sum-exp.
+__device__ __forceinline__ void write_loss(const HeadRows& h, int i, float2 sum, float* loss, float* lse) {
+    const float log_s = logf(sum.y), total = sum.x + log_s;
     const int r = h.row[i];
     h.lse[i] = total;
     if (lse) lse[r] = total;
     // (m - z) + log s: near 0 it keeps its digits where lse - z would not
-    if (loss) loss[r] = h.weight[i] * ((own.x - h.z_token[i]) + log_s);
+    if (loss) loss[r] = h.weight[i] * ((sum.x - __ldcg(h.z_token + i)) + log_s);
 }
 
-// dz of the kept exponentials, in place: a thread 8 of them.  What rounding
-// them once more costs is at most another half step of 16 bits; the token's
-// own element, a difference from 1, is made of its logit.
-template <typename T>
-__global__ void __launch_bounds__(256) keep_kernel(T* dz, int64_t stride, const float2* parts, int64_t slices, HeadRows h,
-                                                   int32_t n) {
-    follow_stream();
-    const int row = blockIdx.y;
-    if (row >= h.counted->padded) return;
-    const int c = ((int)blockIdx.x * 256 + (int)threadIdx.x) * 8;
-    if (c >= n) return;
-    const float lse = h.lse[row], g = h.g[row] * h.counted->scale;
-    const float f = g * (1.f / kKeepScale<T>) * exp2_fast((__ldg(&parts[row * slices + c / 32].x) - lse) * kLog2e);
-    uint4* at = reinterpret_cast<uint4*>(dz + row * stride + c);
-    float x[8];
-    widen16(*at, x, T{});
+// A tensor core drops the last bits of a long sum's every step.  The loss is
+// an fp32 number, so its logits are summed in chunks of 1024 products that are
+// added in registers: at k = 4096 the loss errs by 3.6e-7 (fp32 products: 4.5e-7)
+// instead of 1.6e-6, for 4 % of 8192 x 32000 x 4096's time; chunks of 512 err by
+// 1.7e-7 for 7 %, of 2048 by 7.8e-7.
+constexpr int kLogitChunk = 1024 / kBK;
+
+template <int CG, int BN, typename T>
+__global__ void __launch_bounds__(kTileThreads, 1) stats_kernel(const __grid_constant__ LogitArgs p) {
+    constexpr int kCols = BN / (kEpilogueWarps / 4);  // of a warp, at most
+    float z[kCols];
+    tile_products<CG, BN, T>(
+        &p.a, &p.b, true, true,
+        [&] { return plan_rows<CG>(p.h.counted->padded, p.k, p.tiles_n, p.strip, p.columns == 0, 1, kLogitChunk); },
+        [&](uint32_t acc, const Part& part, char* staging, auto&& done) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] *= f;
-    const int d = h.token[row] - c;
-    if (d >= 0 && d < 8) {
-        const float own = g * (exp2_fast((h.z_token[row] - lse) * kLog2e) - 1.f);
+            for (int c = 0; c < kCols; c += 16) {
+                if (c >= part.cols) break;
+                uint32_t raw[16];
+                tmem_ld16(acc + c, raw);
+                tmem_ld_wait(raw);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = d == i ? own : x[i];
+                for (int i = 0; i < 16; ++i) z[c + i] = part.first ? __uint_as_float(raw[i]) : z[c + i] + __uint_as_float(raw[i]);
+            }
+            done();
+            if (!part.last) return;
+            const int row = part.row0 + (threadIdx.x & 31);
+            const int at = p.h.token[row] - part.col0;  // the token's column here
+            Stager<T> stager{staging + (threadIdx.x >> 5) * kStagerBytes, part.row0, 0, p.n};
+#pragma unroll
+            for (int c = 0; c < kCols; c += 32) {
+                const int col = part.col0 + c;
+                if (c >= part.cols || col >= p.n) break;
+                float (&x)[32] = *reinterpret_cast<float (*)[32]>(z + c);
+                if (col + 32 > p.n) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (col + i >= p.n) x[i] = -INFINITY;
+                }
+                float m = kLowest;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) m = fmaxf(m, x[i]);
+                const int d = at - c;
+                if (__any_sync(0xffffffffu, d >= 0 && d < 32) && d >= 0 && d < 32) {
+                    float t = x[0];
+#pragma unroll
+                    for (int i = 1; i < 32; ++i) t = d == i ? x[i] : t;
+                    p.h.z_token[row] = t;
+                }
+                float even = 0.f, odd = 0.f;
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    x[i] = exp2_fast((x[i] - m) * kLog2e);
+                    x[i + 1] = exp2_fast((x[i + 1] - m) * kLog2e);
+                    even += x[i];
+                    odd += x[i + 1];
+                }
+                p.parts[col / 32 * p.pitch + row * p.step] = make_float2(m, even + odd);
+                if (p.keep) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[i] *= kKeepScale<T>;
+                    stager.store(x, col, &p.out, true, nullptr, 0);
+                }
+            }
+        },
+        p.columns);
+    if (!p.join) return;
+    // Few rows: the last CTA to finish joins the slices, a warp a row, which
+    // saves a launch.
+    __shared__ bool last;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) last = atomicAdd(&p.h.counted->ticket, 1u) == gridDim.x - 1;
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    const int slices = (p.n + 31) / 32, lane = threadIdx.x & 31;
+    for (int i = threadIdx.x >> 5; i < p.h.counted->rows; i += kTileThreads / 32) {
+        float2 own = join_parts(p.parts + i * p.step, p.pitch, lane, 32, slices);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            own = join_stats(own, make_float2(__shfl_xor_sync(0xffffffffu, own.x, o), __shfl_xor_sync(0xffffffffu, own.y, o)));
+        if (lane == 0) write_loss(p.h, i, own, p.loss, p.lse);
     }
-    *at = narrow16(x, T{});
+}
+
+constexpr int kJoinedRows = 16;  // about one for each warp of the last CTA
+
+// Log-sum-exp and loss of 8 counted rows per CTA, or of 4 where rows are few:
+// kRows lanes take neighbouring rows, the others slices in turn.
+constexpr int kJoinThreads = 512;
+template <int kRows>
+__global__ void __launch_bounds__(kJoinThreads) stats_join_kernel(const float2* parts, int64_t pitch, int slices, HeadRows h,
+                                                                  float* loss, float* lse) {
+    constexpr int kTurns = kJoinThreads / kRows;
+    __shared__ float2 sums[kTurns][kRows];
+    follow_stream();
+    const int at = threadIdx.x % kRows, turn = threadIdx.x / kRows, i = blockIdx.x * kRows + at;
+    if ((int)blockIdx.x * kRows >= h.counted->rows) return;
+    float2 own = join_parts(parts + i, pitch, turn, kTurns, slices);
+    sums[turn][at] = own;
+    __syncthreads();
+    for (int o = kTurns / 2; o > 0; o /= 2) {
+        if (turn < o) sums[turn][at] = own = join_stats(own, sums[turn + o][at]);
+        __syncthreads();
+    }
+    if (turn || i >= h.counted->rows) return;
+    write_loss(h, i, own, loss, lse);
+}
+
+// dz of the kept exponentials, in place: a CTA 32 rows of 256 columns.  What
+// rounding them once more costs is at most another half step of 16 bits; the
+// token's own element, a difference from 1, is made of its logit.
+constexpr int kKeepRows = 32, kKeepCols = 256;
+template <typename T>
+__global__ void __launch_bounds__(256) keep_kernel(T* dz, int64_t stride, const float2* parts, int64_t pitch, HeadRows h,
+                                                   int32_t n) {
+    __shared__ float factor[kKeepCols / 32][kKeepRows];
+    follow_stream();
+    const int row0 = blockIdx.y * kKeepRows, col0 = blockIdx.x * kKeepCols;
+    if (row0 >= h.counted->padded) return;
+    {
+        const int r = threadIdx.x % kKeepRows, q = threadIdx.x / kKeepRows;
+        if (col0 + 32 * q < n)
+            factor[q][r] = h.g[row0 + r] * h.counted->scale * (1.f / kKeepScale<T>) *
+                           exp2_fast((__ldcs(&parts[(col0 / 32 + q) * pitch + row0 + r].x) - h.lse[row0 + r]) * kLog2e);
+    }
+    __syncthreads();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = col0 + lane * 8;
+    if (c >= n) return;
+    uint4 v[kKeepRows / 8];
+    T* at = dz + (int64_t)(row0 + warp) * stride + c;
+#pragma unroll
+    for (int k = 0; k < kKeepRows / 8; ++k) v[k] = *reinterpret_cast<const uint4*>(at + 8 * k * stride);
+#pragma unroll
+    for (int k = 0; k < kKeepRows / 8; ++k) {
+        const int r = warp + 8 * k, row = row0 + r;
+        const float f = factor[lane / 4][r];
+        float x[8];
+        widen16(v[k], x, T{});
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] *= f;
+        const int d = h.token[row] - c;
+        if (d >= 0 && d < 8) {
+            const float own =
+                h.g[row] * h.counted->scale * (exp2_fast((h.z_token[row] - h.lse[row]) * kLog2e) - 1.f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = d == i ? own : x[i];
+        }
+        *reinterpret_cast<uint4*>(at + 8 * k * stride) = narrow16(x, T{});
+    }
 }
 
 // dz of a piece, scaled.
@@ -304,9 +440,9 @@ template <int CG, int BN, typename T>
 __global__ void __launch_bounds__(kTileThreads, 1) dz_kernel(const __grid_constant__ LogitArgs p) {
     tile_products<CG, BN, T>(
         &p.a, &p.b, true, true,
-        [&] { return plan_rows<CG>(p.h.counted->padded, p.k, p.tiles_n, p.strip, true, 1); },
-        [&](uint32_t acc, int row0, int col0, int cols, int, const TilePlan&, char* staging) {
-            const int row = row0 + (threadIdx.x & 31);
+        [&] { return plan_rows<CG>(p.h.counted->padded, p.k, p.tiles_n, p.strip, true); },
+        [&](uint32_t acc, const Part& part, char* staging, auto&& done) {
+            const int row0 = part.row0, col0 = part.col0, cols = part.cols, row = row0 + (threadIdx.x & 31);
             const int at = p.h.token[row] - p.first - col0;
             const float lse = p.h.lse[row], g = p.h.g[row] * p.h.counted->scale;
             Stager<T> stager{staging + (threadIdx.x >> 5) * kStagerBytes, row0, 0, p.n};
@@ -324,6 +460,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) dz_kernel(const __grid_consta
                 }
                 stager.store(z, col0 + c, &p.out, true, nullptr, 0);
             }
+            done();
         });
 }
 
@@ -332,22 +469,24 @@ __global__ void __launch_bounds__(kTileThreads, 1) dz_kernel(const __grid_consta
 struct GradArgs {
     CUtensorMap a, b, out;
     HeadRows h;
-    float* sums;            // dx: [splits][pitch rows][sums_stride]
+    float* sums;            // dx: [parts][pitch rows][sums_stride]
     int64_t pitch, sums_stride;
     bool add;               // dx: to what is there
     void* dweight;          // its piece
     int64_t dweight_stride;
     bool tma_out;
     int32_t m, n, k;        // dweight: m; dx: k (the others are the device's)
-    int32_t tiles_m, tiles_n, strip, splits;
+    int32_t tiles_m, tiles_n, strip;
+    int32_t first_k, most_parts;  // dx: the first piece's k
 };
 
 template <int CG, int BN, typename T>
 __global__ void __launch_bounds__(kTileThreads, 1) dweight_kernel(const __grid_constant__ GradArgs p) {
     tile_products<CG, BN, T>(
         &p.a, &p.b, false, false,
-        [&] { return plan_rows<CG>(p.m, p.h.counted->padded, p.tiles_n, p.strip, true, 1); },
-        [&](uint32_t acc, int row0, int col0, int cols, int, const TilePlan&, char* staging) {
+        [&] { return plan_rows<CG>(p.m, p.h.counted->padded, p.tiles_n, p.strip, true); },
+        [&](uint32_t acc, const Part& part, char* staging, auto&& done) {
+            const int row0 = part.row0, col0 = part.col0, cols = part.cols;
             const float unscale = p.h.counted->unscale;
             Stager<T> stager{staging + (threadIdx.x >> 5) * kStagerBytes, row0, p.m, p.n};
             for (int c = 0; c < cols && col0 + c < p.n; c += 32) {
@@ -359,7 +498,28 @@ __global__ void __launch_bounds__(kTileThreads, 1) dweight_kernel(const __grid_c
                 for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(raw[i]) * unscale;
                 stager.store(x, col0 + c, &p.out, p.tma_out, static_cast<T*>(p.dweight), p.dweight_stride);
             }
+            done();
         });
+}
+
+// Parts in which dx's long sums are made side by side, at most `most`: its
+// tiles are few, and parts fill the last wave, or the only one.  In units of a
+// pipeline stage (0.36 us), a wave takes its share of k and four stages more;
+// a part of m rows is written and read once.
+template <int CG, int BN>
+__device__ __forceinline__ int parts_of(int rows, int tiles_n, int k, int most) {
+    const int tiles = (rows + kBM * CG - 1) / (kBM * CG) * tiles_n, workers = (int)gridDim.x / CG, kts = (k + kBK - 1) / kBK;
+    const float traffic = (float)tiles * (kBM * CG * BN * 8 / 2.4e6f);  // of a part: 2.4 MB in a stage's time
+    int best = 1;
+    float least = 0.f;
+    for (int s = 1; s <= most; ++s) {
+        const float time = (float)((tiles * s + workers - 1) / workers) * ((float)kts / s + 4.f) + (s > 1 ? s * traffic : 0.f);
+        if (s == 1 || time < least) {
+            least = time;
+            best = s;
+        }
+    }
+    return best;
 }
 
 // A lane's row of 32 sums, 32 bytes at a time (rows of sums start on 32-byte boundaries).
@@ -388,9 +548,15 @@ template <int CG, int BN, typename T>
 __global__ void __launch_bounds__(kTileThreads, 1) dx_kernel(const __grid_constant__ GradArgs p) {
     tile_products<CG, BN, T>(
         &p.a, &p.b, true, false,
-        [&] { return plan_rows<CG>(p.h.counted->padded, p.k, p.tiles_n, p.strip, true, p.splits); },
-        [&](uint32_t acc, int row0, int col0, int cols, int split, const TilePlan&, char*) {
-            float* to = p.sums + (split * p.pitch + row0 + (threadIdx.x & 31)) * p.sums_stride;
+        [&] {
+            // (every piece has the first one's parts; a last piece with less than a stage for each adds to the first)
+            const int rows = p.h.counted->padded, parts = parts_of<CG, BN>(rows, p.tiles_n, p.first_k, p.most_parts);
+            if (!p.add && blockIdx.x == 0 && threadIdx.x == 0) p.h.counted->parts = parts;
+            return plan_rows<CG>(rows, p.k, p.tiles_n, p.strip, true, (p.k + kBK - 1) / kBK >= parts ? parts : 1);
+        },
+        [&](uint32_t acc, const Part& part, char*, auto&& done) {
+            const int row0 = part.row0, col0 = part.col0, cols = part.cols;
+            float* to = p.sums + (part.split * p.pitch + row0 + (threadIdx.x & 31)) * p.sums_stride;
             // (the sums' rows are as long as whole tiles)
             for (int c = 0; c < cols && col0 + c < p.n; c += 32) {
                 uint32_t raw[32];
@@ -398,14 +564,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) dx_kernel(const __grid_consta
                 tmem_ld_wait(raw);
                 add_or_store(to + col0 + c, raw, p.add);
             }
+            done();
         });
 }
 
 // dx of all rows: the sums of the parts, unscaled and rounded; 0 for rows that
 // do not count.
 template <typename T>
-__global__ void __launch_bounds__(256) dx_round_kernel(const float* sums, int64_t pitch, int64_t sums_stride, int splits,
-                                                       HeadRows h, T* dx, int64_t dx_stride, int64_t rows, int32_t cols,
+__global__ void __launch_bounds__(256) dx_round_kernel(const float* sums, int64_t pitch, int64_t sums_stride, HeadRows h, T* dx, int64_t dx_stride, int64_t rows, int32_t cols,
                                                        int pieces) {
     follow_stream();
     const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -415,7 +581,7 @@ __global__ void __launch_bounds__(256) dx_round_kernel(const float* sums, int64_
     const int at = h.place[r];
     float x[8] = {};
     if (at >= 0) {
-        for (int s = 0; s < splits; ++s) {
+        for (int s = 0; s < h.counted->parts; ++s) {
             const float4* from = reinterpret_cast<const float4*>(sums + (s * pitch + at) * sums_stride + c);
             const float4 u = __ldcs(from), v = __ldcs(from + 1);
             x[0] += u.x; x[1] += u.y; x[2] += u.z; x[3] += u.w;
@@ -448,7 +614,7 @@ struct HeadLayout {
     int64_t pitch;                   // rows, rounded up to whole tiles
     int64_t x_stride, w_stride, sums_stride;
     int64_t piece, pieces;           // columns of the vocabulary
-    int32_t splits;                  // parts of the vocabulary in which dx is summed side by side
+    int32_t most_parts;              // in which dx may be summed side by side
     bool big;                        // tiles on pairs of SMs
     HeadLayout(int64_t rows, int64_t vocab, int64_t k, bool copy_weight, bool forward, bool dx, bool dweight, int sms) {
         pitch = (rows + 255) / 256 * 256;
@@ -462,20 +628,10 @@ struct HeadLayout {
         pieces = (vocab + most - 1) / most;
         piece = ((vocab + pieces - 1) / pieces + 255) / 256 * 256;
         pieces = (vocab + piece - 1) / piece;
-        // dx has few tiles and long sums: parts of the sums make the last wave
-        // full, or the only one.  (A part more costs its share of writing and
-        // reading the sums, about as much as four of its pipeline stages.)
-        const int64_t edge = big ? 256 : 128, workers = big ? pairs : sms, kts = std::min(piece, vocab) / kBK + 1;
+        // room for twice as many parts as fill a wave, each of 16 stages or more
+        const int64_t edge = big ? 256 : 128, workers = big ? pairs : sms, kts = (std::min(piece, vocab) + kBK - 1) / kBK;
         const int64_t tiles = (rows + edge - 1) / edge * ((k + edge - 1) / edge);
-        splits = 1;
-        double least = 0;
-        for (int s = 1; s <= 16 && kts >= 16 * s && tiles <= 4 * workers; ++s) {
-            const double time = (double)((tiles * s + workers - 1) / workers) * ((double)kts / s + 4) + 0.05 * kts * (s > 1);
-            if (s == 1 || time < least) {
-                least = time;
-                splits = s;
-            }
-        }
+        most_parts = (int32_t)std::max<int64_t>(1, std::min(std::min<int64_t>(16, kts / 16), 2 * workers / tiles));
         x_stride = (k + 7) / 8 * 8;
         w_stride = x_stride;
         sums_stride = (k + 255) / 256 * 256;
@@ -493,7 +649,7 @@ struct HeadLayout {
         w = take(copy_weight ? vocab * w_stride * 2 : 0);
         parts = take(forward ? pitch * slices(vocab) * 8 : 0);
         dz = take(dx || dweight ? pitch * piece * 2 : 0);
-        sums = take(dx ? splits * pitch * sums_stride * 4 : 0);
+        sums = take(dx ? most_parts * pitch * sums_stride * 4 : 0);
         bytes = at;
     }
     static int64_t slices(int64_t vocab) { return (vocab + 31) / 32; }
@@ -536,41 +692,73 @@ struct Head {
         if (units > (1 << 29)) return cudaErrorInvalidValue;
         return launch_cluster(kernel, args, grid(units), kTileThreads, S::kSmem, CG, stream);
     }
-    // z = x W^T over columns [first, first + n) of the vocabulary.
-    int logits(LogitArgs& p, int64_t first, int64_t n, const void* kernel) const {
+    // z = x W^T over columns [first, first + n) of the vocabulary, in tiles of `width` columns.
+    int logits(LogitArgs& p, int64_t first, int64_t n, int width) const {
         p.h = h;
-        p.slices = HeadLayout::slices(a.vocab);
+        p.pitch = at.pitch;
+        p.step = 1;
         p.n = (int32_t)n;
         p.k = a.k;
         p.first = (int32_t)first;
-        p.tiles_n = (int32_t)((n + BN - 1) / BN);
-        p.strip = strip_of(p.tiles_n, BN, a.k);
+        p.tiles_n = (int32_t)((n + width - 1) / width);
+        p.strip = strip_of(p.tiles_n, width, a.k);
         const char* b = static_cast<const char*>(w) + first * w_stride * 2;
         if (const int e = make_map(&p.a, a.dtype, ws + at.x, at.x_stride, at.pitch, a.k, kBM)) return e;
-        if (const int e = make_map(&p.b, a.dtype, b, w_stride, n, a.k, S::kRowsB)) return e;
-        void* args[] = {&p};
-        // (half tiles make at most twice as many units)
-        return tiles(kernel, rows_of_tiles(a.rows) * p.tiles_n * 2, args);
+        return make_map(&p.b, a.dtype, b, w_stride, n, a.k, width / CG);
     }
     int forward(bool keep) const {
         LogitArgs p{};
         p.parts = reinterpret_cast<float2*>(ws + at.parts);
         p.keep = keep;
-        int e = keep ? make_map(&p.out, a.dtype, ws + at.dz, at.piece, at.pitch, a.vocab, 32, 32) : cudaSuccess;
-        if (!e) e = logits(p, 0, a.vocab, (const void*)stats_kernel<CG, BN, T>);
+        if (keep)
+            if (const int e = make_map(&p.out, a.dtype, ws + at.dz, at.piece, at.pitch, a.vocab, 32, 32)) return e;
+        void* args[] = {&p};
+        int e;
+        if (a.rows <= kBM) {
+            // One row of tiles: reading the weight is what takes time, and tiles of
+            // one width, at most 256, fill whole waves of SMs (32000 tokens: 143
+            // tiles of 224 columns, not 250 of 128 in a wave and two thirds).
+            const int64_t waves = (((int64_t)a.vocab + 255) / 256 + sms - 1) / sms;
+            p.columns = (int32_t)(((a.vocab + waves * sms - 1) / (waves * sms) + 31) / 32 * 32);
+            p.join = a.rows <= kJoinedRows;
+            p.loss = a.loss;
+            p.lse = a.lse;
+            e = Head<1, 256, T>{a, at, h, ws, w, w_stride, sms, stream}.logits(p, 0, a.vocab, p.columns);
+            if (p.join && !keep) {  // a row's parts side by side
+                p.pitch = 1;
+                p.step = HeadLayout::slices(a.vocab);
+            }
+            if (!e)
+                e = launch_cluster((const void*)stats_kernel<1, 256, T>, args, std::min<int64_t>(p.tiles_n, sms),
+                                   kTileThreads, TileShape<1, 256>::kSmem, 1, stream);
+        } else {
+            e = logits(p, 0, a.vocab, BN);
+            // (half tiles make at most twice as many units)
+            if (!e) e = tiles((const void*)stats_kernel<CG, BN, T>, rows_of_tiles(a.rows) * p.tiles_n * 2, args);
+        }
         if (e) return e;
         const float2* parts = p.parts;
-        int64_t slices = p.slices, stride = at.piece;
+        int64_t pitch = at.pitch, stride = at.piece;
         HeadRows rows = h;
-        float *loss = a.loss, *lse = a.lse;
-        void* args[] = {&parts, &slices, &rows, &loss, &lse};
-        e = launch_after((const void*)stats_join_kernel, dim3((unsigned)a.rows), 32 * kJoinWarps, args, stream);
+        if (!p.join) e = join(parts);
         if (e || !keep) return e;
         T* dz = reinterpret_cast<T*>(ws + at.dz);
         int32_t n = a.vocab;
-        void* keep_args[] = {&dz, &stride, &parts, &slices, &rows, &n};
-        return launch_after((const void*)keep_kernel<T>, dim3((a.vocab + 2047) / 2048, (unsigned)std::max<int64_t>(64, (a.rows + 63) / 64 * 64)),
-                            256, keep_args, stream);
+        void* keep_args[] = {&dz, &stride, &parts, &pitch, &rows, &n};
+        const unsigned padded = (unsigned)std::max<int64_t>(64, (a.rows + 63) / 64 * 64);
+        return launch_after((const void*)keep_kernel<T>, dim3((a.vocab + kKeepCols - 1) / kKeepCols, padded / kKeepRows), 256,
+                            keep_args, stream);
+    }
+    int join(const float2* parts) const {
+        int64_t pitch = at.pitch;
+        int slices = (int)HeadLayout::slices(a.vocab);
+        HeadRows rows = h;
+        float *loss = a.loss, *lse = a.lse;
+        void* join_args[] = {&parts, &pitch, &slices, &rows, &loss, &lse};
+        // (few rows: 4 per CTA, a sector of each slice)
+        const bool few = a.rows <= 1024;
+        return launch_after(few ? (const void*)stats_join_kernel<4> : (const void*)stats_join_kernel<8>,
+                            dim3((unsigned)((a.rows + (few ? 3 : 7)) / (few ? 4 : 8))), kJoinThreads, join_args, stream);
     }
     int gradients(bool kept) const {
         for (int64_t first = 0; first < a.vocab; first += at.piece) {
@@ -579,7 +767,9 @@ struct Head {
             if (!kept) {
                 LogitArgs p{};
                 e = make_map(&p.out, a.dtype, ws + at.dz, at.piece, at.pitch, n, 32, 32);
-                if (!e) e = logits(p, first, n, (const void*)dz_kernel<CG, BN, T>);
+                void* args[] = {&p};
+                if (!e) e = logits(p, first, n, BN);
+                if (!e) e = tiles((const void*)dz_kernel<CG, BN, T>, rows_of_tiles(a.rows) * p.tiles_n * 2, args);
             }
             if (!e && a.dweight) e = dweight(first, n);
             if (!e && a.dx) e = dx(first, n);
@@ -588,11 +778,11 @@ struct Head {
         if (!a.dx) return cudaSuccess;
         const float* sums = reinterpret_cast<const float*>(ws + at.sums);
         int64_t pitch = at.pitch, sums_stride = at.sums_stride, stride = a.dx_stride, rows = a.rows;
-        int splits = at.splits, pieces = (a.k + 255) / 256;
+        int pieces = (a.k + 255) / 256;
         int32_t cols = a.k;
         HeadRows hr = h;
         T* out = static_cast<T*>(a.dx);
-        void* args[] = {&sums, &pitch, &sums_stride, &splits, &hr, &out, &stride, &rows, &cols, &pieces};
+        void* args[] = {&sums, &pitch, &sums_stride, &hr, &out, &stride, &rows, &cols, &pieces};
         const int64_t grid = (rows * pieces + 7) / 8;
         if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
         return launch_after((const void*)dx_round_kernel<T>, dim3((unsigned)grid), 256, args, stream);
@@ -625,15 +815,15 @@ struct Head {
         p.add = first > 0;
         p.n = a.k;
         p.k = (int32_t)n;
-        // (a last piece that has less than a stage for each part is added to the first part's sums)
-        p.splits = (n + kBK - 1) / kBK >= at.splits ? at.splits : 1;
+        p.first_k = (int32_t)std::min<int64_t>(at.piece, a.vocab);
+        p.most_parts = at.most_parts;
         p.tiles_n = (a.k + BN - 1) / BN;
         p.strip = strip_of(p.tiles_n, BN, n);
         const char* b = static_cast<const char*>(w) + first * w_stride * 2;
         if (const int e = make_map(&p.a, a.dtype, ws + at.dz, at.piece, at.pitch, n, kBM)) return e;
         if (const int e = make_map(&p.b, a.dtype, b, w_stride, n, a.k, kBK)) return e;
         void* args[] = {&p};
-        return tiles((const void*)dx_kernel<CG, BN, T>, rows_of_tiles(a.rows) * p.tiles_n * p.splits * 2, args);
+        return tiles((const void*)dx_kernel<CG, BN, T>, rows_of_tiles(a.rows) * p.tiles_n * std::max(2, p.most_parts), args);
     }
 };
 
@@ -662,27 +852,32 @@ int launch_head(const HeadArgs& a, bool forward, void* workspace, int sm_count, 
         w = ws + at.w;
         w_stride = at.w_stride;
     }
-    {
-        HeadArgs copy_of = a;
-        void* args[] = {&copy_of, &h};
-        if ((e = launch_after((const void*)select_kernel, dim3(1), kSelectThreads, args, stream))) return e;
-    }
     auto run = [&](auto t) -> int {
         using T = decltype(t);
-        const T* x = static_cast<const T*>(a.x);
+        HeadArgs all = a;
         T* out = reinterpret_cast<T*>(ws + at.x);
-        int64_t stride = a.x_stride, rows = a.rows, out_stride = at.x_stride;
-        int32_t cols = a.k;
+        int64_t out_stride = at.x_stride;
         int pieces = (a.k + 255) / 256;
-        void* args[] = {&x, &stride, &rows, &cols, &out, &out_stride, &h, &pieces};
-        const int64_t padded = std::max<int64_t>(64, (a.rows + 63) / 64 * 64);
-        const int64_t grid = (padded * pieces + 7) / 8;
+        const int64_t padded = std::max<int64_t>(64, (a.rows + 63) / 64 * 64), grid = (padded * pieces + 7) / 8;
         if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-        if (const int e = launch_after((const void*)gather_kernel<T>, dim3((unsigned)grid), 256, args, stream)) return e;
+        if (a.rows <= kFewRows) {
+            void* args[] = {&all, &h, &out, &out_stride, &pieces};
+            if (const int e = launch_after((const void*)select_few_kernel<T>, dim3((unsigned)std::min<int64_t>(grid, 2 * sm_count)),
+                                           kFewThreads, args, stream))
+                return e;
+        } else {
+            void* select_args[] = {&all, &h};
+            if (const int e = launch_after((const void*)select_kernel, dim3(1), kSelectThreads, select_args, stream)) return e;
+            const T* x = static_cast<const T*>(a.x);
+            int64_t stride = a.x_stride, rows = a.rows;
+            int32_t cols = a.k;
+            void* args[] = {&x, &stride, &rows, &cols, &out, &out_stride, &h, &pieces};
+            if (const int e = launch_after((const void*)gather_kernel<T>, dim3((unsigned)grid), 256, args, stream)) return e;
+        }
         auto products = [&](const auto& head) {
             const bool gradients = a.dx || a.dweight;
-            // (a row of the pass over the kept exponentials is a row of its grid)
-            const bool keep = forward && gradients && at.pieces == 1 && a.rows <= 65472;
+            // (32 rows of the pass over the kept exponentials are a row of its grid)
+            const bool keep = forward && gradients && at.pieces == 1 && a.rows <= 32 * 65000;
             int e = forward ? head.forward(keep) : cudaSuccess;
             if (!e && gradients) e = head.gradients(keep);
             return e;

@@ -95,10 +95,12 @@ __device__ __forceinline__ void stage_mma(uint32_t acc, uint32_t a, uint32_t b, 
 // drained), k values a sum, tiles, of which those from `whole` on are done in
 // two halves of their columns, walked through in strips of `strip` columns of
 // tiles; or, with splits > 1 (then whole = all tiles), every tile once for each
-// part of k.
+// part of k.  The sum of a unit is handed over every `chunk` stages, anew each
+// time.
 struct TilePlan {
-    int m, k, tiles_m, tiles_n, strip, whole, splits;
+    int m, k, tiles_m, tiles_n, strip, whole, splits, chunk;
 };
+constexpr int kOneChunk = 1 << 26;  // stages: more than any sum has
 
 // ---- a tile of 128 x BN (CG = 1) or 256 x BN (CG = 2) ------------
 
@@ -165,11 +167,17 @@ struct Stager {
 //
 // plan() says what there is to do, once the kernels before this one are done
 // (a row count may come from one of them).  Each warp of the first sixteen
-// calls drain(accumulator's address, first row, first column, columns, split,
-// plan, staging) for its 32 rows of a unit; a unit's sum is complete then.
+// calls drain(accumulator's address, part, staging, done) for its 32 rows of a
+// unit (or of a chunk of it), which calls done() when it has read the
+// accumulator.  `columns` (0 = BN) is the width of tiles narrower than BN, a
+// multiple of 32; CG = 1 and no halves then.
+struct Part {
+    int row0, col0, cols, split;
+    bool first, last;  // of the unit's chunks
+};
 template <int CG, int BN, typename T, typename Plan, typename Drain>
 __device__ __forceinline__ void tile_products(const CUtensorMap* map_a, const CUtensorMap* map_b, bool a_kmajor,
-                                              bool b_kmajor, Plan&& make_plan, Drain&& drain) {
+                                              bool b_kmajor, Plan&& make_plan, Drain&& drain, int columns = 0) {
     using S = TileShape<CG, BN>;
     extern __shared__ char dynamic[];
     __shared__ int gave_up;
@@ -216,15 +224,17 @@ __device__ __forceinline__ void tile_products(const CUtensorMap* map_a, const CU
     const int all_kts = (p.k + kBK - 1) / kBK;
     auto kt_begin = [&](int u) { return p.splits == 1 ? 0 : (int)((int64_t)(u / tiles) * all_kts / p.splits); };
     auto kt_end = [&](int u) { return p.splits == 1 ? all_kts : (int)((int64_t)(u / tiles + 1) * all_kts / p.splits); };
+    const int bn = columns ? columns : BN;
+    const uint32_t stage_bytes = columns ? S::kBytesA + columns * kBK * 2 : S::kStage;
     auto tile_at = [&](int u, int& row0, int& col0) {  // returns the unit's columns
         if (p.splits > 1) u %= tiles;
         const bool half = u >= p.whole;
         const int t = half ? p.whole + (u - p.whole) / 2 : u;
         const int strip = t / (p.tiles_m * p.strip) * p.strip, width = min(p.strip, p.tiles_n - strip);
         const int in_strip = t - strip * p.tiles_m;
-        col0 = (strip + in_strip % width) * BN + (half && (u - p.whole) % 2 ? BN / 2 : 0);
+        col0 = (strip + in_strip % width) * bn + (half && (u - p.whole) % 2 ? BN / 2 : 0);
         row0 = in_strip / width * (kBM * CG) + (int)rank * kBM;
-        return half ? BN / 2 : BN;
+        return half ? BN / 2 : bn;
     };
 
     if (warp == kEpilogueWarps && lane == 0) {
@@ -239,7 +249,7 @@ __device__ __forceinline__ void tile_products(const CUtensorMap* map_a, const CU
             for (int kt = kt_begin(u); kt < kt1; ++kt) {
                 if (!(ok = mbar_wait(empty(s), parity, &gave_up))) break;
                 const uint32_t bar = CG == 2 ? cluster_map(full(s), 0) : full(s);
-                if (rank == 0) mbar_expect(full(s), CG * S::kStage);
+                if (rank == 0) mbar_expect(full(s), CG * stage_bytes);
                 const uint32_t dst = stages + s * S::kStage;
                 load_operand<CG>(dst, map_a, a_kmajor, kBM, row0, kt * kBK, bar);
                 load_operand<CG>(dst + S::kBytesA, map_b, b_kmajor, S::kRowsB, b0, kt * kBK, bar);
@@ -264,43 +274,62 @@ __device__ __forceinline__ void tile_products(const CUtensorMap* map_a, const CU
         bool ok = true;
         for (int u = first; u < units && ok; u += step) {
             const uint32_t idesc =
-                instruction_desc(kIsBf16<T>, a_kmajor, b_kmajor, kBM * CG, p.splits == 1 && u >= p.whole ? BN / 2 : BN);
-            if (!(ok = mbar_wait(acc_empty(i), acc_parity, &gave_up))) break;
-            tcgen05_after_sync();
+                instruction_desc(kIsBf16<T>, a_kmajor, b_kmajor, kBM * CG, p.splits == 1 && u >= p.whole ? BN / 2 : bn);
             const int kt0 = kt_begin(u), kt1 = kt_end(u);
-            for (int kt = kt0; kt < kt1; ++kt) {
-                if (!(ok = mbar_wait(full(s), parity, &gave_up))) break;
+            for (int c0 = kt0; c0 < kt1 && ok; c0 += p.chunk) {
+                if (!(ok = mbar_wait(acc_empty(i), acc_parity, &gave_up))) break;
                 tcgen05_after_sync();
-                const uint32_t src = stages + s * S::kStage;
-                stage_mma<CG>(tmem + i * BN, src, src + S::kBytesA, a_kmajor, b_kmajor, idesc, kt == kt0);
-                mma_commit<CG>(empty(s));
-                if (++s == S::kStages) {
-                    s = 0;
-                    parity ^= 1;
+                const int c1 = min(kt1, c0 + p.chunk);
+                for (int kt = c0; kt < c1; ++kt) {
+                    if (!(ok = mbar_wait(full(s), parity, &gave_up))) break;
+                    tcgen05_after_sync();
+                    const uint32_t src = stages + s * S::kStage;
+                    stage_mma<CG>(tmem + i * BN, src, src + S::kBytesA, a_kmajor, b_kmajor, idesc, kt == c0);
+                    mma_commit<CG>(empty(s));
+                    if (++s == S::kStages) {
+                        s = 0;
+                        parity ^= 1;
+                    }
                 }
+                mma_commit<CG>(acc_full(i));
+                i ^= 1;
+                if (i == 0) acc_parity ^= 1;
             }
-            mma_commit<CG>(acc_full(i));
-            i ^= 1;
-            if (i == 0) acc_parity ^= 1;
         }
     } else if (warp < kEpilogueWarps) {
         const int quarter = warp & 3;
         int i = 0;
         uint32_t parity = 0;
-        for (int u = first; u < units; u += step) {
+        bool ok = true;
+        for (int u = first; u < units && ok; u += step) {
+            Part part;
             int row0, col0;
-            const int cols = tile_at(u, row0, col0) / (kEpilogueWarps / 4), at = (warp >> 2) * cols;  // the warp's
-            if (!mbar_wait(acc_full(i), parity, &gave_up, product_limit(all_kts))) break;
-            __syncwarp();
-            tcgen05_after_sync();
-            if (row0 + quarter * 32 < p.m)
-                drain(tmem + i * BN + at + ((uint32_t)(quarter * 32) << 16), row0 + quarter * 32, col0 + at, cols,
-                      p.splits == 1 ? 0 : u / tiles, p, staging);
-            tcgen05_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(CG == 2 ? cluster_map(acc_empty(i), 0) : acc_empty(i));
-            i ^= 1;
-            if (i == 0) parity ^= 1;
+            // the warp's columns: a quarter of the tile's (of narrow tiles, of BN's)
+            const int width = tile_at(u, row0, col0), quarter_cols = (columns ? BN : width) / (kEpilogueWarps / 4);
+            const int at = (warp >> 2) * quarter_cols;
+            part.row0 = row0 + quarter * 32;
+            part.col0 = col0 + at;
+            part.cols = min(quarter_cols, width - at);
+            part.split = p.splits == 1 ? 0 : u / tiles;
+            const int kt0 = kt_begin(u), kt1 = kt_end(u);
+            for (int c0 = kt0; c0 < kt1; c0 += p.chunk) {
+                if (!(ok = mbar_wait(acc_full(i), parity, &gave_up, product_limit(all_kts)))) break;
+                __syncwarp();
+                tcgen05_after_sync();
+                part.first = c0 == kt0;
+                part.last = kt1 - c0 <= p.chunk;
+                auto done = [&] {
+                    tcgen05_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(CG == 2 ? cluster_map(acc_empty(i), 0) : acc_empty(i));
+                };
+                if (part.row0 < p.m && part.cols > 0)
+                    drain(tmem + i * BN + at + ((uint32_t)(quarter * 32) << 16), part, staging, done);
+                else
+                    done();
+                i ^= 1;
+                if (i == 0) parity ^= 1;
+            }
         }
         if (lane == 0) tma_store_wait();
     }
