@@ -208,8 +208,9 @@ __global__ void __launch_bounds__(256) gather_kernel(const T* x, int64_t stride,
 struct LogitArgs {
     CUtensorMap a, b, out;
     HeadRows h;
-    float2* parts;          // maximum and sum of exponentials of row r's slice q of 32 columns, at
-    int64_t pitch, step;    //   q * pitch + r * step
+    float2* parts;          // [slices of 32 columns][pitch rows] maximum and sum of exponentials
+    int64_t pitch;
+    float2* joined;         // few rows: [rows][CTAs]
     bool keep;              // stats: store the exponentials too
     int32_t columns;        // stats: of narrow tiles, or 0
     float *loss, *lse;      // stats of few rows: what the last CTA writes (either may be nullptr)
@@ -289,10 +290,13 @@ __device__ __forceinline__ void write_loss(const HeadRows& h, int i, float2 sum,
 // 1.7e-7 for 7 %, of 2048 by 7.8e-7.
 constexpr int kLogitChunk = 1024 / kBK;
 
+constexpr int kJoinedRows = 16;  // "few rows": about one for each warp of the last CTA
+
 template <int CG, int BN, typename T>
 __global__ void __launch_bounds__(kTileThreads, 1) stats_kernel(const __grid_constant__ LogitArgs p) {
     constexpr int kCols = BN / (kEpilogueWarps / 4);  // of a warp, at most
     float z[kCols];
+    float2 run = make_float2(kLowest, 0.f);  // few rows: of this thread's row, over all its tiles
     tile_products<CG, BN, T>(
         &p.a, &p.b, true, true,
         [&] { return plan_rows<CG>(p.h.counted->padded, p.k, p.tiles_n, p.strip, p.columns == 0, 1, kLogitChunk); },
@@ -339,7 +343,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) stats_kernel(const __grid_con
                     even += x[i];
                     odd += x[i + 1];
                 }
-                p.parts[col / 32 * p.pitch + row * p.step] = make_float2(m, even + odd);
+                if (p.join) run = join_stats(run, make_float2(m, even + odd));
+                if (!p.join || p.keep) p.parts[col / 32 * p.pitch + row] = make_float2(m, even + odd);
                 if (p.keep) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) x[i] *= kKeepScale<T>;
@@ -349,26 +354,33 @@ __global__ void __launch_bounds__(kTileThreads, 1) stats_kernel(const __grid_con
         },
         p.columns);
     if (!p.join) return;
-    // Few rows: the last CTA to finish joins the slices, a warp a row, which
-    // saves a launch.
+    // Few rows, all in the first 32 of the tile: a CTA joins what its warps have,
+    // and the last CTA to finish what the CTAs have, a warp a row; that saves a
+    // launch.
     __shared__ bool last;
-    __threadfence();
+    extern __shared__ char dynamic[];  // (nothing is on its way there any more)
+    float2 (*sums)[32] = reinterpret_cast<float2 (*)[32]>(dynamic);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (warp < kEpilogueWarps && warp % 4 == 0) sums[warp / 4][lane] = run;
+    __syncthreads();
+    if (warp == 0) {
+        for (int w = 1; w < kEpilogueWarps / 4; ++w) run = join_stats(run, sums[w][lane]);
+        if (lane < kJoinedRows) p.joined[lane * gridDim.x + blockIdx.x] = run;
+        __threadfence();
+    }
     __syncthreads();
     if (threadIdx.x == 0) last = atomicAdd(&p.h.counted->ticket, 1u) == gridDim.x - 1;
     __syncthreads();
     if (!last) return;
     __threadfence();
-    const int slices = (p.n + 31) / 32, lane = threadIdx.x & 31;
-    for (int i = threadIdx.x >> 5; i < p.h.counted->rows; i += kTileThreads / 32) {
-        float2 own = join_parts(p.parts + i * p.step, p.pitch, lane, 32, slices);
+    for (int i = warp; i < p.h.counted->rows; i += kTileThreads / 32) {
+        float2 own = join_parts(p.joined + i * gridDim.x, 1, lane, 32, gridDim.x);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             own = join_stats(own, make_float2(__shfl_xor_sync(0xffffffffu, own.x, o), __shfl_xor_sync(0xffffffffu, own.y, o)));
         if (lane == 0) write_loss(p.h, i, own, p.loss, p.lse);
     }
 }
-
-constexpr int kJoinedRows = 16;  // about one for each warp of the last CTA
 
 // Log-sum-exp and loss of 8 counted rows per CTA, or of 4 where rows are few:
 // kRows lanes take neighbouring rows, the others slices in turn.
@@ -647,7 +659,7 @@ struct HeadLayout {
         z_token = take(pitch * 4);
         x = take(pitch * x_stride * 2);
         w = take(copy_weight ? vocab * w_stride * 2 : 0);
-        parts = take(forward ? pitch * slices(vocab) * 8 : 0);
+        parts = take(forward ? (pitch * slices(vocab) + (int64_t)kJoinedRows * sms) * 8 : 0);
         dz = take(dx || dweight ? pitch * piece * 2 : 0);
         sums = take(dx ? most_parts * pitch * sums_stride * 4 : 0);
         bytes = at;
@@ -696,7 +708,6 @@ struct Head {
     int logits(LogitArgs& p, int64_t first, int64_t n, int width) const {
         p.h = h;
         p.pitch = at.pitch;
-        p.step = 1;
         p.n = (int32_t)n;
         p.k = a.k;
         p.first = (int32_t)first;
@@ -721,13 +732,10 @@ struct Head {
             const int64_t waves = (((int64_t)a.vocab + 255) / 256 + sms - 1) / sms;
             p.columns = (int32_t)(((a.vocab + waves * sms - 1) / (waves * sms) + 31) / 32 * 32);
             p.join = a.rows <= kJoinedRows;
+            p.joined = p.parts + HeadLayout::slices(a.vocab) * at.pitch;
             p.loss = a.loss;
             p.lse = a.lse;
             e = Head<1, 256, T>{a, at, h, ws, w, w_stride, sms, stream}.logits(p, 0, a.vocab, p.columns);
-            if (p.join && !keep) {  // a row's parts side by side
-                p.pitch = 1;
-                p.step = HeadLayout::slices(a.vocab);
-            }
             if (!e)
                 e = launch_cluster((const void*)stats_kernel<1, 256, T>, args, std::min<int64_t>(p.tiles_n, sms),
                                    kTileThreads, TileShape<1, 256>::kSmem, 1, stream);
