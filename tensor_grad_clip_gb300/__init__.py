@@ -11,6 +11,11 @@ memory and streams.  Typical use::
     tl = TensorList(params, grads, exp_avgs, exp_avg_sqs, groups=[g_mat, ...])
     opt.step(tl, grad_divisor=64.0, max_norm=1.0)      # async on the current stream
     norm, coef, nonfinite = opt.get_norm()            # waits
+
+Moments in 8 bits, a quarter of their memory, for any of a list's tensors::
+
+    (m, m_scale), (v, v_scale) = zeros_8bit(param), zeros_8bit(param)
+    tl = TensorList([param], [grad], [m], [v], groups=[g_mat], exp_avg_scales=[m_scale], exp_avg_sq_scales=[v_scale])
 """
 from __future__ import annotations
 

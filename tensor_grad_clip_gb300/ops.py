@@ -1,6 +1,7 @@
 """Training operators whose gradients the optimizer step takes: layer norm,
-linear layer and distillation loss, each forward and backward, as sm_103a
-kernels behind the C ABI of include/soma_ops.h (formulas there).
+linear layer, distillation loss, embedding and the cross entropy of a linear
+layer over a vocabulary, each forward and backward, as sm_103a kernels behind
+the C ABI of include/soma_ops.h (formulas there).
 
 Explicit calls, for programs that keep their own backward pass::
 
@@ -12,11 +13,18 @@ Explicit calls, for programs that keep their own backward pass::
     dy, dw1, db1 = linear_backward(dh, y, w1, z, activation="gelu")
     dx, dweight, dbias = layer_norm_backward(dy, x, weight, mean, rstd)
 
-and the same with autograd: layer_norm, linear, distill_loss.
+and for a language model's two ends, here with one table for both::
+
+    x = embedding_forward(tokens, table)
+    loss, dy, dtable = linear_cross_entropy_loss_grad(y, table, targets)
+    embedding_backward(dx, tokens, len(table), out=dtable)
+
+and the same with autograd: layer_norm, linear, distill_loss, embedding,
+linear_cross_entropy.
 
 Tensors are CUDA tensors with unit stride in the last dimension; all leading
 dimensions are rows and must be evenly spaced (any tensor that can be viewed
-as [rows, last]).  Work is enqueued on the current stream, or on `stream` (a
+as [rows, last], a slice tokens[:, 1:] of a batch of texts among them).  Work is enqueued on the current stream, or on `stream` (a
 torch stream or a raw cudaStream_t), which then also owns the outputs; the
 inputs are kept alive for it.  Nothing waits for the GPU, and there is no
 fallback: a refused call raises SomaError, ValueError or TypeError.
