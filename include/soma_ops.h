@@ -221,7 +221,7 @@ soma_status_t soma_embedding_backward(int32_t device, const void *dy, int64_t dy
  * workspace, as does a copy of the rows of x that count, and of weight where
  * its rows do not start on 16-byte boundaries.  Each piece makes its logits
  * again, except that loss_grad with one piece (at most 2 million rows) keeps their
- * exponentials, rounded to 16 bits, in that buffer: dz is then rounded twice.
+ * exponentials in that buffer, rounded to fp16's 11 bits, before it makes dz.
  *
  *   forward    loss and lse (either may be NULL)
  *   backward   dx and dweight (either may be NULL) from forward's lse

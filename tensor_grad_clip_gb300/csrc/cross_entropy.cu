@@ -245,10 +245,11 @@ __device__ __forceinline__ void load_logits(uint32_t acc, int col, int n, float 
     }
 }
 
-// What the kept exponentials, at most 1, are multiplied by: fp16 has no
-// small enough numbers for what a vocabulary's tail weighs.
-template <typename T>
-constexpr float kKeepScale = kIsBf16<T> ? 1.f : 16384.f;
+// The kept exponentials, at most 1, are fp16 whatever the operands are: its 11
+// bits lose little beside the 8 that bf16's dz is rounded to (in bf16 they
+// would cost as much again as that).  Times 2^14, so that fp16 has numbers for
+// what a vocabulary's tail weighs: down to 2^-38.
+constexpr float kKeepScale = 16384.f;
 
 __device__ __forceinline__ float2 join_stats(float2 a, float2 b) {
     const float m = fmaxf(a.x, b.x);
@@ -290,7 +291,8 @@ __device__ __forceinline__ void write_loss(const HeadRows& h, int i, float2 sum,
 // 1.7e-7 for 7 %, of 2048 by 7.8e-7.
 constexpr int kLogitChunk = 1024 / kBK;
 
-constexpr int kJoinedRows = 16;  // "few rows": about one for each warp of the last CTA
+constexpr int kJoinedRows = 16;  // "few rows": about one for each warp of the last CTA (22.5 us for 16 rows, 26 with a
+                                 // kernel of its own)
 
 template <int CG, int BN, typename T>
 __global__ void __launch_bounds__(kTileThreads, 1) stats_kernel(const __grid_constant__ LogitArgs p) {
@@ -314,7 +316,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) stats_kernel(const __grid_con
             if (!part.last) return;
             const int row = part.row0 + (threadIdx.x & 31);
             const int at = p.h.token[row] - part.col0;  // the token's column here
-            Stager<T> stager{staging + (threadIdx.x >> 5) * kStagerBytes, part.row0, 0, p.n};
+            Stager<__half> stager{staging + (threadIdx.x >> 5) * kStagerBytes, part.row0, 0, p.n};
 #pragma unroll
             for (int c = 0; c < kCols; c += 32) {
                 const int col = part.col0 + c;
@@ -347,7 +349,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) stats_kernel(const __grid_con
                 if (!p.join || p.keep) p.parts[col / 32 * p.pitch + row] = make_float2(m, even + odd);
                 if (p.keep) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] *= kKeepScale<T>;
+                    for (int i = 0; i < 32; ++i) x[i] *= kKeepScale;
                     stager.store(x, col, &p.out, true, nullptr, 0);
                 }
             }
@@ -404,8 +406,7 @@ __global__ void __launch_bounds__(kJoinThreads) stats_join_kernel(const float2* 
     write_loss(h, i, own, loss, lse);
 }
 
-// dz of the kept exponentials, in place: a CTA 32 rows of 256 columns.  What
-// rounding them once more costs is at most another half step of 16 bits; the
+// dz of the kept exponentials, in place: a CTA 32 rows of 256 columns.  The
 // token's own element, a difference from 1, is made of its logit.
 constexpr int kKeepRows = 32, kKeepCols = 256;
 template <typename T>
@@ -418,7 +419,7 @@ __global__ void __launch_bounds__(256) keep_kernel(T* dz, int64_t stride, const 
     {
         const int r = threadIdx.x % kKeepRows, q = threadIdx.x / kKeepRows;
         if (col0 + 32 * q < n)
-            factor[q][r] = h.g[row0 + r] * h.counted->scale * (1.f / kKeepScale<T>) *
+            factor[q][r] = h.g[row0 + r] * h.counted->scale * (1.f / kKeepScale) *
                            exp2_fast((__ldcs(&parts[(col0 / 32 + q) * pitch + row0 + r].x) - h.lse[row0 + r]) * kLog2e);
     }
     __syncthreads();
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(256) keep_kernel(T* dz, int64_t stride, const 
         const int r = warp + 8 * k, row = row0 + r;
         const float f = factor[lane / 4][r];
         float x[8];
-        widen16(v[k], x, T{});
+        widen16(v[k], x, __half{});
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] *= f;
         const int d = h.token[row] - c;
@@ -583,8 +584,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) dx_kernel(const __grid_consta
 // dx of all rows: the sums of the parts, unscaled and rounded; 0 for rows that
 // do not count.
 template <typename T>
-__global__ void __launch_bounds__(256) dx_round_kernel(const float* sums, int64_t pitch, int64_t sums_stride, HeadRows h, T* dx, int64_t dx_stride, int64_t rows, int32_t cols,
-                                                       int pieces) {
+__global__ void __launch_bounds__(256) dx_round_kernel(const float* sums, int64_t pitch, int64_t sums_stride, HeadRows h,
+                                                       T* dx, int64_t dx_stride, int64_t rows, int32_t cols, int pieces) {
     follow_stream();
     const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int64_t r = item / pieces;

@@ -430,6 +430,9 @@ def _tokens(t, name, other):
     code = _code(t, name, _INDEX)
     if t.device != other.device:
         raise ValueError(f"{name}: on {t.device}, expected {other.device}")
+    if t.dim() == 1 and t.is_cuda and t.is_contiguous():  # (host time: most calls)
+        n = t.shape[0]
+        return t.data_ptr(), n, 1, n, code
     if t.dim() == 0:
         t = t.unsqueeze(0)
     m = _matrix(t, name)

@@ -45,7 +45,8 @@ class Case:
 
     def reference(self, grad_loss=None, lse=None, kept=False):
         """Loss, lse, dx, dweight and their bounds in fp64; lse: as given to the backward pass; kept: exponentials are
-        rounded to 16 bits before dz is, which is another half step of p, or of fp16's smallest 2^-24 / 2^14 of the largest."""
+        rounded to fp16 before dz is, half a step of p, or of fp16's smallest, 2^-24 / 2^14 of the largest (which is at most
+        1 above p's own slice: g times 2^-39)."""
         x, w = self.x.double(), self.w.double()
         counts = (self.t >= 0) & (self.t < self.vocab)
         weight = torch.ones(self.rows, device="cuda", dtype=torch.float64) if self.weight is None else self.weight.double()
@@ -70,7 +71,7 @@ class Case:
         # rounded once to 16 bits; what is scaled below the type's smallest steps (fp16: 2^-25 of 2^14 / the largest |g|)
         step = g.abs().max() * 2.0 ** -38 if self.dtype == torch.float16 else 2.0 ** -126
         if kept:
-            e_dz = e_dz + g.abs()[:, None] * (HALF_ULP[self.dtype] * p + (2.0 ** -39 if self.dtype == torch.float16 else 2.0 ** -126))
+            e_dz = e_dz + g.abs()[:, None] * (HALF_ULP[torch.float16] * p + 2.0 ** -39)
         e_dz = e_dz + HALF_ULP[self.dtype] * (dz.abs() + e_dz) + step
         mag = dz.abs() + e_dz
         dx, dw = dz @ w, dz.t() @ x
