@@ -18,6 +18,13 @@
 //   dx       dz W added to fp32 sums, which a last kernel rounds
 // The number of rows that count is only known on the device: the products read
 // it there.
+//
+// Bound by the tensor cores, for few rows by reading the weight.  Measured
+// (GB300, cuBLAS bf16 1916 TFLOP/s in a burst, 1723 in a loop; 85 % of the rows
+// count): loss of 8192 rows, 32000 x 4096, 1.13 ms, 1612 TFLOP/s; loss and
+// gradients of 4096 rows, 131072 x 4096, 7.3 ms, 1536 TFLOP/s counted as three
+// products (9.4 ms with the logits made twice); of 2500 rows, 32000 x 1024
+// fp16, 369 us; loss of 16 rows, 32000 x 1024, 22.4 us, 2.9 TB/s.
 #include <math.h>
 
 #include <algorithm>
