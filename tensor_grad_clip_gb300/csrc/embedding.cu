@@ -14,7 +14,7 @@
 // which they are before the sort is done.
 //
 // Measured (GB300, 6786 GB/s copy): 16384 tokens of 4096 bf16 looked up in 34.2
-// us; their gradient in a table of 32000 rows 85.4 us, of which zeroing beside
+// us; their gradient in a table of 32000 rows 76 us, of which zeroing beside
 // the sort takes 40 (a memset takes 38) and the sums 27 (5.5 TB/s); 5003 tokens
 // of 1003 fp32 added to a gradient 24.5 us, three dependent launches.
 #include <math.h>
@@ -224,8 +224,8 @@ __device__ __forceinline__ void zero_bytes(char* p, int64_t bytes, int64_t at, i
     for (int64_t i = at; i < words; i += step) __stcs(body + i, make_uint4(0, 0, 0, 0));
 }
 
-constexpr int64_t kPage = 32768;  // bytes
-constexpr int kZeroCtas = 4;  // per SM: 90 us for the table of 32000 x 4096 bf16 and 16384 tokens; 95 with 2, 92 with 8
+constexpr int64_t kPage = 16384;  // bytes
+constexpr int kZeroCtas = 8;      // per SM, one after the other
 
 // CTA `at` of `ctas` zeroes its part of the table.
 __device__ __forceinline__ void zero_table(const SortArgs& a, int at, int ctas) {
@@ -596,10 +596,19 @@ int launch_sort(SortArgs& s, int sm_count, void* stream) {
     // CTAs that zero: a page each at least, at most kZeroCtas per SM
     const int zeros = (int)std::min<int64_t>(kZeroCtas * sm_count, (zero + kPage - 1) / kPage);
     if (one_cluster(s.rows)) {
+        // More CTAs sort faster (5003 rows in 11 us with eight, 23 with one), fewer
+        // leave the zeroing more room: clusters of eight do not fill every SM.  So
+        // as few as are done when the table is zeroed (about 9 us and 2.7 for each
+        // 1000 rows of a CTA; 6.5 GB/ms), and one zeroing CTA per SM at a time,
+        // which its shared memory sees to: 16384 tokens into 32000 x 4096 bf16 76 us
+        // with clusters of two, 78 of four, 84 of eight or with three CTAs per SM.
+        const double zeroed = (double)zero / 6.5e6;
         int ctas = 1;
-        while (ctas < kSortCtas && (int64_t)ctas * 1024 < s.rows) ctas *= 2;
+        while (ctas < kSortCtas && ((int64_t)ctas * kSortShare < s.rows ||
+                                    ((int64_t)ctas * 1024 < s.rows && 9 + 2.7e-3 * s.rows / ctas > zeroed)))
+            ctas *= 2;
         s.share = (int32_t)((s.rows + ctas - 1) / ctas);
-        const int smem = s.share * 16;
+        const int smem = zeros ? std::max(s.share * 16, 100 << 10) : s.share * 16;
         if (const int e = allow_smem((const void*)cluster_sort_kernel, smem)) return e;
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(ctas + (zeros + ctas - 1) / ctas * ctas);
