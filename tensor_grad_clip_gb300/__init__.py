@@ -63,7 +63,7 @@ def _lowp_code(dtype) -> int:
 def _stream_handle(stream) -> int:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -188,15 +188,17 @@ class TensorList:
             e.trainable = 1 if tr else 0
             e.owned = 1 if owned[k] else 0
 
+        pointer = ctypes.cast(self.array, ctypes.POINTER(soma_tensor_t))
+        # what the C calls take of the list, made once
+        self._entries = (pointer, n) if not eight else (
+            pointer, ctypes.cast(self.scales, ctypes.POINTER(soma_scales_t)), n)
+
     def pointer(self):
-        return ctypes.cast(self.array, ctypes.POINTER(soma_tensor_t))
+        return self._entries[0]
 
     def _call(self, name: str):
         """The C function that takes this list, and its list arguments."""
-        if self.scales is None:
-            return getattr(_abi, name), (self.pointer(), self.n)
-        return getattr(_abi, name + "8"), (self.pointer(), ctypes.cast(self.scales, ctypes.POINTER(soma_scales_t)),
-                                           self.n)
+        return getattr(_abi, name if self.scales is None else name + "8"), self._entries
 
 
 class SomaOpt:
