@@ -215,7 +215,7 @@ soma_status_t soma_embedding_backward(int32_t device, const void *dy, int64_t dy
  *
  * Logits, exponentials and sums are fp32.  dz is rounded once to the operands'
  * 16 bits before the two products, whose tensor-core operands are 16-bit; a
- * power of two, found from the largest |g|, keeps it in fp16's range.  The
+ * factor, found from the largest |g|, keeps it in fp16's range.  The
  * gradients take the vocabulary in pieces; a piece's dz, at most 512 MB or the
  * weight's size if that is more (512 bytes a row at least), lies in the
  * workspace, as does a copy of the rows of x that count, and of weight where

@@ -304,6 +304,33 @@ def test_streams_graphs_and_equal_bits(ops):
     assert all(torch.equal(a, b) for a, b in zip(want, got))
 
 
+@pytest.mark.parametrize("rows", [1, 16, 17])
+def test_few_rows_replayed_and_at_once(ops, rows):
+    """The last CTA to finish joins few rows: every call and every replay finds its own."""
+    torch.manual_seed(10)
+    cases = [Case(rows, 20000, 512, torch.bfloat16, ignored=0) for _ in range(2)]
+    want = [ops.linear_cross_entropy_forward(c.x, c.w, c.t, row_weight=c.weight) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[ops.linear_cross_entropy_forward(c.x, c.w, c.t, row_weight=c.weight, stream=s) for c, s in zip(cases, streams)]
+           for _ in range(20)]
+    torch.cuda.synchronize()
+    for pair in got:
+        for g, w in zip(pair, want):
+            assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+    c, graph = cases[0], torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=streams[0]):
+        first = ops.linear_cross_entropy_forward(c.x, c.w, c.t, row_weight=c.weight)
+        second = ops.linear_cross_entropy_forward(c.x, c.w, c.t, row_weight=c.weight)
+    for k in range(5):
+        c.t[0] = -1 if k % 2 else 7  # another row counts, or none does
+        graph.replay()
+        torch.cuda.synchronize()
+        loss, lse = ops.linear_cross_entropy_forward(c.x, c.w, c.t, row_weight=c.weight)
+        for g in (first, second):
+            assert torch.equal(g[0], loss) and torch.equal(g[1], lse)
+
+
 def test_the_whole_path_of_a_language_model(ops):
     """Tokens to a step: embedding, layer norm, linear, cross entropy, all gradients, and AdamW with moments in 8 bits."""
     from tensor_grad_clip_gb300 import SomaOpt, TensorList, zeros_8bit
