@@ -210,8 +210,8 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
 }
-__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+__device__ __forceinline__ void st_cluster_u32x2(uint32_t addr, uint2 v) {
+    asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
 }
 
 // Zeroes `bytes` bytes (a multiple of 2) from p on, with the threads [at, at + 1, ...) of `step`.
@@ -243,7 +243,7 @@ __device__ __forceinline__ void zero_table(const SortArgs& a, int at, int ctas) 
 // each in shared memory and hand each other the items of a pass through it.
 // The other clusters zero the table.
 __global__ void __launch_bounds__(kSortThreads) cluster_sort_kernel(const __grid_constant__ SortArgs a) {
-    extern __shared__ uint32_t sort_smem[];
+    extern __shared__ uint2 sort_smem[];  // token and row, so that an item moves in one store
     __shared__ uint32_t hist[kSortWarps][kMaxDigits];
     __shared__ uint32_t total[kMaxDigits], start[kMaxDigits], scratch[kSortWarps];
     launch_dependents();
@@ -253,18 +253,16 @@ __global__ void __launch_bounds__(kSortThreads) cluster_sort_kernel(const __grid
         return;
     }
     const int begin = rank * share, n = max(0, min(share, (int)a.rows - begin));
-    uint32_t* keys[2] = {sort_smem, sort_smem + 2 * share};
-    uint32_t* order[2] = {sort_smem + share, sort_smem + 3 * share};
+    uint2* items[2] = {sort_smem, sort_smem + share};
     for (int i = threadIdx.x; i < n; i += kSortThreads) {
         const int v = token_at(a.tokens, begin + i, a.vocab);
-        keys[0][i] = v < 0 ? a.vocab : v;
-        order[0][i] = begin + i;
+        items[0][i] = make_uint2(v < 0 ? a.vocab : v, begin + i);
     }
     __syncthreads();
     const int digits = 1 << a.digit_bits;
     for (int p = 0; p < a.passes; ++p) {
         const int from = p & 1, shift = p * a.digit_bits;
-        auto key = [&](int i) { return keys[from][i] >> shift & (digits - 1); };
+        auto key = [&](int i) { return items[from][i].x >> shift & (digits - 1); };
         count_digits(hist, total, n, digits, key);
         cluster_sync_all();  // every CTA's totals are there
         uint32_t all = 0, before = 0;
@@ -286,14 +284,13 @@ __global__ void __launch_bounds__(kSortThreads) cluster_sort_kernel(const __grid
         __syncthreads();
         const bool last = p == a.passes - 1;
         scatter_digits(hist, start, n, key, [&](int i, uint32_t place) {
-            const uint32_t k = keys[from][i], r = order[from][i];
+            const uint2 item = items[from][i];
             if (last) {
-                a.keys[place] = k;
-                a.order[place] = r;
+                a.keys[place] = item.x;
+                a.order[place] = item.y;
             } else {
                 const uint32_t c = place / share, at = place - c * share;
-                st_cluster_u32(cluster_map(smem_addr(keys[from ^ 1] + at), c), k);
-                st_cluster_u32(cluster_map(smem_addr(order[from ^ 1] + at), c), r);
+                st_cluster_u32x2(cluster_map(smem_addr(items[from ^ 1] + at), c), item);
             }
         });
         cluster_sync_all();  // the items have arrived; nobody reads this pass's totals any more
