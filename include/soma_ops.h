@@ -182,8 +182,8 @@ soma_status_t soma_distill_loss_grad(int32_t device, const void *logits, int64_t
  * and dweight[vocab][cols] are in dtype; 1 <= vocab, cols <= 2^30; scale is
  * finite.
  *
- * Sums are fp32, of a token's rows in rising order (64 sorted positions at a
- * time), times scale, rounded once.  Without accumulate all of dweight is
+ * Sums are fp32, of a token's rows in rising order (16 to 64 sorted positions
+ * at a time, by the sizes), times scale, rounded once.  Without accumulate all of dweight is
  * written, rows without a token with 0; with it only the rows of tokens that
  * occur are read and written (a table shared with the last linear layer takes
  * that one's gradient first). */
