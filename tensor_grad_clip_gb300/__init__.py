@@ -85,14 +85,19 @@ def zeros_8bit(like):
     return codes, torch.zeros(-(-like.numel() // SOMA_STATE_BLOCK), dtype=torch.float32, device=like.device)
 
 
-def to_8bit(moment):
-    """(codes, scales) of an fp32 moment, rounded to nearest: exp_avg, or the
-    square root of exp_avg_sq (which is what the step holds in 8 bits)."""
+def to_8bit(moment, second_moment: bool = False):
+    """(codes, scales) of an fp32 moment, rounded to nearest: exp_avg, or, with
+    second_moment, the square root of exp_avg_sq (which is what the step holds
+    in 8 bits).  A second moment that is not 0 then gets at least the first
+    code, as in the step: a weight whose exp_avg is not 0 would move by
+    exp_avg / eps where it became 0."""
     import torch
     flat = moment.detach().float().reshape(-1)
     blocks = torch.nn.functional.pad(flat, (0, -flat.numel() % SOMA_STATE_BLOCK)).view(-1, SOMA_STATE_BLOCK)
     scales = blocks.abs().amax(1) * (1.0 / 448.0)
     values = blocks / torch.where(scales > 0, scales, 1.0)[:, None]
+    if second_moment:
+        values = torch.where(blocks > 0, values.clamp(min=2.0 ** -9), values)
     codes = values.clamp(-448.0, 448.0).to(torch.float8_e4m3fn)
     return codes.view(-1)[:flat.numel()].reshape(moment.shape), scales
 
@@ -116,8 +121,9 @@ class TensorList:
     exp_avg_scales / exp_avg_sq_scales: optional; where they have a tensor and
     not None, that entry's moments are held in 8 bits: exp_avgs and exp_avg_sqs
     are float8_e4m3fn, the scales float32 with one value for each
-    SOMA_STATE_BLOCK elements (zeros_8bit makes both; exp_avg_sqs holds the
-    square root, see soma_opt_step8 in soma_opt.h)."""
+    SOMA_STATE_BLOCK elements (zeros_8bit makes both, to_8bit those of a run
+    with fp32 moments; exp_avg_sqs holds the square root, see soma_opt_step8 in
+    soma_opt.h)."""
 
     def __init__(self, params: Sequence, grads: Sequence, exp_avgs: Sequence, exp_avg_sqs: Sequence,
                  groups: Sequence[int], trainable: Optional[Sequence[bool]] = None,

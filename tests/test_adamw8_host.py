@@ -103,5 +103,18 @@ def test_conversion_on_the_cpu():
     assert codes.dtype == F8 and torch.equal(from_8bit(codes, scales)[:3], x[:3])
 
 
+def test_a_converted_second_moment_stays_above_0():
+    x = torch.cat([torch.tensor([1.0, 1e-6, 0.0, 1e-30]), torch.zeros(252), torch.tensor([0.0, 2.0 ** -60, 1e25, 3.0])])
+    codes, scales = to_8bit(x, second_moment=True)
+    assert torch.equal(from_8bit(codes, scales) > 0, x > 0)
+    # at least the first code, 2^-9, of a block whose largest is 448; what is above it is rounded as any moment is
+    assert codes[1].item() == codes[3].item() == 2.0 ** -9
+    plain, plain_scales = to_8bit(x)
+    above = plain.float() > 0
+    assert torch.equal(scales, plain_scales) and torch.equal(codes.float()[above], plain.float()[above])
+    nothing = to_8bit(torch.zeros(300), second_moment=True)
+    assert not nothing[0].float().any() and not nothing[1].any()
+
+
 def test_struct_layout():
     assert ctypes.sizeof(_abi.soma_scales_t) == 16 and _abi.SOMA_STATE_BLOCK == 256

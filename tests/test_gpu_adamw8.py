@@ -418,3 +418,23 @@ def test_conversion():
     assert ((back - x).abs() <= x.abs() * 2.0 ** -4 * (1 + 2.0 ** -20) + x.abs().max() / 448 * 2.0 ** -10).all()
     codes, scales = zeros_8bit(x)
     assert not from_8bit(codes, scales).any()
+
+
+def test_a_step_after_a_conversion_stays_bounded():
+    """An element whose second moment is far below its block's largest, converted from fp32, then a step without gradient."""
+    n = 3 * BLOCK
+    m, root = torch.full((n,), 1e-6, device="cuda"), torch.full((n,), 1e-6, device="cuda")
+    m[::BLOCK], root[::BLOCK] = 0.01, 1.0
+    e = Entry(n)
+    e.g.zero_()
+    e.p.zero_()
+    (mc, e.ms), (vc, e.vs) = to_8bit(m), to_8bit(root, second_moment=True)
+    e.m.copy_(mc), e.v.copy_(vc)
+    opt = new_opt(step=999, lr=1.0, eps=1e-8)
+    opt.step(make_list([e]), 1.0, 1.0)
+    bc1, bc2 = 1 - 0.9 ** 1000, 1 - 0.999 ** 1000
+    exact = 0.9 * m.double() / bc1 / (math.sqrt(0.999 / bc2) * root.double() + 1e-8)
+    # e4m3: m is within 2^-4 of itself and half of the first code, 2^-10 of 1 / 448 of the block's largest; sqrt(v) is not
+    # below 1 - 2^-4 of itself (2 % for the step's own fp32 and the parts that these bounds multiply)
+    most = exact * (1 + 2.0 ** -4 + 0.01 / 448 * 2.0 ** -10 / m.double()) / (1 - 2.0 ** -4) * 1.02
+    assert (-e.p.double() <= most).all() and (e.p <= 0).all()
