@@ -57,7 +57,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // NaN where eithe
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
-__device__ __forceinline__ float reciprocal_fast(float x) {  // within 2^-23
+__device__ __forceinline__ float reciprocal_fast(float x) {  // within 2^-23; infinite for subnormal x
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
@@ -82,6 +82,10 @@ __device__ __forceinline__ float warp_top(float x) {
 // codes; the weights' update is fused.
 __device__ __forceinline__ void step_block(Eight& x, float& ms, float& vs, const GroupHp& h, float scale, uint32_t mixed) {
     float m[8], root[8], top_m = 0.f, top_v = 0.f;
+    // (the reciprocal takes subnormal numbers for 0: where eps is one, which a
+    // weight without moments is divided by, everything is 2^24 times as large)
+    const float up = h.eps < 0x1p-126f ? 0x1p24f : 1.f;
+    const float step_size = h.step_size * up, inv_sqrt_bc2 = h.inv_sqrt_bc2 * up, eps = h.eps * up;
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
         const float2 a = from_e4m3((i < 4 ? x.m.x : x.m.y) >> (8 * (i % 4)) & 0xffff);
@@ -95,7 +99,7 @@ __device__ __forceinline__ void step_block(Eight& x, float& ms, float& vs, const
         m[i] = __fadd_rn(__fmul_rn(m[i], h.beta1), __fmul_rn(g, h.one_minus_beta1));
         root[i] = sqrtf(__fadd_rn(__fmul_rn(__fmul_rn(root[i], root[i]), h.beta2),
                                   __fmul_rn(__fmul_rn(g, g), h.one_minus_beta2)));
-        x.p[i] = fmaf(-h.step_size, m[i] * reciprocal_fast(fmaf(root[i], h.inv_sqrt_bc2, h.eps)), x.p[i] * h.decay);
+        x.p[i] = fmaf(-step_size, m[i] * reciprocal_fast(fmaf(root[i], inv_sqrt_bc2, eps)), x.p[i] * h.decay);
         top_m = max_nan(top_m, fabsf(m[i]));
         top_v = max_nan(top_v, root[i]);
     }

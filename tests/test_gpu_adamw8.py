@@ -438,3 +438,29 @@ def test_a_step_after_a_conversion_stays_bounded():
     # below 1 - 2^-4 of itself (2 % for the step's own fp32 and the parts that these bounds multiply)
     most = exact * (1 + 2.0 ** -4 + 0.01 / 448 * 2.0 ** -10 / m.double()) / (1 - 2.0 ** -4) * 1.02
     assert (-e.p.double() <= most).all() and (e.p <= 0).all()
+
+
+@pytest.mark.parametrize("eps", [1e-38, 1e-40, 3e-45])
+def test_an_eps_that_is_subnormal(eps):
+    """Weights without gradient and moments are divided by eps alone: they only decay, as beside fp32 moments."""
+    torch.manual_seed(13)
+    entries = [Entry(n, grad, shift=shift, eight=eight) for n, grad, shift, eight in (
+        (1000, torch.float32, 0, True), (1000, torch.bfloat16, 5, True), (1000, torch.float32, 0, False))]
+    for e in entries:
+        quiet = torch.rand(e.n, device="cuda") < 0.3
+        quiet[256:512] = True
+        e.quiet = quiet
+        e.g[quiet] = 0
+        for t in (e.m, e.v):
+            t.view(torch.uint8 if e.eight else torch.float32)[quiet] = 0
+        e.guards = [raw.clone() for raw, _ in e.buffers]
+    hp = {**HP, "eps": eps}
+    want = reference_step(entries, 10, hp, 1.0, 1.0)
+    before = [e.p.clone() for e in entries]
+    opt = new_opt(step=9, eps=eps)
+    opt.step(make_list(entries), 1.0, 1.0)
+    check_step(entries, 10, want[2])
+    for e, p in zip(entries, before):
+        assert torch.isfinite(e.p).all()
+        decayed = p[e.quiet].double() * (1 - hp["lr"] * hp["weight_decay"])
+        assert ((e.p[e.quiet].double() - decayed).abs() <= 2 * U32 * decayed.abs()).all()
