@@ -216,12 +216,19 @@ soma_status_t soma_embedding_backward(int32_t device, const void *dy, int64_t dy
  * Logits, exponentials and sums are fp32.  dz is rounded once to the operands'
  * 16 bits before the two products, whose tensor-core operands are 16-bit; a
  * factor, found from the largest |g|, keeps it in fp16's range.  The
- * gradients take the vocabulary in pieces; a piece's dz, at most 512 MB or the
- * weight's size if that is more (512 bytes a row at least), lies in the
- * workspace, as does a copy of the rows of x that count, and of weight where
- * its rows do not start on 16-byte boundaries.  Each piece makes its logits
+ * gradients take the vocabulary in pieces.  Each piece makes its logits
  * again, except that loss_grad with one piece (at most 2 million rows) keeps their
- * exponentials in that buffer, rounded to fp16's 11 bits, before it makes dz.
+ * exponentials in dz's buffer, rounded to fp16's 11 bits, before it makes dz.
+ * The workspace holds (rows rounded up to 256)
+ *   - a copy of the rows of x that count, and of weight where its rows do not
+ *     start on 16-byte boundaries;
+ *   - for gradients, a piece's dz: at most 512 MB, or the weight's size if that
+ *     is more (512 bytes a row at least);
+ *   - for the loss of more than 16 rows, 8 bytes for every row and 32 columns:
+ *     of all columns where exponentials are kept (an eighth of dz's buffer), else
+ *     of as many as take 256 MB (64 bytes a row at least);
+ *   - for dx, fp32 sums: rows x k (k rounded up to 256) of them, of few rows and
+ *     a small k several times that, up to 80 MB.
  *
  *   forward    loss and lse (either may be NULL)
  *   backward   dx and dweight (either may be NULL) from forward's lse

@@ -7,7 +7,9 @@
 //            that do not count cost nothing in the products, and what they
 //            hold (NaN, say) reaches no gradient
 //   stats    z = x W^T; maximum and sum of exponentials of every 32 logits
-//   join     log-sum-exp and loss
+//   join     log-sum-exp and loss; where the statistics of all logits would
+//            take more than 256 MB, the two run over one piece of the vocabulary
+//            after the other, and the rows' running statistics are carried on
 // and for the gradients, for one piece of the vocabulary after the other,
 //   dz       z again; dz = g (exp(z - lse) - [its token]), rounded to the
 //            operands' 16 bits into a buffer of the piece's size; where one
@@ -323,7 +325,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) stats_kernel(const __grid_con
             done();
             if (!part.last) return;
             const int row = part.row0 + (threadIdx.x & 31);
-            const int at = p.h.token[row] - part.col0;  // the token's column here
+            const int at = p.h.token[row] - p.first - part.col0;  // the token's column here
             Stager<__half> stager{staging + (threadIdx.x >> 5) * kStagerBytes, part.row0, 0, p.n};
 #pragma unroll
             for (int c = 0; c < kCols; c += 32) {
@@ -393,11 +395,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) stats_kernel(const __grid_con
 }
 
 // Log-sum-exp and loss of 8 counted rows per CTA, or of 4 where rows are few:
-// kRows lanes take neighbouring rows, the others slices in turn.
+// kRows lanes take neighbouring rows, the others slices in turn.  Of a piece
+// of the vocabulary: joined with those before it; the last one writes the loss.
 constexpr int kJoinThreads = 512;
 template <int kRows>
 __global__ void __launch_bounds__(kJoinThreads) stats_join_kernel(const float2* parts, int64_t pitch, int slices, HeadRows h,
-                                                                  float* loss, float* lse) {
+                                                                  float* loss, float* lse, float2* run, bool first, bool last) {
     constexpr int kTurns = kJoinThreads / kRows;
     __shared__ float2 sums[kTurns][kRows];
     follow_stream();
@@ -411,7 +414,9 @@ __global__ void __launch_bounds__(kJoinThreads) stats_join_kernel(const float2* 
         __syncthreads();
     }
     if (turn || i >= h.counted->rows) return;
-    write_loss(h, i, own, loss, lse);
+    if (!first) own = join_stats(run[i], own);
+    if (last) write_loss(h, i, own, loss, lse);
+    else run[i] = own;
 }
 
 // dz of the kept exponentials, in place: a CTA 32 rows of 256 columns.  The
@@ -640,12 +645,18 @@ int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 // The buffer for a piece's dz: half a gigabyte or as much as the weight has,
 // or what one column of tiles needs.
 constexpr int64_t kPieceBytes = 512ll << 20;
+// What the statistics take that are joined together (8 bytes for 32 logits:
+// 8192 rows of a vocabulary of 131072).
+constexpr int64_t kStatsBytes = 256ll << 20;
 
 struct HeadLayout {
-    int64_t counted, row, place, token, weight, g, lse, z_token, x, w, parts, dz, sums, bytes;
+    int64_t counted, row, place, token, weight, g, lse, z_token, x, w, parts, run, joined, dz, sums, bytes;
     int64_t pitch;                   // rows, rounded up to whole tiles
     int64_t x_stride, w_stride, sums_stride;
     int64_t piece, pieces;           // columns of the vocabulary
+    int64_t stats_piece;             // columns whose statistics are joined together
+    bool keep;                       // the loss and the gradients of one piece: exponentials are kept for dz
+    bool join;                       // few rows: their statistics are joined by the kernel that makes them
     int32_t most_parts;              // in which dx may be summed side by side
     bool big;                        // tiles on pairs of SMs
     HeadLayout(int64_t rows, int64_t vocab, int64_t k, bool copy_weight, bool forward, bool dx, bool dweight, int sms) {
@@ -661,6 +672,12 @@ struct HeadLayout {
         pieces = (vocab + most - 1) / most;
         piece = ((vocab + pieces - 1) / pieces + 255) / 256 * 256;
         pieces = (vocab + piece - 1) / piece;
+        // (32 rows of the pass over the kept exponentials are a row of its grid)
+        keep = forward && (dx || dweight) && pieces == 1 && rows <= 32 * 65000;
+        join = rows <= kJoinedRows;
+        const int64_t most_stats = join ? vocab : std::max<int64_t>(256, kStatsBytes / (8 * pitch) * 32 / 256 * 256);
+        const int64_t stats_pieces = (vocab + most_stats - 1) / most_stats;
+        stats_piece = ((vocab + stats_pieces - 1) / stats_pieces + 255) / 256 * 256;
         // room for twice as many parts as fill a wave, each of 16 stages or more
         const int64_t edge = big ? 256 : 128, workers = big ? pairs : sms, kts = (std::min(piece, vocab) + kBK - 1) / kBK;
         const int64_t tiles = (rows + edge - 1) / edge * ((k + edge - 1) / edge);
@@ -680,7 +697,10 @@ struct HeadLayout {
         z_token = take(pitch * 4);
         x = take(pitch * x_stride * 2);
         w = take(copy_weight ? vocab * w_stride * 2 : 0);
-        parts = take(forward ? (pitch * slices(vocab) + (int64_t)kJoinedRows * sms) * 8 : 0);
+        // kept exponentials need the statistics of all their logits
+        parts = take(!forward || (join && !keep) ? 0 : pitch * slices(keep ? vocab : std::min(stats_piece, vocab)) * 8);
+        run = take(forward && stats_piece < vocab ? pitch * 8 : 0);
+        joined = take(forward && join ? (int64_t)kJoinedRows * sms * 8 : 0);
         dz = take(dx || dweight ? pitch * piece * 2 : 0);
         sums = take(dx ? most_parts * pitch * sums_stride * 4 : 0);
         bytes = at;
@@ -743,62 +763,68 @@ struct Head {
         if (const int e = make_map(&p.a, a.dtype, ws + at.x, at.x_stride, at.pitch, a.k, kBM)) return e;
         return make_map(&p.b, a.dtype, b, w_stride, n, a.k, width / CG);
     }
-    int forward(bool keep) const {
+    int forward() const {
+        for (int64_t first = 0; first < a.vocab; first += at.stats_piece)
+            if (const int e = statistics(first, std::min<int64_t>(at.stats_piece, a.vocab - first))) return e;
+        if (!at.keep) return cudaSuccess;
+        const float2* parts = reinterpret_cast<const float2*>(ws + at.parts);
+        int64_t pitch = at.pitch, stride = at.piece;
+        HeadRows rows = h;
+        T* dz = reinterpret_cast<T*>(ws + at.dz);
+        int32_t n = a.vocab;
+        void* args[] = {&dz, &stride, &parts, &pitch, &rows, &n};
+        const unsigned padded = (unsigned)std::max<int64_t>(64, (a.rows + 63) / 64 * 64);
+        return launch_after((const void*)keep_kernel<T>, dim3((a.vocab + kKeepCols - 1) / kKeepCols, padded / kKeepRows), 256,
+                            args, stream);
+    }
+    // Statistics of columns [first, first + n) of the vocabulary, joined with those before them.
+    int statistics(int64_t first, int64_t n) const {
         LogitArgs p{};
-        p.parts = reinterpret_cast<float2*>(ws + at.parts);
-        p.keep = keep;
-        if (keep)
-            if (const int e = make_map(&p.out, a.dtype, ws + at.dz, at.piece, at.pitch, a.vocab, 32, 32)) return e;
+        p.parts = reinterpret_cast<float2*>(ws + at.parts) + (at.keep ? HeadLayout::slices(first) * at.pitch : 0);
+        p.keep = at.keep;
+        if (at.keep)
+            if (const int e = make_map(&p.out, a.dtype, ws + at.dz + first * 2, at.piece, at.pitch, n, 32, 32)) return e;
         void* args[] = {&p};
         int e;
         if (a.rows <= kBM) {
             // One row of tiles: reading the weight is what takes time, and tiles of
             // one width, at most 256, fill whole waves of SMs (32000 tokens: 143
             // tiles of 224 columns, not 250 of 128 in a wave and two thirds).
-            const int64_t waves = (((int64_t)a.vocab + 255) / 256 + sms - 1) / sms;
-            p.columns = (int32_t)(((a.vocab + waves * sms - 1) / (waves * sms) + 31) / 32 * 32);
-            p.join = a.rows <= kJoinedRows;
-            p.joined = p.parts + HeadLayout::slices(a.vocab) * at.pitch;
+            const int64_t waves = ((n + 255) / 256 + sms - 1) / sms;
+            p.columns = (int32_t)(((n + waves * sms - 1) / (waves * sms) + 31) / 32 * 32);
+            p.join = at.join;
+            p.joined = reinterpret_cast<float2*>(ws + at.joined);
             p.loss = a.loss;
             p.lse = a.lse;
-            e = Head<1, 256, T>{a, at, h, ws, w, w_stride, sms, stream}.logits(p, 0, a.vocab, p.columns);
+            e = Head<1, 256, T>{a, at, h, ws, w, w_stride, sms, stream}.logits(p, first, n, p.columns);
             if (!e)
                 e = launch_cluster((const void*)stats_kernel<1, 256, T>, args, std::min<int64_t>(p.tiles_n, sms),
                                    kTileThreads, TileShape<1, 256>::kSmem, 1, stream);
         } else {
-            e = logits(p, 0, a.vocab, BN);
+            e = logits(p, first, n, BN);
             // (half tiles make at most twice as many units)
             if (!e) e = tiles((const void*)stats_kernel<CG, BN, T>, rows_of_tiles(a.rows) * p.tiles_n * 2, args);
         }
-        if (e) return e;
-        const float2* parts = p.parts;
-        int64_t pitch = at.pitch, stride = at.piece;
-        HeadRows rows = h;
-        if (!p.join) e = join(parts);
-        if (e || !keep) return e;
-        T* dz = reinterpret_cast<T*>(ws + at.dz);
-        int32_t n = a.vocab;
-        void* keep_args[] = {&dz, &stride, &parts, &pitch, &rows, &n};
-        const unsigned padded = (unsigned)std::max<int64_t>(64, (a.rows + 63) / 64 * 64);
-        return launch_after((const void*)keep_kernel<T>, dim3((a.vocab + kKeepCols - 1) / kKeepCols, padded / kKeepRows), 256,
-                            keep_args, stream);
+        return e || p.join ? e : join(p.parts, first, n);
     }
-    int join(const float2* parts) const {
+    int join(const float2* parts, int64_t first_column, int64_t n) const {
         int64_t pitch = at.pitch;
-        int slices = (int)HeadLayout::slices(a.vocab);
+        int slices = (int)HeadLayout::slices(n);
         HeadRows rows = h;
         float *loss = a.loss, *lse = a.lse;
-        void* join_args[] = {&parts, &pitch, &slices, &rows, &loss, &lse};
+        float2* run = reinterpret_cast<float2*>(ws + at.run);
+        bool first = first_column == 0, last = first_column + n == a.vocab;
+        void* join_args[] = {&parts, &pitch, &slices, &rows, &loss, &lse, &run, &first, &last};
         // (few rows: 4 per CTA, a sector of each slice)
         const bool few = a.rows <= 1024;
         return launch_after(few ? (const void*)stats_join_kernel<4> : (const void*)stats_join_kernel<8>,
                             dim3((unsigned)((a.rows + (few ? 3 : 7)) / (few ? 4 : 8))), kJoinThreads, join_args, stream);
     }
-    int gradients(bool kept) const {
+    int gradients() const {
         for (int64_t first = 0; first < a.vocab; first += at.piece) {
             const int64_t n = std::min<int64_t>(at.piece, a.vocab - first);
             int e = cudaSuccess;
-            if (!kept) {
+            if (!at.keep) {
                 LogitArgs p{};
                 e = make_map(&p.out, a.dtype, ws + at.dz, at.piece, at.pitch, n, 32, 32);
                 void* args[] = {&p};
@@ -916,11 +942,8 @@ int launch_head(const HeadArgs& a, bool forward, void* workspace, int sm_count, 
             if (const int e = launch_after((const void*)gather_kernel<T>, dim3((unsigned)grid), 256, args, stream)) return e;
         }
         auto products = [&](const auto& head) {
-            const bool gradients = a.dx || a.dweight;
-            // (32 rows of the pass over the kept exponentials are a row of its grid)
-            const bool keep = forward && gradients && at.pieces == 1 && a.rows <= 32 * 65000;
-            int e = forward ? head.forward(keep) : cudaSuccess;
-            if (!e && gradients) e = head.gradients(keep);
+            int e = forward ? head.forward() : cudaSuccess;
+            if (!e && (a.dx || a.dweight)) e = head.gradients();
             return e;
         };
         if (at.big) return products(Head<2, 256, T>{a, at, h, ws, w, w_stride, sm_count, stream});

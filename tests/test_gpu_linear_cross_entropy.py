@@ -400,3 +400,61 @@ def test_refusals(ops):
             (lambda: ops.linear_cross_entropy_forward(x.cpu(), w, t), ValueError, "CUDA")):
         with pytest.raises(error, match=word):
             call()
+
+
+def part_of(c, at):
+    """The rows `at` of a case, as a case of their own."""
+    part = Case(1, 1, 1, c.dtype)
+    part.x, part.w, part.t, part.weight = c.x[at], c.w, c.t[at], None if c.weight is None else c.weight[at]
+    part.rows, part.vocab, part.k = len(at), c.vocab, c.k
+    return part
+
+
+@pytest.mark.parametrize("rows,vocab,k", [(65536, 131072, 1024), (65536, 262144, 64), (262144, 131072, 4096), (100, 1 << 25, 8)])
+def test_the_workspace_of_the_loss_is_bounded(ops, rows, vocab, k):
+    """The rows that count, 36 bytes a row, and 256 MB: not a share of the logits."""
+    ops._ops_abi.load()
+    pitch = (rows + 255) // 256 * 256
+    need = ops._head_bytes(0, False, rows, vocab, k, 1, 1, 0, 0)
+    assert need <= pitch * (2 * k + 36) + (256 << 20) + (1 << 20)
+    # and with gradients: a piece's dz, an eighth of it, dx in fp32
+    both = ops._head_bytes(0, False, rows, vocab, k, 1, 1, 1, 1)
+    assert both <= need + max(512 << 20, 512 * pitch, vocab * k * 2) * 9 // 8 + pitch * (k + 255) // 256 * 256 * 4 + (80 << 20)
+
+
+@pytest.mark.parametrize("rows,vocab,k,some", [(65536, 50021, 64, 300), (1000, 1_100_003, 8, 60), (100, 4_300_001, 8, 20)])
+def test_statistics_in_pieces_of_the_vocabulary(ops, rows, vocab, k, some):
+    """More than 2^30 logits: their statistics are joined piece by piece."""
+    torch.manual_seed(12)
+    c = Case(rows, vocab, k, torch.bfloat16)
+    loss, lse = ops.linear_cross_entropy_forward(c.x, c.w, c.t, row_weight=c.weight)
+    at = torch.randperm(rows, device="cuda")[:some]
+    part = part_of(c, at)
+    ref = part.reference()
+    assert_close(loss[at], *ref["loss"], "loss")
+    assert_close(lse[at], *ref["lse"], "lse")
+    again = ops.linear_cross_entropy_forward(c.x, c.w, c.t, row_weight=c.weight)
+    assert torch.equal(loss, again[0]) and torch.equal(lse, again[1])
+    loss2, dx, _ = ops.linear_cross_entropy_loss_grad(c.x, c.w, c.t, row_weight=c.weight, weight_grad=False)
+    assert torch.equal(loss, loss2)
+    assert_close(dx[at], *ref["dx"], "dx")
+
+
+def test_statistics_in_pieces_with_kept_exponentials(ops):
+    """As many rows as columns of x are one piece of dz, whose exponentials are kept, but several of statistics."""
+    torch.manual_seed(13)
+    rows, vocab, k = 16384, 65793, 16384
+    c = Case(rows, vocab, k, torch.bfloat16, ignored=0.1)
+    kw = dict(row_weight=c.weight)
+    loss, lse = ops.linear_cross_entropy_forward(c.x, c.w, c.t, **kw)
+    loss2, dx, dw = ops.linear_cross_entropy_loss_grad(c.x, c.w, c.t, **kw)
+    assert torch.equal(loss, loss2)
+    at = torch.randperm(rows, device="cuda")[:10]
+    ref = part_of(c, at).reference(kept=True)
+    assert_close(loss[at], *ref["loss"], "loss")
+    assert_close(dx[at], *ref["dx"], "dx")
+    # the gradients from lse, whose dz is made of the logits: both round dz and the result by 2^-8 at most, at random
+    dx1, dw1 = ops.linear_cross_entropy_backward(torch.ones(rows, device="cuda"), c.x, c.w, c.t, lse, **kw)
+    for a, b in ((dx, dx1), (dw, dw1)):
+        for part in (slice(0, 100), slice(len(a) // 2, len(a) // 2 + 100), slice(len(a) - 100, len(a))):
+            assert (a[part].double() - b[part].double()).norm() <= 2.0 ** -6 * b[part].double().norm()
