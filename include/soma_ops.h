@@ -223,7 +223,9 @@ soma_status_t soma_embedding_backward(int32_t device, const void *dy, int64_t dy
  *   - a copy of the rows of x that count, and of weight where its rows do not
  *     start on 16-byte boundaries;
  *   - for gradients, a piece's dz: at most 512 MB, or the weight's size if that
- *     is more (512 bytes a row at least);
+ *     is more (vocab rounded up to 256, and k too for as many rows or fewer; 512
+ *     bytes a row at least).  As many rows as x has columns, if those are 256 or
+ *     more, are one piece;
  *   - for the loss of more than 16 rows, 8 bytes for every row and 32 columns:
  *     of all columns where exponentials are kept (an eighth of dz's buffer), else
  *     of as many as take 256 MB (64 bytes a row at least);

@@ -666,8 +666,9 @@ struct HeadLayout {
         const int64_t pairs = std::max(1, sms / 2);
         const int64_t t256 = (rows + 255) / 256 * ((vocab + 255) / 256), t128 = (rows + 127) / 128 * ((vocab + 127) / 128);
         big = rows > 128 && (t256 + pairs - 1) / pairs < (t128 + sms - 1) / sms;
-        // (whole tiles: as many rows as columns of x are one piece for any vocabulary)
-        const int64_t buffer = std::max(kPieceBytes, (vocab + 255) / 256 * 256 * k * 2);
+        // (whole tiles on both sides: as many rows as columns of x, 256 of those or more, are one piece for any vocabulary)
+        const int64_t width = k >= 256 && rows <= k ? pitch : k;
+        const int64_t buffer = std::max(kPieceBytes, (vocab + 255) / 256 * 256 * width * 2);
         const int64_t most = std::max<int64_t>(256, buffer / (2 * pitch) / 256 * 256);
         pieces = (vocab + most - 1) / most;
         piece = ((vocab + pieces - 1) / pieces + 255) / 256 * 256;

@@ -458,3 +458,16 @@ def test_statistics_in_pieces_with_kept_exponentials(ops):
     for a, b in ((dx, dx1), (dw, dw1)):
         for part in (slice(0, 100), slice(len(a) // 2, len(a) // 2 + 100), slice(len(a) - 100, len(a))):
             assert (a[part].double() - b[part].double()).norm() <= 2.0 ** -6 * b[part].double().norm()
+
+
+@pytest.mark.parametrize("n,vocab", [(1003, 300000), (4000, 131072), (4096, 131072), (4090, 131073), (257, 1 << 20)])
+def test_as_many_rows_as_columns_are_one_piece(ops, n, vocab):
+    """The workspace has room for dz of the whole vocabulary: the logits are made once."""
+    ops._ops_abi.load()
+    need, without = (ops._head_bytes(0, False, n, vocab, n, 1, 1, 0, wanted) for wanted in (1, 0))
+    pitch = (n + 255) // 256 * 256
+    assert need - without >= pitch * vocab * 2
+    # not for one tile of rows more
+    more, without = (ops._head_bytes(0, False, pitch + 1, vocab, n, 1, 1, 0, wanted) for wanted in (1, 0))
+    if pitch * vocab * 2 >= 512 << 20:
+        assert more - without < (pitch + 256) * vocab * 2
