@@ -228,7 +228,7 @@ soma_status_t soma_embedding_backward(int32_t device, const void *dy, int64_t dy
  *     more, are one piece;
  *   - for the loss of more than 16 rows, 8 bytes for every row and 32 columns:
  *     of all columns where exponentials are kept (an eighth of dz's buffer), else
- *     of as many as take 256 MB (64 bytes a row at least);
+ *     of as many as take 512 MB (64 bytes a row at least);
  *   - for dx, fp32 sums: rows x k (k rounded up to 256) of them, of few rows and
  *     a small k several times that, up to 80 MB.
  *

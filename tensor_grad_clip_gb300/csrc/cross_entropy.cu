@@ -8,7 +8,7 @@
 //            hold (NaN, say) reaches no gradient
 //   stats    z = x W^T; maximum and sum of exponentials of every 32 logits
 //   join     log-sum-exp and loss; where the statistics of all logits would
-//            take more than 256 MB, the two run over one piece of the vocabulary
+//            take more than 512 MB, the two run over one piece of the vocabulary
 //            after the other, and the rows' running statistics are carried on
 // and for the gradients, for one piece of the vocabulary after the other,
 //   dz       z again; dz = g (exp(z - lse) - [its token]), rounded to the
@@ -646,8 +646,10 @@ int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 // or what one column of tiles needs.
 constexpr int64_t kPieceBytes = 512ll << 20;
 // What the statistics take that are joined together (8 bytes for 32 logits:
-// 8192 rows of a vocabulary of 131072).
-constexpr int64_t kStatsBytes = 256ll << 20;
+// 16384 rows of a vocabulary of 131072).  A piece more costs about 40 us, a join
+// and a last wave: 65536 rows, 131072 x 512 7.23 ms with 256 MB, 7.02 with 512,
+// 6.95 with 1024, 6.91 in one piece of 2.1 GB; nothing at k = 1024 (11.6 to 11.8).
+constexpr int64_t kStatsBytes = 512ll << 20;
 
 struct HeadLayout {
     int64_t counted, row, place, token, weight, g, lse, z_token, x, w, parts, run, joined, dz, sums, bytes;
