@@ -214,8 +214,13 @@ soma_status_t soma_embedding_backward(int32_t device, const void *dy, int64_t dy
  * 1 <= k, vocab <= 2^30, rows <= 2^30.
  *
  * Logits, exponentials and sums are fp32.  dz is rounded once to the operands'
- * 16 bits before the two products, whose tensor-core operands are 16-bit; a
- * factor, found from the largest |g|, keeps it in fp16's range.  The
+ * 16 bits before the two products, whose tensor-core operands are 16-bit; one
+ * factor for all rows brings the largest |g| to 2^14, near fp16's top.  With
+ * fp16 operands dz has then steps of 2^-38 of the largest |g|, whatever a row's
+ * own is: rows of up to 2^-10 of it lose nothing that matters (steps of 2^-28 of
+ * their own g), a row of 2^-20 of it every probability below 2^-19, so that its
+ * dx is known to about 2^-19 of g sum_v |weight_v| only.  bf16 has no such limit.
+ * The
  * gradients take the vocabulary in pieces.  Each piece makes its logits
  * again, except that loss_grad with one piece (at most 2 million rows) keeps their
  * exponentials in dz's buffer, rounded to fp16's 11 bits, before it makes dz.

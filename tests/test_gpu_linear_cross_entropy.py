@@ -175,6 +175,24 @@ def test_gradients_far_from_1(ops, scale):
         Case(200, 700, 96, torch.float16, scale=scale if scale > 1 else 1e-3).check(ops)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("powers", [10, 24])
+def test_rows_of_very_different_weight(ops, dtype, powers):
+    """Each row's own dx, beside rows whose weight is up to 2^powers times as large: bf16 loses nothing, fp16 what lies below
+    2^-38 of the largest (half such a step for every dz, in the reference's bound)."""
+    torch.manual_seed(14)
+    for rows, vocab, k in ((200, 700, 96), (1100, 5000, 64)):
+        c = Case(rows, vocab, k, dtype)
+        c.weight *= 1024 * torch.exp2(-powers * torch.rand(rows, device="cuda"))
+        c.g = torch.sign(c.g)
+        c.check(ops)
+        ref, bound = c.reference()["dx"]
+        if powers == 10:  # no row's bound is set by another's weight: it is below 2^-6 of |g| sum_v p_v |w_v| + |w_t|
+            p = torch.softmax(c.x.double() @ c.w.double().t(), 1)
+            own = c.weight.double()[:, None] * (p @ c.w.double().abs() + c.w.double().abs()[c.t.clamp(0, vocab - 1)])
+            assert (bound <= 2.0 ** -6 * own + 2.0 ** -24)[c.counts].all()
+
+
 def test_rows_that_do_not_count_reach_nothing(ops):
     torch.manual_seed(4)
     for rows, vocab, k in ((300, 500, 72), (1024, 5000, 64)):
