@@ -475,10 +475,10 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const __grid_constant_
 #pragma unroll
         for (int q = 0; q < kSumDeep; ++q) {
             const int i = i0 + q;
-            if (i >= n) break;
+            if (i >= n || keys[1 + i] >= (uint32_t)a.vocab) break;  // (of a token outside the vocabulary nothing is read)
             columns.load(dy + (int64_t)order[i] * a.dy_stride, raw[q]);
             // what a token's sum is added to, where it ends (read now: one at a time they cost a latency each)
-            if (kAdd && keys[1 + i] < (uint32_t)a.vocab && keys[1 + i] != keys[2 + i]) columns.load(out(keys[1 + i]), before[kAdd ? q : 0]);
+            if (kAdd && keys[1 + i] != keys[2 + i]) columns.load(out(keys[1 + i]), before[kAdd ? q : 0]);
         }
 #pragma unroll
         for (int q = 0; q < kSumDeep; ++q) {
