@@ -448,9 +448,9 @@ __global__ void __launch_bounds__(256) keep_kernel(T* dz, int64_t stride, const 
         const float f = factor[lane / 4][r];
         float x[8];
         widen16(v[k], x, __half{});
+        const int token = h.token[row], d = token - c;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= f;
-        const int d = h.token[row] - c;
+        for (int i = 0; i < 8; ++i) x[i] = token < 0 ? 0.f : x[i] * f;  // (the padding: NaN where weight is not finite)
         if (d >= 0 && d < 8) {
             const float own =
                 h.g[row] * h.counted->scale * (exp2_fast((h.z_token[row] - h.lse[row]) * kLog2e) - 1.f);
@@ -471,6 +471,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) dz_kernel(const __grid_consta
             const int row0 = part.row0, col0 = part.col0, cols = part.cols, row = row0 + (threadIdx.x & 31);
             const int at = p.h.token[row] - p.first - col0;
             const float lse = p.h.lse[row], g = p.h.g[row] * p.h.counted->scale;
+            // (the padding's g is 0, but where weight is not finite its logits are not either)
+            const bool padding = row0 + 32 > p.h.counted->rows;
             Stager<T> stager{staging + (threadIdx.x >> 5) * kStagerBytes, row0, 0, p.n};
             for (int c = 0; c < cols && col0 + c < p.n; c += 32) {
                 float z[32];
@@ -479,6 +481,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) dz_kernel(const __grid_consta
                 const bool here = __any_sync(0xffffffffu, d >= 0 && d < 32);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) z[i] = g * exp2_fast((z[i] - lse) * kLog2e);
+                if (padding && p.h.token[row] < 0) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) z[i] = 0.f;
+                }
                 if (here) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i)

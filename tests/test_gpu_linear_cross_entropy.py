@@ -221,6 +221,19 @@ def test_no_row_counts(ops):
         assert not loss.any() and not dx.any() and not dw.any()
 
 
+@pytest.mark.parametrize("rows", [1, 40, 200, 1100])
+def test_no_row_counts_and_a_weight_is_not_finite(ops, rows):
+    """Every gradient is 0, as where the weight is finite, not 0 times infinity of the padding's logits."""
+    x, w = matrix(rows, 64, torch.bfloat16), matrix(3000, 64, torch.bfloat16)
+    w[7, 3], w[2999, 60] = math.inf, math.nan
+    t = torch.full((rows,), -100, device="cuda")
+    loss, dx, dw = ops.linear_cross_entropy_loss_grad(x, w, t)
+    assert not loss.any() and not dx.any() and not dw.any()
+    one = torch.ones(rows, device="cuda")
+    dx, dw = ops.linear_cross_entropy_backward(one, x, w, t, 0 * one)
+    assert not dx.any() and not dw.any()
+
+
 def test_infinities_stay_in_their_row(ops):
     torch.manual_seed(5)
     c = Case(130, 200, 64, torch.bfloat16, ignored=0, weights=False)
