@@ -20,7 +20,8 @@
 // 20 random bits and dropping as many rounds up or down with the
 // probabilities that make the mean exact.  Rounding to nearest would not do:
 // with beta2 = 0.999 one step moves sqrt(v) by 0.05 %, where e4m3's steps are
-// 6 to 12 %, and every second moment would stay where it is.
+// 6 to 12 %, and a second moment that moves against its block's largest (all
+// that move with it are carried by the scale) would stay where it is.
 #include <cuda_fp8.h>
 #include <math.h>
 

@@ -464,3 +464,38 @@ def test_an_eps_that_is_subnormal(eps):
         assert torch.isfinite(e.p).all()
         decayed = p[e.quiet].double() * (1 - hp["lr"] * hp["weight_decay"])
         assert ((e.p[e.quiet].double() - decayed).abs() <= 2 * U32 * decayed.abs()).all()
+
+
+def test_rounding_by_chance_follows_what_moves_against_its_block():
+    """One element of each block keeps its moments, and the block its scales, while the others' decay: 0.05 % a step of
+    sqrt(v), which rounded to nearest would stay where it is."""
+    torch.manual_seed(15)
+    n, largest = 1 << 18, 2.0
+    e = Entry(n)
+    first = torch.zeros(n, dtype=torch.bool, device="cuda")
+    first[::BLOCK] = True
+    e.g.copy_(torch.where(first, largest, 0.0))  # m and v of constant gradients: the gradient, and its square
+    start = torch.where(first, largest, torch.rand(n, device="cuda") * 0.75 + 0.25)
+    for codes, scales, second in ((e.m, "ms", False), (e.v, "vs", True)):
+        c, s = to_8bit(start, second_moment=second)
+        codes.copy_(c)
+        setattr(e, scales, s)
+    m0, r0 = e.moments()
+    # (the test says something: to nearest, one step changes no second moment's code)
+    nearest, _ = to_8bit(torch.where(first, r0, r0 * math.sqrt(0.999)).float(), second_moment=True)
+    assert torch.equal(nearest.view(torch.uint8), e.v.view(torch.uint8))
+    opt, tl = new_opt(), make_list([e])
+    # a step of e4m3 is at most an eighth of the value.  A rounding that moves a share f of a step has the variance
+    # f (1 - f) steps^2: f is at most 0.0005 x 16 for sqrt(v), whose steps are then 1 / 16 of it (f / 256 = 0.0005 / 16, and
+    # 0.0005 / 8 at the other end), and at most 1 / 4 is f (1 - f) for m.  6 deviations of the mean of n elements; 2^-17 of a
+    # step is what 16 random bits leave of the mean.
+    for steps, left, variance, moments in ((10, 0.9 ** 10, 10 * 0.25 / 64, 0), (400, 0.999 ** 200, 400 * 0.0005 / 8, 1)):
+        while opt.get_group_step(0) < steps:
+            opt.step(tl, 1.0, 1e30)
+        now, before = e.moments()[moments][~first], (m0, r0)[moments][~first]
+        ratio = (now / before).mean().item()
+        bound = 6 * left * math.sqrt(variance / now.numel()) * 1.1 + left * steps * (2.0 ** -17 / 8 + 8 * U32)
+        assert abs(ratio - left) <= bound, (moments, ratio, left, bound)
+        assert bound < (1 - left) / 50
+        kept = e.moments()[moments][first]
+        assert ((kept - largest).abs() <= largest * steps * 8 * U32).all()
