@@ -24,7 +24,8 @@ linear_cross_entropy.
 
 Tensors are CUDA tensors with unit stride in the last dimension; all leading
 dimensions are rows and must be evenly spaced (any tensor that can be viewed
-as [rows, last], a slice tokens[:, 1:] of a batch of texts among them).  Work is enqueued on the current stream, or on `stream` (a
+as [rows, last]).  Tokens may be a slice tokens[:, 1:] or a column tokens[:, -1]
+of a batch of texts.  Work is enqueued on the current stream, or on `stream` (a
 torch stream or a raw cudaStream_t), which then also owns the outputs; the
 inputs are kept alive for it.  Nothing waits for the GPU, and there is no
 fallback: a refused call raises SomaError, ValueError or TypeError.
@@ -433,6 +434,8 @@ def _tokens(t, name, other):
     if t.dim() == 1 and t.is_cuda and t.is_contiguous():  # (host time: most calls)
         n = t.shape[0]
         return t.data_ptr(), n, 1, n, code
+    if t.dim() == 1 and t.is_cuda and t.stride(0) > 0:  # one token of each text
+        return t.data_ptr(), t.stride(0), t.shape[0], 1, code
     if t.dim() == 0:
         t = t.unsqueeze(0)
     m = _matrix(t, name)

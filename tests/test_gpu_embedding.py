@@ -164,6 +164,23 @@ def test_a_slice_of_a_batch_of_texts(ops):
     assert one.shape == (24,) and torch.equal(one, ops.embedding_forward(texts[3, 4:5], table)[0])
 
 
+@pytest.mark.parametrize("kind", [torch.int32, torch.int64])
+def test_one_token_of_each_text(ops, kind):
+    """A column of a batch of texts, as a generation loop looks it up, and every third token of one text."""
+    table = torch.randn(100, 24, device="cuda").bfloat16()
+    texts = torch.randint(-2, 103, (70, 33), device="cuda", dtype=kind)
+    for index in (texts[:, -1], texts[:, 0], texts[5, ::3], texts[:1, 4], texts[:0, 1]):
+        y, whole = ops.embedding_forward(index, table), index.contiguous()
+        assert y.shape == (*index.shape, 24) and torch.equal(y, ops.embedding_forward(whole, table))
+        dy = torch.randn(len(index), 24, device="cuda").bfloat16()
+        assert torch.equal(ops.embedding_backward(dy, index, 100), ops.embedding_backward(dy, whole, 100))
+    weight = table.clone().requires_grad_()
+    ops.embedding(texts[:, -1], weight).sum().backward()
+    assert_gradient(weight.grad, torch.ones(70, 24, device="cuda"), texts[:, -1], 100, 1.0)
+    with pytest.raises(ValueError, match="unit stride"):
+        ops.embedding_forward(texts[:1, 0].expand(5), table)
+
+
 def test_autograd_and_differences(ops):
     table = torch.randn(50, 24, device="cuda", requires_grad=True)
     index = torch.randint(-1, 50, (4, 30), device="cuda")

@@ -282,6 +282,20 @@ def test_shapes_and_slices(ops):
     assert empty.shape == (0, 20) and not dw.any()
 
 
+@pytest.mark.parametrize("kind", [torch.int32, torch.int64])
+def test_one_target_of_each_text(ops, kind):
+    torch.manual_seed(16)
+    hidden, w = matrix(6 * 20, 64, torch.bfloat16).view(6, 20, 64), matrix(90, 64, torch.bfloat16)
+    texts = torch.randint(-1, 90, (6, 25), device="cuda", dtype=kind)
+    x, t = hidden[:, -1], texts[:, 20]
+    assert not t.is_contiguous()
+    got, want = (ops.linear_cross_entropy_loss_grad(x, w, v) for v in (t, t.contiguous()))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    lse = ops.linear_cross_entropy_forward(x, w, t)[1]
+    got, want = (ops.linear_cross_entropy_backward(torch.ones(6, device="cuda"), x, w, v, lse) for v in (t, t.contiguous()))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_autograd_and_differences(ops):
     torch.manual_seed(7)
     c = Case(40, 60, 24, torch.float16, ignored=0.3)
