@@ -11,8 +11,8 @@
  * Outputs must not overlap inputs or each other except where a call says so.
  *
  * Types are SOMA_DTYPE_F32, _BF16 or _F16.  Every sum, statistic and
- * exponential is held in fp32; an output is rounded to its type once, to
- * nearest even.  Results do not depend on the schedule: the same call on the
+ * exponential is held in fp32, except where a call says so; an output is rounded
+ * to its type once, to nearest even.  Results do not depend on the schedule: the same call on the
  * same device gives the same bits.
  *
  * Memory belongs to the caller.  A call that needs scratch memory says how
@@ -200,7 +200,8 @@ soma_status_t soma_embedding_backward(int32_t device, const void *dy, int64_t dy
                                       int32_t index_type, double scale, void *stream);
 
 /* ---- cross entropy of a linear layer over a vocabulary -------------------------
- * The last linear layer and its loss in one, without the logits in memory:
+ * The last linear layer and its loss in one, whose logits are not stored (16 bits
+ * for each of a piece of them are, for gradients):
  *   z_rv   = sum_j x_rj * weight_vj,   lse_r = log sum_v exp(z_rv)
  *   loss_r = row_weight_r * (lse_r - z_{r, t_r})
  * and for grad_loss_r = dL/dloss_r, with g_r = row_weight_r * grad_loss_r,
@@ -210,7 +211,8 @@ soma_status_t soma_embedding_backward(int32_t device, const void *dy, int64_t dy
  * t_r = target[r / length][r % length] as for the embedding, rows = batch *
  * length; row_weight[rows] fp32 (NULL = 1).  A row counts if its weight is not
  * 0 and its target lies in [0, vocab); any other row has loss, lse and gradient
- * 0, whatever its x and grad_loss hold (rows of padding, a target of -100).
+ * 0, whatever its x and grad_loss hold (rows of padding, a target of -100), and
+ * where no row counts dweight is 0 whatever weight holds.
  * 1 <= k, vocab <= 2^30, rows <= 2^30.
  *
  * Logits, exponentials and sums are fp32.  dz is rounded once to the operands'
@@ -220,10 +222,10 @@ soma_status_t soma_embedding_backward(int32_t device, const void *dy, int64_t dy
  * own is: rows of up to 2^-10 of it lose nothing that matters (steps of 2^-28 of
  * their own g), a row of 2^-20 of it every probability below 2^-19, so that its
  * dx is known to about 2^-19 of g sum_v |weight_v| only.  bf16 has no such limit.
- * The
- * gradients take the vocabulary in pieces.  Each piece makes its logits
+ * The gradients take the vocabulary in pieces.  Each piece makes its logits
  * again, except that loss_grad with one piece (at most 2 million rows) keeps their
- * exponentials in dz's buffer, rounded to fp16's 11 bits, before it makes dz.
+ * exponentials in dz's buffer, rounded to fp16's 11 bits, before it makes dz; its
+ * gradients then differ from backward's by that rounding.
  * The workspace holds (rows rounded up to 256)
  *   - a copy of the rows of x that count, and of weight where its rows do not
  *     start on 16-byte boundaries;

@@ -23,10 +23,13 @@
 //
 // Bound by the tensor cores, for few rows by reading the weight.  Measured
 // (GB300, cuBLAS bf16 1916 TFLOP/s in a burst, 1723 in a loop; 85 % of the rows
-// count): loss of 8192 rows, 32000 x 4096, 1.13 ms, 1612 TFLOP/s; loss and
-// gradients of 4096 rows, 131072 x 4096, 7.3 ms, 1536 TFLOP/s counted as three
-// products (9.4 ms with the logits made twice); of 2500 rows, 32000 x 1024
-// fp16, 369 us; loss of 16 rows, 32000 x 1024, 22.4 us, 2.9 TB/s.
+// count; calls in a row, and graph replays after the slash): loss of 8192 rows,
+// 32000 x 4096, 1.13 to 1.22 / 1.07 to 1.13 ms, 1500 to 1700 TFLOP/s; loss and
+// gradients of 4096 rows, 131072 x 4096, 7.2 to 7.5 / 7.2 ms, 1500 to 1560
+// TFLOP/s counted as three products; of 2500 rows, 32000 x 1024 fp16, 370 to 382
+// / 360 us; loss of 16 rows, 32000 x 1024, 25 to 28 / 22 us, 3 TB/s.  Where
+// the rows are two pieces, the logits are made twice: loss and gradients of 8192
+// rows (all count), 131072 x 4096, 22.0 ms, 1600 TFLOP/s counted as four products.
 #include <math.h>
 
 #include <algorithm>
@@ -301,8 +304,10 @@ __device__ __forceinline__ void write_loss(const HeadRows& h, int i, float2 sum,
 // 1.7e-7 for 7 %, of 2048 by 7.8e-7.
 constexpr int kLogitChunk = 1024 / kBK;
 
-constexpr int kJoinedRows = 16;  // "few rows": about one for each warp of the last CTA (22.5 us for 16 rows, 26 with a
-                                 // kernel of its own)
+// "Few rows": about one for each warp of the last CTA.  16 rows, 32000 x 1024
+// 22.0 us (22.1 with a kernel of its own), 131072 x 4096 175 us (189); 32 rows,
+// whose warps take two each, 22.7 and 176 us (22.0 and 188).
+constexpr int kJoinedRows = 16;
 
 template <int CG, int BN, typename T>
 __global__ void __launch_bounds__(kTileThreads, 1) stats_kernel(const __grid_constant__ LogitArgs p) {

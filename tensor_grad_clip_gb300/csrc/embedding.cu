@@ -13,11 +13,13 @@
 // CTAs zero the table, the rows with tokens too: that costs less than knowing
 // which they are before the sort is done.
 //
-// Measured (GB300, 6786 GB/s copy): 16384 tokens of 4096 bf16 looked up in 34.2
-// us; their gradient in a table of 32000 rows 72.5 us, of which zeroing beside
-// the sort takes 38 (as long as a memset) and the sums 27 (5.5 TB/s); 5003
-// tokens of 1003 fp32 added to a gradient 21.1 us, three dependent launches;
-// 65536 tokens are sorted in 35 us.
+// Measured (GB300, 6786 GB/s copy; graph replays, a call takes 1 to 3 us more):
+// 16384 tokens of 4096 bf16 looked up in 34.3 us; their gradient in a table of
+// 32000 rows 72.2 us, of which zeroing beside the sort takes 38 (as long as a
+// memset) and the sums 28 (5.5 TB/s), or 81 where each gradient goes to other
+// memory than the one before (of that L2 still holds a part); 5003 tokens of
+// 1003 fp32 added to a gradient 21.0 us, three dependent launches; 65536 tokens
+// are sorted in 34 us.
 #include <math.h>
 
 #include <algorithm>
